@@ -343,9 +343,10 @@ def _fork_plain(m, pool, parents, children, page):
 def _extend_plain(m, rows, page):
     """One token more for each sequence in `rows`: the tokens' slots, and what became of each request."""
     old = m["lens"][rows].long()
-    need = old % page == 0
+    room = old < m["tables"].shape[1] * page
+    need = (old % page == 0) & room
     rank = torch.cumsum(need, 0) - need.long()
-    fits = (~need | (rank < m["nfree"])) & (old < m["tables"].shape[1] * page)
+    fits = room & (~need | (rank < m["nfree"]))
     top = m["free"][(m["nfree"] - 1 - rank).clamp_min(0)]
     col = (old // page).clamp_max(m["tables"].shape[1] - 1)
     entry = torch.where(need & fits, top, m["tables"][rows, col])
