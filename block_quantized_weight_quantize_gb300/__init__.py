@@ -22,7 +22,7 @@ BLOCK = {Q8_0: 32, Q4K: 256, Q6K: 256}
 FORMATS = {"f16": F16, "q8_0": Q8_0, "q4k": Q4K, "q6k": Q6K}
 
 QB_OK, QB_E_ARG, QB_E_FORMAT, QB_E_BLOCK, QB_E_CUDA, QB_E_UNREADABLE, QB_E_DEVICE = 0, -1, -2, -3, -4, -5, -6
-QB_E_SCRATCH = -7
+QB_E_SCRATCH, QB_E_PAGES, QB_E_INDEX = -7, -8, -9
 STATIC_SCRATCH_BYTES = 1 << 20  # QB_STATIC_SCRATCH_BYTES
 MAX_MATS = 4  # QB_MAX_MATS
 
@@ -34,7 +34,10 @@ EXPORTS = ("quantize_act", "q_gemv", "quantize_act_f16", "q_gemv_f16", "q_check_
            "q_block_values", "q_device_status", "q_strerror", "q_matvec", "q_matvec_workspace_bytes",
            "q_matvec_static", "q_gemv_many", "q_gemv_f16_many", "q_matvec_many", "quantize_act_sub32",
            "q_gemv_sub32", "q_matvec_sub32_workspace_bytes", "q_matvec_sub32", "kv_head_codes", "kv_cache_rows",
-           "kv_quantize_heads", "kv_scores", "q_gemv_fp8", "q_matvec_host_workspace_bytes", "q_matvec_host", "q_gemv_w2")
+           "kv_quantize_heads", "kv_scores", "q_gemv_fp8", "q_matvec_host_workspace_bytes", "q_matvec_host", "q_gemv_w2",
+           "kv4_block_bytes", "kv4_append", "kv4_read", "kv4_attn_workspace_bytes", "kv4_attn",
+           "kv_pages_workspace_bytes", "kv_pages_reset", "kv_pages_extend", "kv_pages_fork", "kv_pages_free",
+           "kv_pages_compact", "kv_pages_copy")
 PERBLOCK, SUB32 = 0, 1  # QB_PERBLOCK, QB_SUB32: how an activation (or a query head) is scaled
 
 
@@ -387,3 +390,18 @@ def matvec(fmt: int, W, rows: int, K: int, x, out=None, act=None, stream=None):
     quantize_act(BLOCK[fmt], x, *act, stream=stream)
     q_gemv(fmt, W, rows, K, act, ncols, out, stream)
     return out
+
+
+# ------------------------------------------------------------------ the paged 4-bit cache (kv4.py)
+
+_KV4 = ("Kv4", "KvSeqs", "KvPages", "T_F32", "T_F16", "T_BF16") + EXPORTS[EXPORTS.index("kv4_block_bytes"):]
+
+
+def __getattr__(name):
+    # kv4.py imports torch: it is loaded by the first use of one of its names
+    if name in _KV4:
+        from . import kv4
+        value = getattr(kv4, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

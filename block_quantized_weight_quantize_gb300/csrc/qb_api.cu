@@ -270,7 +270,7 @@ int q_device_status(void *stream) {
     if (cudaMemcpyToSymbolAsync(g_fault, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess)
         return QB_E_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return QB_E_CUDA;
-    return h ? QB_E_DEVICE : QB_OK;
+    return h & kFaultMbarTimeout ? QB_E_DEVICE : h ? QB_E_INDEX : QB_OK;
 }
 
 static int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -667,6 +667,8 @@ const char *q_strerror(int status) {
     case QB_E_UNREADABLE: return "weights hold an infinite or NaN block scale";
     case QB_E_DEVICE: return "a kernel gave up a bounded wait";
     case QB_E_SCRATCH: return "request needs more than the library's static scratch (QB_STATIC_SCRATCH_BYTES)";
+    case QB_E_PAGES: return "no free page, or no room in the sequence's table row";
+    case QB_E_INDEX: return "a kernel met a slot, page or row number outside its cache";
     default: return "unknown status";
     }
 }

@@ -27,6 +27,8 @@ __host__ __device__ inline int64_t record_bytes(int f, int64_t K) {
 // Bit set in the library's device fault word (a __device__ int in qb_api.cu,
 // passed to kernels by address) when a kernel gives up a bounded wait.
 constexpr int kFaultMbarTimeout = 1;
+// ... and when a 4-bit cache or page kernel meets an index outside its cache.
+constexpr int kFaultIndex = 2;
 
 // ---------------------------------------------------------------- PTX wrappers
 

@@ -1,0 +1,134 @@
+// qb_kv4.cuh -- the stored form of the paged 4-bit key/value cache (declared
+// in qgemv.h) as the kernels see it: sizes, the places of codes and steps, and
+// element types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qb_common.cuh"
+#include "qb_launch.h"
+
+namespace qb {
+
+__host__ __device__ constexpr int kv4_padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+// bytes of one (page, key head) block of `page` rows
+__host__ __device__ constexpr int kv4_block(int page, int dp) { return 2 * page * (dp / 2 + dp / 16); }
+
+struct Kv4View {
+    uint8_t *data;
+    int npages, page, pshift, nkv, d, dp;
+    int64_t block_bytes;
+};
+
+inline Kv4View kv4_view(const qb_kv4 &c) {
+    Kv4View v;
+    v.data = static_cast<uint8_t *>(c.data);
+    v.npages = c.npages;
+    v.page = c.page;
+    v.pshift = c.page == 16 ? 4 : c.page == 32 ? 5 : 6;
+    v.nkv = c.nkv;
+    v.d = c.d;
+    v.dp = kv4_padded(c.d);
+    v.block_bytes = kv4_block(c.page, v.dp);
+    return v;
+}
+
+// Byte offset in a block of `page` rows of the word that holds elements
+// 8*oct .. 8*oct+7 of a key row, and of the two halves (4 elements each) of a
+// value row (half h of 0, 1); w = groups a plane.
+__device__ __forceinline__ int kv4_key_word(int page, int w, int r, int oct) {
+    const int G = oct >> 2, t = oct & 3;
+    return ((((G >> 2) * page + r) * 4 + t) * w + (G & 3)) * 4;
+}
+__device__ __forceinline__ int kv4_value_half(int page, int w, int r, int oct, int h) {
+    const int G = oct >> 2, c = (2 * (oct & 3) + h) ^ (4 * ((r >> 1) & 1));
+    return ((((G >> 2) * page + r) * 8 + c) * w + (G & 3)) * 2;
+}
+
+// Eight consecutive elements of `type` as f32; p is aligned to their size (16 or 32 bytes).
+template <int TYPE>
+__device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
+    if constexpr (TYPE == QB_T_F32) {
+        const float4 a = static_cast<const float4 *>(p)[0], b = static_cast<const float4 *>(p)[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 u = *static_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == QB_T_F16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+// Eight f32 values rounded once to `type` and stored.
+template <int TYPE>
+__device__ __forceinline__ void store8(void *p, const float (&x)[8]) {
+    if constexpr (TYPE == QB_T_F32) {
+        static_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        static_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == QB_T_F16) {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        *static_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__host__ __device__ constexpr int type_bytes(int type) { return type == QB_T_F32 ? 4 : 2; }
+
+// Launchers (qb_kv4_rows.cu, qb_kv4_attn.cu, qb_kv_pages.cu); arguments checked by the C entries.
+int launch_kv4_append(const Kv4View &c, int type, const void *k, int64_t ks, const void *v, int64_t vs,
+                      const int32_t *slots, int64_t n, cudaStream_t stream);
+int launch_kv4_read(const Kv4View &c, int type, const int32_t *slots, int64_t n, void *k, int64_t ks, void *v,
+                    int64_t vs, cudaStream_t stream);
+
+struct Kv4AttnArgs {
+    Kv4View c;
+    qb_kv_seqs s;
+    int type;
+    const void *q;
+    int64_t q_stride;
+    int64_t ntok;
+    int nh;
+    float scale;
+    int window;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    uint8_t *ws;
+    int *fault;
+};
+int64_t kv4_attn_ws(int nkv, int dp, int nh);
+int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream);
+
+int64_t kv_pages_ws(int npages, int nrows);
+int launch_kv_pages_reset(const qb_kv_pages &p, cudaStream_t stream);
+int launch_kv_pages_extend(const qb_kv_pages &p, const int32_t *rows, const int32_t *counts, int n, int32_t *slots,
+                           int64_t nslots, int32_t *status, cudaStream_t stream);
+int launch_kv_pages_fork(const qb_kv_pages &p, void *data, int nlayers, int64_t page_bytes, const int32_t *parents,
+                         const int32_t *children, int n, int32_t *status, void *ws, cudaStream_t stream);
+int launch_kv_pages_free(const qb_kv_pages &p, const int32_t *rows, int n, cudaStream_t stream);
+int launch_kv_pages_compact(const qb_kv_pages &p, void *data, int nlayers, int64_t page_bytes, void *ws,
+                            cudaStream_t stream);
+int launch_kv_pages_copy(void *data, int nlayers, int64_t npages, int64_t page_bytes, const int32_t *src,
+                         const int32_t *dst, int n, cudaStream_t stream);
+
+}  // namespace qb

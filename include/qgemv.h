@@ -94,7 +94,9 @@ enum {
     QB_E_CUDA = -4,       /* a CUDA call or launch failed */
     QB_E_UNREADABLE = -5, /* q_check_weights found an inf/NaN block scale (numerics page, Unreadable) */
     QB_E_DEVICE = -6,     /* a kernel gave up a bounded wait (q_device_status) */
-    QB_E_SCRATCH = -7     /* q_matvec_static: the request needs more than the library's static scratch */
+    QB_E_SCRATCH = -7,    /* q_matvec_static: the request needs more than the library's static scratch */
+    QB_E_PAGES = -8,      /* no free page, or no room in the sequence's table row (a status that kernels write) */
+    QB_E_INDEX = -9       /* a kernel met a slot, page or row number outside its cache (q_device_status) */
 };
 
 /* Size of the library's static scratch array used by q_matvec_static. */
@@ -238,8 +240,9 @@ QB_API int q_block_values(qb_fmt fmt, const void *W, int64_t rows, int64_t K, co
                    int32_t *C, int32_t *O, float *v, void *stream);
 
 /* Reads and clears the library's device fault word (set when a kernel gives
- * up a bounded wait on its own copies).  Synchronizes `stream`.  Returns
- * QB_OK or QB_E_DEVICE. */
+ * up a bounded wait on its own copies, or when a 4-bit cache or page kernel
+ * meets an index outside its cache).  Synchronizes `stream`.  Returns QB_OK,
+ * QB_E_DEVICE or QB_E_INDEX. */
 QB_API int q_device_status(void *stream);
 
 /* Most matrices one grouped call (q_gemv_many, q_gemv_f16_many,
@@ -400,6 +403,169 @@ QB_API int64_t q_matvec_host_workspace_bytes(int scaling, qb_fmt fmt, int64_t ro
  * errors are those of q_matvec / q_matvec_sub32. */
 QB_API int q_matvec_host(int scaling, qb_fmt fmt, const void *W, int64_t rows, int64_t K, const float *x_host,
                          int ncols, float *out_host, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- A paged key/value cache in 4 bits, and attention over it.
+ *
+ * Stored form.  A row (one token, one key head) of d elements is padded with
+ * zeros to dp = 64, 128 or 256 elements and cut into groups of 32.  A group's
+ * step is its element of largest magnitude (the positive one where two are
+ * equal) over -8, rounded to binary16; an element's code is 8 plus the nearest
+ * integer (ties to even, kept in -8..7) of the f32 product of the element and
+ * the step's correctly rounded f32 reciprocal; it stands for (code - 8) * step.
+ * NaN elements are passed over by the step and get code 8 (zero); a group
+ * whose step overflows binary16 (an infinity in it, or magnitudes from
+ * 524160 up) reads back as NaN, and a row's dots with it are NaN; a step that
+ * rounds to zero makes the group zeros.
+ *
+ * A page holds `page` (16, 32 or 64) tokens of every key head: nkv blocks of
+ * kv4_block_bytes(page, d) bytes, each
+ *     keys' codes (page*dp/2 B) | keys' steps (page*dp/16 B) | values' codes | values' steps
+ * with steps f16 [page][dp/32].  With w = min(dp/32, 4) groups a plane (dp/128
+ * planes of up to 128 elements), the code of row r, element i (group G = i/32,
+ * plane p = G/4, g = G%4, e = i%32) is nibble N of its code area (byte N/2,
+ * the low half where N is even):
+ *     keys:    N = (((p*page + r)*4 + e/8)*w + g)*8 + e%8
+ *     values:  N = (((p*page + r)*8 + (e/4 ^ 4*(r>>1 & 1)))*w + g)*4 + e%4
+ * so that a thread of a tensor-core fragment finds its share of a row in one
+ * wide load, and the shares of neighbouring rows in different banks. */
+
+/* Element types of the rows, queries and outputs of the calls below. */
+typedef enum { QB_T_F32 = 0, QB_T_F16 = 1, QB_T_BF16 = 2 } qb_type;
+
+/* One layer's cache: data is device memory, 16-byte aligned, npages pages of
+ * nkv * kv4_block_bytes(page, d) bytes.  d % 8 == 0, 8 <= d <= 256;
+ * 1 <= nkv <= 1024; npages * page < 2^31. */
+typedef struct {
+    void *data;
+    int npages;
+    int page;
+    int nkv;
+    int d;
+} qb_kv4;
+
+/* Bytes of one (page, key head) block, or a negative QB_E_* code. */
+QB_API int64_t kv4_block_bytes(int page, int d);
+
+/* Writes n rows of keys and values of every key head into the cache: token
+ * i's rows k + i*k_stride and v + i*v_stride (elements; nkv*d contiguous ones
+ * each) go to slot slots[i] = page number * page + place in the page.  A slot
+ * below zero is passed over; one past the cache is passed over and reported by
+ * q_device_status.  Slots of one call are distinct.  k, v 16-byte aligned, strides
+ * multiples of 16 bytes.  Asynchronous on stream, one launch. */
+QB_API int kv4_append(const qb_kv4 *cache, qb_type type, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *slots, int64_t n, void *stream);
+
+/* Reads n rows back: the values that the stored codes and steps stand for,
+ * rounded once to `type`, into k and v (strides as in kv4_append).  A slot
+ * below zero, or past the cache (reported), reads as zeros. */
+QB_API int kv4_read(const qb_kv4 *cache, qb_type type, const int32_t *slots, int64_t n, void *k, int64_t k_stride,
+                    void *v, int64_t v_stride, void *stream);
+
+/* The sequences of a call (device memory): sequence s has the table row
+ * tables + R*maxp and the length lens[R] with R = rows[s] (rows NULL: R = s);
+ * key i of it is row i % page of page tables[..][i / page].  Its new tokens
+ * are q_start[s] .. q_start[s+1]-1 of the call's (q_start NULL: the one token
+ * s), the last ones of its lens[R] tokens, already in the cache.
+ * 1 <= nseq <= 8192. */
+typedef struct {
+    const int32_t *tables;
+    const int32_t *lens;
+    const int32_t *rows;
+    const int32_t *q_start;
+    int nrows;
+    int maxp;
+    int nseq;
+} qb_kv_seqs;
+
+/* Device workspace kv4_attn needs for any call with this cache's nkv and d and
+ * nh query heads, or a negative QB_E_* code.  It needs no initial contents. */
+QB_API int64_t kv4_attn_workspace_bytes(const qb_kv4 *cache, int nh);
+
+/* Attention of ntok new tokens over the cache.  Token j of sequence s (T new
+ * ones of length n) is at place P = n - T + j and sees the keys i <= P, and
+ * with window > 0 only those with i > P - window.  For each of the nh query
+ * heads (head h reads key head h / (nh/nkv)), over the keys that it sees,
+ *     z_i = scale * sum_e q_e k_ie,  out = sum_i exp(z_i) v_i / sum_i exp(z_i),
+ *     lse = log sum_i exp(z_i);
+ * a token that sees no key gets out 0 and lse -infinity.  q and out
+ * [ntok][nh][d] of `type` with q_stride and out_stride elements between
+ * tokens; lse f32 [ntok][nh] or NULL.  Sums and softmax statistics are f32; with
+ * QB_T_F32 queries and probabilities enter the products as pairs of f16 (22
+ * bits), otherwise as one f16.  Queries of magnitude past 2^110 are out of
+ * range.  q, out 16-byte aligned, strides multiples of 16 bytes; nh % nkv == 0.
+ * workspace: at least kv4_attn_workspace_bytes() bytes, 16-byte aligned, not
+ * shared with a call that may run at the same time.  A length past its table row is cut to it; a row
+ * or page number outside its range reads as no keys / page 0 and is reported
+ * by q_device_status; tokens that no sequence holds are not written. */
+QB_API int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void *q, int64_t q_stride,
+                    int64_t ntok, int nh, float scale, int window, void *out, int64_t out_stride, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- The pages of a cache: who holds which.
+ *
+ * A pool of npages pages serves nrows sequences; its state is device memory:
+ * nfree[0] free pages, free_pages[npages] a stack of them (the next to go is
+ * free_pages[nfree-1]), refs[npages] how many sequences hold a page, and for
+ * each sequence its length lens[nrows] and its table row
+ * tables[nrows][maxp]: ceil(len/page) page numbers, then -1.  A page held
+ * more than once is full.  The pages' bytes are opaque here: any cache laid
+ * out [layers][npages][page_bytes] can use these calls, page_bytes % 16 == 0.
+ * npages <= 2^20.  Every call is asynchronous on stream and gives the same
+ * state whatever the order its threads run in.  Sequence numbers
+ * outside 0..nrows-1 are passed over and reported by q_device_status. */
+typedef struct {
+    int32_t *nfree;
+    int32_t *free_pages;
+    int32_t *refs;
+    int32_t *lens;
+    int32_t *tables;
+    int page;
+    int npages;
+    int nrows;
+    int maxp;
+} qb_kv_pages;
+
+/* Device workspace of kv_pages_fork and kv_pages_compact, or QB_E_ARG. */
+QB_API int64_t kv_pages_workspace_bytes(const qb_kv_pages *pages);
+
+/* Every page free (page 0 the next to go), every sequence empty. */
+QB_API int kv_pages_reset(const qb_kv_pages *pages, void *stream);
+
+/* Room for counts[i] >= 0 more tokens of sequence rows[i], i < n (distinct
+ * sequences), served in order: pages are taken for them, the lengths grow, and
+ * the new tokens' slots (as kv4_append takes them) follow one another in
+ * `slots`, request after request.  A request that the pages left by those
+ * before it (refused ones counted as served) or its table row cannot hold is refused whole:
+ * its slots are -1.  status[i]: QB_OK, QB_E_PAGES or QB_E_ARG.  slots has room
+ * for `nslots` entries; those past it are dropped and reported. */
+QB_API int kv_pages_extend(const qb_kv_pages *pages, const int32_t *rows, const int32_t *counts, int n,
+                           int32_t *slots, int64_t nslots, int32_t *status, void *stream);
+
+/* Sequence children[i] (empty) becomes a copy of parents[i], i < n: full pages
+ * are shared, a partly filled last page is copied, in every layer of data, to
+ * a free page.  Children are distinct and none is a parent of the same call.
+ * status[i]: QB_OK, QB_E_PAGES (no free page: the child stays empty), or
+ * QB_E_ARG (a child that is not empty). */
+QB_API int kv_pages_fork(const qb_kv_pages *pages, void *data, int nlayers, int64_t page_bytes,
+                         const int32_t *parents, const int32_t *children, int n, int32_t *status, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Sequences rows[i], i < n (distinct), become empty; pages that nobody holds
+ * any more go back to the stack in ascending order. */
+QB_API int kv_pages_free(const qb_kv_pages *pages, const int32_t *rows, int n, void *stream);
+
+/* Moves the pool together: with U pages held, the i-th held page from U up
+ * (ascending) is moved, in every layer of data, to the i-th free page below U;
+ * tables and refs follow, and the free pages are U..npages-1 (U the next to
+ * go), so that the pool's end can be given back. */
+QB_API int kv_pages_compact(const qb_kv_pages *pages, void *data, int nlayers, int64_t page_bytes, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Copies page src[i] to page dst[i], i < n, in every layer.  No page is both a
+ * source and a destination, no destination listed twice.  Pairs outside the
+ * pool are passed over and reported. */
+QB_API int kv_pages_copy(void *data, int nlayers, int64_t npages, int64_t page_bytes, const int32_t *src,
+                         const int32_t *dst, int n, void *stream);
 
 /* A static string for a status code. */
 QB_API const char *q_strerror(int status);
