@@ -8,8 +8,9 @@ products take one f16 factor) and the sums with at most A = 2^-19 of Z (f32
 sums of up to a few hundred rounded terms a partial sum, and the rescalings).  So
 a score is off by Z*(2E + A), a probability by twice that relatively (its own
 exponent and the normalizing sum's), a product with a value by E + A more; the
-output is rounded once.  A probability below 2^-126 may vanish: n keys with
-values of at most V lose n*V*2^-126.
+output is rounded once.  A probability below 2^-38 may vanish (f16's least
+number under a largest one of 2^14, as the header states): n keys with values of
+at most V lose n*V*2^-38.
 """
 import numpy as np
 import pytest
@@ -161,7 +162,7 @@ class Batch:
         e = IN[self.name]
         off = zabs * (2 * e + SUM)
         tol = (2 * off + e + SUM)[..., None] * mag + OUT[self.name] * np.abs(want) + 2.0 ** -24 * (self.name != "f32")
-        tol += len(self.v) * np.abs(self.v).max(initial=0) * 2.0 ** -126
+        tol += len(self.v) * np.abs(self.v).max(initial=0) * 2.0 ** -38
         got = out.double().cpu().numpy()
         assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / np.maximum(tol, 1e-30))
         gl = lse.double().cpu().numpy()
