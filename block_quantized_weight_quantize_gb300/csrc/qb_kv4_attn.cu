@@ -10,8 +10,13 @@ namespace qb {
 int64_t kv4_attn_ws(int nkv, int dp, int nh) {
     (void)nkv;
     (void)nh;
-    const int64_t workers = (int64_t)std::min(num_sms(), 256) * kStepWarps;
-    return workers * 2 * kMaxRows * (4 * dp + 8) + workers * 2 * 16;
+    int64_t most = 0;
+    for (int nt = 1; nt <= 2; ++nt)
+        for (int pair = 0; pair < 2; ++pair) {
+            const int64_t workers = (int64_t)step_grid() * step_warps(dp, pair != 0, nt), rows = step_rows(pair != 0, nt);
+            most = std::max(most, workers * 2 * (rows * (4 * dp + 8) + 16));
+        }
+    return most;
 }
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {

@@ -9,20 +9,24 @@
 // again a product with whole codes, of the probabilities times the steps.  m is
 // the running maximum; sums and maxima are f32.
 //
-// Operands.  Codes become f16 without a conversion.  Keys: a code in the low bits
-// of an f16 is the subnormal c * 2^-24, exact, so a mask is the whole unpacking;
-// the -8 is the accumulator's initial value, -8 * sum of the queries.
-// Values: (1024 + c) - 1032 by one packed addition (the sum of probabilities
-// times 8 taken off at the end would cancel where the values' mean is small).
-// Queries are scaled by a power of two a row to f16's top; in f32 they enter as
-// two f16 (high and low part, 22 bits), in rows r and r + 8 of the same
-// m16n8k16 product.  The probabilities times steps likewise, scaled by a power of
-// two that follows the largest step seen (as the running maximum does).
+// Operands.  The codes are the A side (16 keys, or 16 of the value's elements, by
+// 16), the rows the 8 columns of the B side, since a step has few rows: 4 rows as
+// pairs (high part, low part) in f32 or where there are no more, else 8 rows.  Codes become f16
+// without a conversion: a code in the low bits of an f16 is the subnormal
+// c * 2^-24, exact, and 1024 + c is one OR away.  Half-precision keys take the
+// first where there are 8 rows, with -8 * sum of the queries as the sums'
+// initial value; elsewhere a
+// packed addition takes 1032 off (the sum of q or p times 8 taken off at the end
+// costs f32 its last three bits: an error of 1.4e-6 against 2.1e-7).  Queries are
+// scaled by a power of two a row to f16's top; in f32 they enter as two f16 (22
+// bits).  The probabilities times steps likewise, scaled by a power of two that
+// follows the largest step seen (as the running maximum does), and pass from the
+// scores' layout to the B side by an 8 x 8 transpose in registers.
 //
-// Layout.  A lane of the B fragment (column g, slots of t) needs 8 elements of
-// key g in one word: the cache's key rows are ordered so that one wide load holds
-// a lane's words of all groups; value rows so that it holds a lane's halves.
-// Columns are keys in the order 0 7 1 6 2 5 3 4 (column 2t: key t, 2t + 1: key
+// Layout.  A lane of the A fragment (row g, slots of t) needs 8 elements of key g
+// in one word: the cache's key rows are ordered so that one wide load holds a
+// lane's words of all groups; value rows so that it holds a lane's halves.
+// Rows of 8 are keys in the order 0 7 1 6 2 5 3 4 (row 2t: key t, 2t + 1: key
 // 7 - t), which keeps both loads free of bank conflicts.
 //
 // Work.  Units of 32 keys of one (sequence, key head, row tile), counted along
@@ -33,21 +37,33 @@
 // sums in the workspace, joined by kv4_combine_kernel in the order of the keys.
 #pragma once
 
+#include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "qb_kv4.cuh"
 
 namespace qb {
 
-constexpr int kStepWarps = 8;
 constexpr int kUnit = 32;       // keys a unit
-constexpr int kMaxRows = 16;    // rows (token, query head) of a row tile
 constexpr int kSeqChunk = 32;   // sequences summed together in a block's table
 
-template <int DP>
-constexpr int step_stages() { return DP == 64 ? 8 : DP == 128 ? 6 : 3; }
-template <int DP>
-constexpr int step_unit_bytes() { return kv4_block(kUnit, DP); }
+__host__ __device__ constexpr int step_unit_bytes(int dp) { return kv4_block(kUnit, dp); }
+// Rows (token, query head) of a row tile: nt column tiles of 4 rows, as pairs of
+// high and low part, or of 8 rows.
+__host__ __device__ constexpr int step_rows(bool pair, int nt) { return (pair ? 4 : 8) * nt; }
+// Warps of a block (one a multiprocessor), by the registers that a lane's sums
+// (dp / 4 * nt of them), queries and scores take.
+__host__ __device__ constexpr int step_warps(int dp, bool pair, int nt) {
+    return dp * nt > 128 ? 8 : pair && nt == 1 ? 16 : 12;
+}
+__host__ __device__ constexpr int step_stages(int dp, bool pair, int nt) {
+    const int n = 221184 / (step_warps(dp, pair, nt) * step_unit_bytes(dp));
+    return n > 8 ? 8 : n;
+}
+
+constexpr int kMaxGrid = 256, kMaxWorkers = kMaxGrid * 16;
+inline int step_grid() { return std::min(num_sms(), kMaxGrid); }
 
 struct StepK {
     Kv4AttnArgs a;
@@ -55,8 +71,8 @@ struct StepK {
     int nosplit;      // a worker's share is whole items
     int nworkers;
     int min_share;    // units
-    float *part;      // [nworkers][2][kMaxRows][DP]
-    float2 *stat;     // [nworkers][2][kMaxRows] running maximum, sum
+    float *part;      // [nworkers][2][rows][DP]
+    float2 *stat;     // [nworkers][2][rows] running maximum, sum
     int4 *meta;       // [nworkers][2] of the item that starts at a worker and goes on: the last worker that
                       // holds a piece of it (-1: no such item), first token, tokens, key head; row tile
 };
@@ -75,14 +91,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// rows 8..15 of A and of the sums are not used
-__device__ __forceinline__ void mma_f16(float (&c)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "{\n\t.reg .f32 x, y;\n\t"
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, x, y}, {%2, %3, %4, %3}, {%5, %6}, "
-        "{%0, %1, %7, %7};\n\t}"
-        : "+f"(c[0]), "+f"(c[1])
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.0f));
+// An 8 x 8 matrix of f16, a row's two neighbours a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Codes in the low (or second) four bits of each half, as code - 8.
+__device__ __forceinline__ uint32_t centre_lo(uint32_t w) {
+    uint32_t b = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + c
+    __half2 &h = *reinterpret_cast<__half2 *>(&b);
+    h = __hadd2(h, __float2half2_rn(-1032.0f));
+    return b;
+}
+__device__ __forceinline__ uint32_t centre_hi(uint32_t w) {
+    uint32_t b = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 c
+    __half2 &h = *reinterpret_cast<__half2 *>(&b);
+    h = __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
+    return b;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -140,66 +167,55 @@ __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0,
     nu = max(1, (q.len + kUnit - 1) / kUnit - u0);
 }
 
-// MODE 0: f32 rows (R = 8, two f16 a factor); 1: half precision, up to 8 rows; 2: half precision, 16 rows.
-template <int MODE>
-constexpr int step_rows() { return MODE == 2 ? 16 : 8; }
-
-// position in the call's work
+// A place in the call's work: sequence, key head, row tile, unit of the key axis.
 struct StepPos {
-    int s, kvh, rt, u;       // sequence, key head, row tile, unit of the item
-    int row, len, T, q0;     // the sequence
-    int u0, nu, nrt;
-    int base;                // the sequences base .. base + 31 are in the lanes' registers
-    SeqInfo mine;            // lane l: sequence base + l
+    int s, kvh, rt, u, u_end;  // u counts from the sequence's first key
+    int row, len;
 };
 
-template <int R>
-__device__ __forceinline__ void step_load_seq(const StepK &p, StepPos &x, int lane) {
-    for (;;) {  // past sequences without new tokens
-        if (x.s >= x.base + 32) {
-            x.base = x.s;
-            x.mine = seq_info(p.a, x.base + lane, false);
-        }
-        const int l = x.s - x.base;
-        x.row = __shfl_sync(0xFFFFFFFFu, x.mine.row, l);
-        x.len = __shfl_sync(0xFFFFFFFFu, x.mine.len, l);
-        x.T = __shfl_sync(0xFFFFFFFFu, x.mine.T, l);
-        x.q0 = __shfl_sync(0xFFFFFFFFu, x.mine.q0, l);
-        if (x.T > 0 || x.s >= p.a.s.nseq) break;
-        ++x.s;
-    }
-    const SeqInfo q = {x.row, x.len, x.T, x.q0};
-    seq_units(q, p.a.window, x.u0, x.nu);
-    x.nrt = (x.T * p.grp + R - 1) / R;
+// Sequence s: from the warp's table (those from `base` on), else from memory.
+__device__ __forceinline__ SeqInfo step_seq(const StepK &p, const SeqInfo *tab, int base, int s) {
+    if (s < base + 32) return tab[s - base];
+    return seq_info(p.a, s, false);
 }
 
-// the next unit; whether it begins another item
+// Enters the first sequence from x.s on that has new tokens.
+__device__ __forceinline__ SeqInfo step_enter(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
+    SeqInfo q = step_seq(p, tab, base, x.s);
+    while (q.T == 0 && x.s < p.a.s.nseq) q = step_seq(p, tab, base, ++x.s);
+    int nu;
+    seq_units(q, p.a.window, x.u, nu);
+    x.u_end = x.u + nu;
+    x.row = q.row;
+    x.len = q.len;
+    return q;
+}
+
+// The item after the one that x is in; u at its beginning.
 template <int R>
-__device__ __forceinline__ bool step_next(const StepK &p, StepPos &x, int lane) {
-    if (++x.u < x.nu) return false;
-    x.u = 0;
-    if (++x.rt == x.nrt) {
+__device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
+    const SeqInfo q = step_seq(p, tab, base, x.s);
+    if (++x.rt == (q.T * p.grp + R - 1) / R) {
         x.rt = 0;
         if (++x.kvh == p.a.c.nkv) {
             x.kvh = 0;
             ++x.s;
-            step_load_seq<R>(p, x, lane);
         }
     }
-    return true;
+    step_enter(p, tab, base, x);
 }
 
-template <int DP, int MODE, int SB>
-__global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const StepK p) {
-    constexpr int R = step_rows<MODE>(), NR = MODE == 2 ? 2 : 1;   // rows of a tile, rows of a lane
-    constexpr int NC = MODE == 1 ? 2 : 4;                          // sums a lane holds of a product
-    constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;  // groups, groups a plane, planes
-    constexpr int kStages = step_stages<DP>(), kBytes = step_unit_bytes<DP>();
-    constexpr int kSub = kv4_block(SB, DP);                        // a sub-block of SB rows in shared memory
+template <int DP, bool PAIR, int NT, int SB>
+__global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_kernel(const StepK p) {
+    constexpr int kWarps = step_warps(DP, PAIR, NT), kStages = step_stages(DP, PAIR, NT), kBytes = step_unit_bytes(DP);
+    constexpr int R = step_rows(PAIR, NT), RT = R / NT, NH = PAIR ? 1 : 2;  // rows: of a tile, a column tile, a lane's
+    constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;         // groups, groups a plane, planes
+    constexpr int kSub = kv4_block(SB, DP);                               // a sub-block of SB rows in shared memory
     constexpr int kCodes = SB * DP / 2, kSteps = SB * DP / 16, kPlane = SB * 16 * W;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full_bars[kStepWarps][kStages];
+    __shared__ __align__(8) uint64_t full_bars[kWarps][kStages];
     __shared__ long long chunk_sum[8192 / kSeqChunk + 1];
+    __shared__ SeqInfo tabs[kWarps][32];  // a warp's sequences, from its first one's chunk on
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t *ring = smem + warp * kStages * kBytes;
@@ -212,10 +228,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
 
     // ---- the work: units before each chunk of sequences
     const int nseq = p.a.s.nseq, nchunks = (nseq + kSeqChunk - 1) / kSeqChunk;
-    SeqInfo mine = {0, 0, 0, 0};
-    for (int c = warp; c < nchunks; c += kStepWarps) {
+    for (int c = warp; c < nchunks; c += kWarps) {
         const SeqInfo q = seq_info(p.a, c * kSeqChunk + lane, blockIdx.x == 0);
-        if (nchunks == 1) mine = q;
         int u0, nu;
         seq_units(q, p.a.window, u0, nu);
         long long n = (long long)p.a.c.nkv * ((q.T * p.grp + R - 1) / R) * (p.nosplit ? 1 : nu);
@@ -224,17 +238,19 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
         if (lane == 0) chunk_sum[c] = n;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        long long sum = 0;
-        for (int c = 0; c < nchunks; ++c) {
-            const long long n = chunk_sum[c];
-            chunk_sum[c] = sum;
-            sum += n;
+    if (nchunks > 1) {
+        if (threadIdx.x == 0) {
+            long long sum = 0;
+            for (int c = 0; c < nchunks; ++c) {
+                const long long n = chunk_sum[c];
+                chunk_sum[c] = sum;
+                sum += n;
+            }
+            chunk_sum[nchunks] = sum;
         }
-        chunk_sum[nchunks] = sum;
+        __syncthreads();
     }
-    __syncthreads();
-    const long long total = chunk_sum[nchunks];
+    const long long total = nchunks > 1 ? chunk_sum[nchunks] : chunk_sum[0];
     // workers in the order of the units: neighbours are on different multiprocessors
     const int worker = warp * gridDim.x + blockIdx.x;
     long long share = (total + p.nworkers - 1) / p.nworkers;
@@ -243,38 +259,42 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
     if (lane == 0 && !p.nosplit) p.meta[worker * 2].x = -1;
     if (begin >= end) return;
 
+    const int count = (int)(end - begin);  // units (items) of this worker
+    SeqInfo *tab = tabs[warp];
+    int base;
     StepPos cur;
-    cur.s = 0;
     {
         int lo = 0, hi = nchunks;  // the chunk that holds unit `begin`
         while (hi - lo > 1) {
             const int m = (lo + hi) / 2;
             if (chunk_sum[m] <= begin) lo = m; else hi = m;
         }
-        cur.base = lo * kSeqChunk;
-        if (nchunks == 1 && warp == 0) cur.mine = mine;
-        else cur.mine = seq_info(p.a, cur.base + lane, false);
+        base = lo * kSeqChunk;
+        const SeqInfo q = seq_info(p.a, base + lane, false);
+        tab[lane] = q;
         int u0, nu;
-        seq_units(cur.mine, p.a.window, u0, nu);
-        const int items = p.a.c.nkv * ((cur.mine.T * p.grp + R - 1) / R);
-        const long long n = (long long)items * (p.nosplit ? 1 : nu);
+        seq_units(q, p.a.window, u0, nu);
+        const int nrt = (q.T * p.grp + R - 1) / R;
+        const long long n = (long long)p.a.c.nkv * nrt * (p.nosplit ? 1 : nu);
         long long sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += y;
         }
-        const long long before = chunk_sum[lo] + sum - n;
+        const long long before = (nchunks > 1 ? chunk_sum[lo] : 0) + sum - n;
         // the last lane with units that starts at or before `begin`
         const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= begin);
         const int l = 31 - __clz(ok);
         const long long rem = begin - __shfl_sync(0xFFFFFFFFu, before, l);
-        cur.s = cur.base + l;
-        step_load_seq<R>(p, cur, lane);
-        const long long it = p.nosplit ? rem : rem / cur.nu;
-        cur.u = p.nosplit ? 0 : (int)(rem - it * cur.nu);
-        cur.kvh = (int)(it / cur.nrt);
-        cur.rt = (int)(it - (long long)cur.kvh * cur.nrt);
+        const int l_nu = __shfl_sync(0xFFFFFFFFu, nu, l), l_nrt = __shfl_sync(0xFFFFFFFFu, nrt, l);
+        cur.s = base + l;
+        const long long it = p.nosplit ? rem : rem / l_nu;
+        cur.kvh = (int)(it / l_nrt);
+        cur.rt = (int)(it - (long long)cur.kvh * l_nrt);
+        __syncwarp();
+        step_enter(p, tab, base, cur);
+        if (!p.nosplit) cur.u += (int)(rem - it * l_nu);
     }
 
     // ---- the copies, kStages units ahead.  A lane has one piece of a unit:
@@ -296,38 +316,41 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
         dst_off = lane * kSub;
     }
     StepPos ahead = cur;
-    long long left_ahead = end - begin;
-    int pg = 0;  // this lane's page of the unit at `ahead`
-    bool pg_there = false;
+    int left_ahead = count;
+    int pg = -1;  // this lane's page of the unit at `ahead`; below zero: none
     auto find_page = [&]() {
-        pg_there = false;
+        pg = -1;
         if (left_ahead > 0 && nbytes) {
-            const int u = ahead.u0 + ahead.u;
-            const int pi = p.a.c.page == 64 ? u >> 1 : p.a.c.page == 32 ? u : 2 * u + sub;
-            if ((p.a.c.page == 64 ? u * kUnit : pi * p.a.c.page) < ahead.len) {
-                pg_there = true;
+            const int pi = p.a.c.page == 64 ? ahead.u >> 1 : p.a.c.page == 32 ? ahead.u : 2 * ahead.u + sub;
+            if ((p.a.c.page == 64 ? ahead.u * kUnit : pi * p.a.c.page) < ahead.len) {
                 pg = p.a.s.tables[(int64_t)ahead.row * p.a.s.maxp + pi];
+                if ((uint32_t)pg >= (uint32_t)p.a.c.npages) pg = INT_MAX;  // reported when its copy is due
             }
         }
     };
     int islot = 0;
     auto issue = [&]() {
         if (left_ahead > 0) {
-            if (pg_there && (pg < 0 || pg >= p.a.c.npages)) {
+            if (pg == INT_MAX) {
                 atomicOr(p.a.fault, kFaultIndex);
                 pg = 0;
             }
-            int bytes = pg_there ? nbytes : 0;
-#pragma unroll
-            for (int o = 4; o; o >>= 1) bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, o);  // pieces are in lanes 0..7
-            if (lane == 0) mbar_arrive_expect_tx(full + islot, (uint32_t)bytes);
+            const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
+            // half a page's pieces make a whole unit; the others are alike
+            if (lane == 0)
+                mbar_arrive_expect_tx(full + islot, !there ? 0u : p.a.c.page == 64 ? (uint32_t)kBytes
+                                                                                   : (uint32_t)(__popc(there) * kSub));
             __syncwarp();
-            if (pg_there)
+            if (pg >= 0)
                 bulk_g2s(ring + islot * kBytes + dst_off,
                          p.a.c.data + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes + src_off +
-                             (((ahead.u0 + ahead.u) & 1) ? half_mul : 0),
+                             ((ahead.u & 1) ? half_mul : 0),
                          (uint32_t)nbytes, full + islot);
-            const bool item_end = step_next<R>(p, ahead, lane);
+            bool item_end = false;
+            if (++ahead.u == ahead.u_end) {
+                item_end = true;
+                step_item<R>(p, tab, base, ahead);
+            }
             left_ahead -= p.nosplit ? (item_end ? 1 : 0) : 1;
             find_page();
         }
@@ -338,105 +361,87 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
     for (int i = 0; i < kStages; ++i) issue();
 
     // ---- this lane's places in a unit
-    const int key0 = t, key1 = 7 - t;                      // its columns 2t, 2t + 1 of eight keys
-    const int kcol = (g & 1) ? 7 - (g >> 1) : (g >> 1);    // the key of column g
-    const int koff = kcol * 16 * W + t * 4 * W;
-    const int voff0 = kCodes + kSteps + key0 * 16 * W + ((g ^ (4 * (t >> 1))) * 2 * W);
-    const int voff1 = kCodes + kSteps + key1 * 16 * W + ((g ^ (4 * (1 - (t >> 1)))) * 2 * W);
+    const int krow = (g & 1) ? 7 - (g >> 1) : (g >> 1);  // the key of row g of eight
+    const int koff = krow * 16 * W + t * 4 * W;
+    const int voff0 = kCodes + kSteps + t * 16 * W + ((g ^ (4 * (t >> 1))) * 2 * W);
+    const int voff1 = kCodes + kSteps + (7 - t) * 16 * W + ((g ^ (4 * (1 - (t >> 1)))) * 2 * W);
 
-    long long left = end - begin;
+    int left = count;
     int slot = 0;
     uint32_t phase = 0;
     while (left > 0) {
         // ---- an item, or this worker's piece of it
-        const int s_kvh = cur.kvh, s_rt = cur.rt, s_q0 = cur.q0, s_T = cur.T, s_len = cur.len, s_nu = cur.nu;
-        const bool from_start = cur.u == 0;
-        const long long item_left = s_nu - cur.u;  // units of the item from here on
-        const int units = (int)(p.nosplit ? item_left : min(item_left, left));
+        const int s_kvh = cur.kvh, s_rt = cur.rt, s_len = cur.len;
+        const SeqInfo sq = step_seq(p, tab, base, cur.s);
+        const int s_q0 = sq.q0, s_T = sq.T;
+        int u0, nu;
+        seq_units(sq, p.a.window, u0, nu);
+        const bool from_start = cur.u == u0;
+        const int item_left = cur.u_end - cur.u;  // units of the item from here on
+        const int units = p.nosplit ? item_left : min(item_left, left);
         const bool to_end = units == item_left;
 
-        // the lane's rows: token and head, place, queries as fragments
-        int pos[NR], first[NR];
-        int64_t otok[NR];
-        int ohead[NR];
-        bool live[NR];
-        uint32_t A[NG][2][NR == 2 || MODE == 0 ? 4 : 2];
-        float cinit[NG][MODE == 1 ? 1 : 2], cs[NR];
+        // the queries as B fragments: column g of tile n is a row (half precision) or a row's high or low part (f32)
+        uint32_t B[NT][NG][2][2];
+        float cinit[NT][NG][PAIR ? 1 : 2], cs[NT][NH];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const int rho = s_rt * R + g + 8 * r;
-            const int j = rho / p.grp;
-            live[r] = j < s_T;
-            pos[r] = live[r] ? s_len - s_T + j : -1;
-            first[r] = p.a.window ? max(0, pos[r] - p.a.window + 1) : 0;
-            otok[r] = s_q0 + j;
-            ohead[r] = s_kvh * p.grp + rho - j * p.grp;
-            float x[NG][8];
-            float top = 0.0f;
+        for (int n = 0; n < NT; ++n) {
+            const int rho = s_rt * R + n * RT + (PAIR ? g >> 1 : g), j = rho / p.grp;
+            const bool live = j < s_T;
+            const int64_t at = (int64_t)(s_q0 + j) * p.a.q_stride + (int64_t)(s_kvh * p.grp + rho - j * p.grp) * p.a.c.d;
+            auto load = [&](int G, float (&x)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+                const int el = G * 32 + t * 8;
+                if (!live || el >= p.a.c.d) return;
+                if (PAIR && p.a.type == QB_T_F32) {
+                    load8<QB_T_F32>(static_cast<const float *>(p.a.q) + at + el, x);
+                } else {
+                    const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at + el;
+                    if (p.a.type == QB_T_F16) load8<QB_T_F16>(q, x); else load8<QB_T_BF16>(q, x);
+                }
+            };
+            float x[8], top = 0.0f;
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
+                load(G, x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[G][i] = 0.0f;
-                if (live[r] && G * 32 + t * 8 < p.a.c.d) {
-                    const int64_t at = otok[r] * p.a.q_stride + (int64_t)ohead[r] * p.a.c.d + G * 32 + t * 8;
-                    if constexpr (MODE == 0) {
-                        load8<QB_T_F32>(static_cast<const float *>(p.a.q) + at, x[G]);
-                    } else {
-                        const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at;
-                        if (p.a.type == QB_T_F16) load8<QB_T_F16>(q, x[G]); else load8<QB_T_BF16>(q, x[G]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[G][i]));
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
             }
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // the row's largest magnitude into [2^14, 2^15)
             const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 14;
             const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            cs[r] = p.a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + 10) << 23) * exp2f((float)e);
+            // undone in the scores, with the codes' 2^-24 where they stand as subnormals
+            const float back = p.a.scale * 1.4426950408889634f * exp2f((float)(e - 14 + (PAIR ? 0 : 24)));
+#pragma unroll
+            for (int h = 0; h < NH; ++h) cs[n][h] = __shfl_sync(0xFFFFFFFFu, back, PAIR ? 8 * t : 8 * t + 4 * h);
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
-                float hi[8], lo[8], sh = 0.0f, sl = 0.0f;
+                load(G, x);
+                float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float y = x[G][i] * f;
-                    hi[i] = __half2float(__float2half_rn(y));
-                    lo[i] = y - hi[i];
-                    sh += hi[i];
-                    if (MODE == 0) {
-                        lo[i] = __half2float(__float2half_rn(lo[i]));
-                        sl += lo[i];
-                    }
+                    const float y = x[i] * f, hi = __half2float(__float2half_rn(y));
+                    x[i] = PAIR && (g & 1) ? y - hi : hi;
+                    sum += x[i];
                 }
-                sh += __shfl_xor_sync(0xFFFFFFFFu, sh, 1);
-                sh += __shfl_xor_sync(0xFFFFFFFFu, sh, 2);
-                const float c8 = -8.0f / 16777216.0f;
-                if constexpr (MODE == 0) {
-                    sl += __shfl_xor_sync(0xFFFFFFFFu, sl, 1);
-                    sl += __shfl_xor_sync(0xFFFFFFFFu, sl, 2);
-                    cinit[G][0] = c8 * sh;
-                    cinit[G][1] = c8 * sl;
+                if constexpr (PAIR) {
+                    cinit[n][G][0] = 0.0f;
                 } else {
-                    cinit[G][r] = c8 * sh;
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    sum *= -8.0f / 16777216.0f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) cinit[n][G][h] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * h);
                 }
+                // as subnormals, every second code stands as 16 c * 2^-24
+                const float odd = PAIR ? 1.0f : 0.0625f;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    // codes 2m, 2m + 4 stand as c * 2^-24, codes 2m + 1, 2m + 5 as 16 c * 2^-24
-                    const uint32_t a_lo = pack_f16(hi[2 * m], hi[2 * m + 4]);
-                    const uint32_t a_hi = pack_f16(hi[2 * m + 1] * 0.0625f, hi[2 * m + 5] * 0.0625f);
-                    if constexpr (MODE == 0) {
-                        A[G][m][0] = a_lo;
-                        A[G][m][2] = a_hi;
-                        A[G][m][1] = pack_f16(lo[2 * m], lo[2 * m + 4]);
-                        A[G][m][3] = pack_f16(lo[2 * m + 1] * 0.0625f, lo[2 * m + 5] * 0.0625f);
-                    } else if constexpr (MODE == 1) {
-                        A[G][m][0] = a_lo;
-                        A[G][m][1] = a_hi;
-                    } else {
-                        A[G][m][r] = a_lo;
-                        A[G][m][2 + r] = a_hi;
-                    }
+                    B[n][G][m][0] = pack_f16(x[2 * m], x[2 * m + 4]);
+                    B[n][G][m][1] = pack_f16(x[2 * m + 1] * odd, x[2 * m + 5] * odd);
                 }
             }
         }
@@ -445,174 +450,180 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
         const int pos_hi = s_len - s_T + min(s_T - 1, (s_rt * R + R - 1) / p.grp);
         const int first_hi = p.a.window ? max(0, pos_hi - p.a.window + 1) : 0;
 
-        float O[NG][4][NC];
-        float m[NR], l[NR];
+        float O[NT][NG][2][4];
+        float m[NT][NH], l[NT][NH];
         int eb = 1;  // biased exponent (binary16's) of the largest step so far
 #pragma unroll
-        for (int G = 0; G < NG; ++G)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int G = 0; G < NG; ++G)
 #pragma unroll
-                for (int c = 0; c < NC; ++c) O[G][j][c] = 0.0f;
+                for (int i = 0; i < 8; ++i) O[n][G][i / 4][i % 4] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.0f;
+            for (int h = 0; h < NH; ++h) {
+                m[n][h] = -INFINITY;
+                l[n][h] = 0.0f;
+            }
         }
 
-        for (int un = 0; un < units; ++un) {
-            const int k0 = (cur.u0 + cur.u) * kUnit;
-            const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
-            if (!__all_sync(0xFFFFFFFFu, landed)) return;  // a copy never completed: fault word raised
-            const uint8_t *ub = ring + slot * kBytes;
-            const bool masked = k0 + kUnit - 1 > pos_lo || k0 < first_hi;
-
-            // ---- scores of this lane's eight keys
-            float z[4][2 * NR];
+        auto unit = [&](const uint8_t *ub, int k0, auto masked) {
+            // ---- scores: key krow + 16 b + 8 i, this lane's rows
+            float z[NT][2][2][NH];
+            uint32_t vs[2][2][NG / 2];  // the values' steps of the same keys
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const uint8_t *kb = ub + (nt * 8 / SB) * kSub + 0;
-                const int r0 = (nt * 8) % SB;
+            for (int b = 0; b < 2; ++b) {
+                const uint8_t *kb = ub + (b * 16 / SB) * kSub;
+                const int r0 = (b * 16) % SB;
+                uint32_t st[2][NG / 2];
 #pragma unroll
-                for (int i = 0; i < 2 * NR; ++i) z[nt][i] = 0.0f;
-                uint32_t st0[NG / 2], st1[NG / 2];
-                lds<NG / 2>(kb + kCodes + (r0 + key0) * NG * 2, st0);
-                lds<NG / 2>(kb + kCodes + (r0 + key1) * NG * 2, st1);
+                for (int i = 0; i < 2; ++i) {
+                    lds<NG / 2>(kb + kCodes + (r0 + 8 * i + krow) * NG * 2, st[i]);
+                    lds<NG / 2>(kb + 2 * kCodes + kSteps + (r0 + 8 * i + krow) * NG * 2, vs[b][i]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) z[n][b][i][h] = 0.0f;
+                }
 #pragma unroll
                 for (int pl = 0; pl < NP; ++pl) {
-                    uint32_t w[W];
-                    lds<W>(kb + pl * kPlane + r0 * 16 * W + koff, w);
+                    uint32_t w0[W], w1[W];
+                    lds<W>(kb + pl * kPlane + r0 * 16 * W + koff, w0);
+                    lds<W>(kb + pl * kPlane + (r0 + 8) * 16 * W + koff, w1);
 #pragma unroll
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
-                        const uint32_t v = w[gi] >> 8;
-                        float acc[NC];
-                        if constexpr (MODE == 1) {
-                            acc[0] = acc[1] = cinit[G][0];
-                            mma_f16(acc, A[G][0][0], A[G][0][1], w[gi] & 0x000F000Fu, w[gi] & 0x00F000F0u);
-                            mma_f16(acc, A[G][1][0], A[G][1][1], v & 0x000F000Fu, v & 0x00F000F0u);
-                        } else {
-                            acc[0] = acc[1] = cinit[G][0];
-                            acc[2] = acc[3] = cinit[G][1];
-                            mma_f16(acc, A[G][0][0], A[G][0][1], A[G][0][2], A[G][0][3], w[gi] & 0x000F000Fu,
-                                    w[gi] & 0x00F000F0u);
-                            mma_f16(acc, A[G][1][0], A[G][1][1], A[G][1][2], A[G][1][3], v & 0x000F000Fu,
-                                    v & 0x00F000F0u);
+                        float acc[NT][4];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            acc[n][0] = acc[n][2] = cinit[n][G][0];
+                            acc[n][1] = acc[n][3] = cinit[n][G][PAIR ? 0 : 1];
                         }
-                        const float2 d0 = unpack_f16(st0[G / 2]), d1 = unpack_f16(st1[G / 2]);
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm) {
+                            const uint32_t x0 = mm ? w0[gi] >> 8 : w0[gi], x1 = mm ? w1[gi] >> 8 : w1[gi];
+                            uint32_t a0, a1, a2, a3;
+                            if constexpr (PAIR) {
+                                a0 = centre_lo(x0);
+                                a1 = centre_lo(x1);
+                                a2 = centre_hi(x0);
+                                a3 = centre_hi(x1);
+                            } else {
+                                a0 = x0 & 0x000F000Fu;
+                                a1 = x1 & 0x000F000Fu;
+                                a2 = x0 & 0x00F000F0u;
+                                a3 = x1 & 0x00F000F0u;
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_f16(acc[n], a0, a1, a2, a3, B[n][G][mm][0], B[n][G][mm][1]);
+                        }
+                        const float2 d0 = unpack_f16(st[0][G / 2]), d1 = unpack_f16(st[1][G / 2]);
                         const float s0 = (G & 1) ? d0.y : d0.x, s1 = (G & 1) ? d1.y : d1.x;
-                        z[nt][0] = fmaf(s0, acc[0], z[nt][0]);
-                        z[nt][1] = fmaf(s1, acc[1], z[nt][1]);
-                        if constexpr (MODE == 0) {
-                            z[nt][0] = fmaf(s0, acc[2], z[nt][0]);
-                            z[nt][1] = fmaf(s1, acc[3], z[nt][1]);
-                        } else if constexpr (MODE == 2) {
-                            z[nt][2] = fmaf(s0, acc[2], z[nt][2]);
-                            z[nt][3] = fmaf(s1, acc[3], z[nt][3]);
-                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int h = PAIR ? 0 : c;
+                                z[n][b][0][h] = fmaf(s0, acc[n][c], z[n][b][0][h]);
+                                z[n][b][1][h] = fmaf(s1, acc[n][2 + c], z[n][b][1][h]);
+                            }
                     }
                 }
             }
-            // ---- the values' steps; those of keys past the end may hold anything
-            uint32_t vs[4][2][NG / 2];
+            uint32_t seen[NT][NH];  // bit 2 b + i: the row sees that key
+            if constexpr (masked) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const uint8_t *vb = ub + (nt * 8 / SB) * kSub + 2 * kCodes + kSteps;
-                const int r0 = (nt * 8) % SB;
-                lds<NG / 2>(vb + (r0 + key0) * NG * 2, vs[nt][0]);
-                lds<NG / 2>(vb + (r0 + key1) * NG * 2, vs[nt][1]);
-            }
-            uint32_t seen = 0xFFFFFFFFu;  // bit nt * 2 + i (+ 8 r): row r sees key i of eight nt
-            if (masked) {
-                seen = 0;
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+                    for (int i = 0; i < 2; ++i)
+                        if (k0 + 16 * b + 8 * i + krow >= s_len) {  // a place that holds no key may hold anything
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int key = k0 + nt * 8 + (i ? key1 : key0);
-                        if (key >= s_len) {
-#pragma unroll
-                            for (int h = 0; h < NG / 2; ++h) vs[nt][i][h] = 0;
+                            for (int h = 0; h < NG / 2; ++h) vs[b][i][h] = 0;
                         }
 #pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            if (key >= first[r] && key <= pos[r]) seen |= 1u << (nt * 2 + i + 8 * r);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        const int j = (s_rt * R + n * RT + (PAIR ? t : 2 * t + h)) / p.grp;
+                        const int pos = j < s_T ? s_len - s_T + j : -1;
+                        const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
+                        seen[n][h] = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = k0 + 8 * k + krow;
+                            if (key >= first && key <= pos) seen[n][h] |= 1u << k;
+                        }
                     }
             }
+            // ---- the running maximum and the steps' largest exponent; both rarely move
             __half2 top2 = __float2half2_rn(0.0f);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < NG / 2; ++h)
-                        top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&vs[nt][i][h])));
+                for (int h = 0; h < NG / 2; ++h)
+                    top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&vs[k >> 1][k & 1][h])));
             top2 = __hmax2(top2, __lowhigh2highlow(top2));
             uint32_t tb = *reinterpret_cast<const uint32_t *>(&top2) & 0xFFFFu;
-            tb = max(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, 1));
-            tb = max(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, 2));
-            const int eb_new = max(eb, (int)(tb >> 10));
-
-            // ---- running maximum
-            float m_new[NR];
-            bool moved = eb_new != eb;
+            bool moved = (int)(tb >> 10) > eb;
+            float top[NT][NH];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float top = m[r];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+                for (int h = 0; h < NH; ++h) {
+                    top[n][h] = m[n][h];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float y = z[nt][2 * r + i] * cs[r];
-                        if (!(seen >> (nt * 2 + i + 8 * r) & 1)) y = -INFINITY;
-                        z[nt][2 * r + i] = y;
-                        top = fmaxf(top, y);
+                    for (int k = 0; k < 4; ++k) {
+                        float y = z[n][k >> 1][k & 1][h] * cs[n][h];
+                        if constexpr (masked) {
+                            if (!(seen[n][h] >> k & 1)) y = -INFINITY;
+                        }
+                        z[n][k >> 1][k & 1][h] = y;
+                        top[n][h] = fmaxf(top[n][h], y);
                     }
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                m_new[r] = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                moved |= m_new[r] != m[r];
-            }
+                    moved |= top[n][h] > m[n][h];
+                }
             if (__any_sync(0xFFFFFFFFu, moved)) {
-                const float fe = __uint_as_float((uint32_t)(127 + eb - eb_new) << 23);
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float al = m_new[r] == m[r] ? 1.0f : ex2(m[r] - m_new[r]);
-                    l[r] *= al;
-                    const float f = al * fe;
-                    m[r] = m_new[r];
+                for (int o = 4; o <= 16; o <<= 1) tb = max(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, o));
+                const int eb_new = max(eb, (int)(tb >> 10));
+                const float fe = __uint_as_float((uint32_t)(127 + eb - eb_new) << 23);
+                eb = eb_new;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float f[NH];
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1)
+                            top[n][h] = fmaxf(top[n][h], __shfl_xor_sync(0xFFFFFFFFu, top[n][h], o));
+                        f[h] = top[n][h] == m[n][h] ? 1.0f : ex2(m[n][h] - top[n][h]);
+                        l[n][h] *= f[h];
+                        f[h] *= fe;
+                        m[n][h] = top[n][h];
+                    }
 #pragma unroll
                     for (int G = 0; G < NG; ++G)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            O[G][j][2 * r] *= f;
-                            O[G][j][2 * r + 1] *= f;
-                            if constexpr (MODE == 0) {
-                                O[G][j][2] *= f;
-                                O[G][j][3] *= f;
-                            }
-                        }
+                        for (int i = 0; i < 8; ++i) O[n][G][i / 4][i % 4] *= f[PAIR ? 0 : i & 1];
                 }
-                eb = eb_new;
             }
             const float pe = __uint_as_float((uint32_t)(127 + 28 - eb) << 23);  // |step| * pe < 2^14
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float mm = m[r] == -INFINITY ? 0.0f : m[r];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+                for (int h = 0; h < NH; ++h) {
+                    const float mm = m[n][h] == -INFINITY ? 0.0f : m[n][h];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float e = ex2(z[nt][2 * r + i] - mm);
-                        l[r] += e;
-                        z[nt][2 * r + i] = e * pe;
+                    for (int k = 0; k < 4; ++k) {
+                        const float e = ex2(z[n][k >> 1][k & 1][h] - mm);
+                        l[n][h] += e;
+                        z[n][k >> 1][k & 1][h] = e * pe;
                     }
-            }
+                }
 
-            // ---- probabilities times steps, times the values' codes
+            // ---- the values' codes times probabilities times steps
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const uint8_t *va = ub + (kk * 16 / SB) * kSub + ((kk * 16) % SB) * 16 * W;
-                const uint8_t *vb = va + 8 * 16 * W;
+            for (int b = 0; b < 2; ++b) {
+                const uint8_t *va = ub + (b * 16 / SB) * kSub + ((b * 16) % SB) * 16 * W, *vb = va + 8 * 16 * W;
 #pragma unroll
                 for (int pl = 0; pl < NP; ++pl) {
                     uint32_t c00[W / 2], c01[W / 2], c10[W / 2], c11[W / 2];
@@ -623,113 +634,112 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
 #pragma unroll
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
-                        uint32_t ah[NR][2], al[2];
+                        uint32_t x[NT][2];
 #pragma unroll
-                        for (int r = 0; r < NR; ++r)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int nt = 2 * kk + h;
-                                const float2 d0 = unpack_f16(vs[nt][0][G / 2]), d1 = unpack_f16(vs[nt][1][G / 2]);
-                                float x0 = z[nt][2 * r] * ((G & 1) ? d0.y : d0.x);
-                                float x1 = z[nt][2 * r + 1] * ((G & 1) ? d1.y : d1.x);
-                                if (masked) {  // a key that the row does not see may hold a step that is not finite
-                                    if (!(seen >> (nt * 2 + 8 * r) & 1)) x0 = 0.0f;
-                                    if (!(seen >> (nt * 2 + 1 + 8 * r) & 1)) x1 = 0.0f;
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 d2 = unpack_f16(vs[b][i][G / 2]);
+                                const float d = (G & 1) ? d2.y : d2.x;
+                                float x0 = z[n][b][i][0] * d, x1 = PAIR ? 0.0f : z[n][b][i][NH - 1] * d;
+                                if constexpr (masked) {  // a key that the row does not see may hold a step that is not finite
+                                    if (!(seen[n][0] >> (2 * b + i) & 1)) x0 = 0.0f;
+                                    if (!(seen[n][NH - 1] >> (2 * b + i) & 1)) x1 = 0.0f;
                                 }
-                                ah[r][h] = pack_f16(x0, x1);
-                                if (MODE == 0) {
-                                    const float2 b = unpack_f16(ah[r][h]);
-                                    al[h] = pack_f16(x0 - b.x, x1 - b.y);
+                                if constexpr (PAIR) {
+                                    const float hi = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);  // f16's 11 bits
+                                    x1 = x0 - hi;
+                                    x0 = hi;
                                 }
+                                x[n][i] = transpose8(pack_f16(x0, x1));
                             }
-                        uint32_t y0 = __byte_perm(c00[gi / 2], c01[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
-                        uint32_t y1 = __byte_perm(c10[gi / 2], c11[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
+                        const uint32_t y0 = __byte_perm(c00[gi / 2], c01[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
+                        const uint32_t y1 = __byte_perm(c10[gi / 2], c11[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t mask = (j & 1) ? 0x00F000F0u : 0x000F000Fu;
-                            uint32_t b0 = (y0 & mask) | 0x64006400u, b1 = (y1 & mask) | 0x64006400u;
-                            __half2 &h0 = *reinterpret_cast<__half2 *>(&b0), &h1 = *reinterpret_cast<__half2 *>(&b1);
-                            if (j & 1) {  // 1024 + 16 c
-                                const __half2 k16 = __float2half2_rn(0.0625f), k72 = __float2half2_rn(-72.0f);
-                                h0 = __hfma2(h0, k16, k72);
-                                h1 = __hfma2(h1, k16, k72);
-                            } else {
-                                const __half2 k1032 = __float2half2_rn(-1032.0f);
-                                h0 = __hadd2(h0, k1032);
-                                h1 = __hadd2(h1, k1032);
-                            }
-                            if constexpr (MODE == 0)
-                                mma_f16(O[G][j], ah[0][0], al[0], ah[0][1], al[1], b0, b1);
-                            else if constexpr (MODE == 1)
-                                mma_f16(O[G][j], ah[0][0], ah[0][1], b0, b1);
-                            else
-                                mma_f16(O[G][j], ah[0][0], ah[1][0], ah[0][1], ah[1][1], b0, b1);
-                            if (j & 1) {
-                                y0 >>= 8;
-                                y1 >>= 8;
-                            }
+                        for (int mm = 0; mm < 2; ++mm) {
+                            const uint32_t v0 = mm ? y0 >> 8 : y0, v1 = mm ? y1 >> 8 : y1;
+                            const uint32_t a0 = centre_lo(v0), a1 = centre_hi(v0), a2 = centre_lo(v1), a3 = centre_hi(v1);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_f16(O[n][G][mm], a0, a1, a2, a3, x[n][0], x[n][1]);
                         }
                     }
                 }
             }
+        };
+
+        for (int u = cur.u; u < cur.u + units; ++u) {
+            const int k0 = u * kUnit;
+            const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
+            if (!__all_sync(0xFFFFFFFFu, landed)) return;  // a copy never completed: fault word raised
+            const uint8_t *ub = ring + slot * kBytes;
+            if (k0 + kUnit - 1 > pos_lo || k0 < first_hi)
+                unit(ub, k0, std::true_type());
+            else
+                unit(ub, k0, std::false_type());
             __syncwarp();  // every lane has read the slot
             issue();
             slot = slot + 1 == kStages ? 0 : slot + 1;
             phase ^= slot == 0 ? 1u : 0u;
-            step_next<R>(p, cur, lane);
         }
 
         // ---- the item's rows: out, or this piece's sums
+        const bool whole = from_start && to_end;
+        const float fo = __uint_as_float((uint32_t)(127 - 28 + eb) << 23);  // undoes pe
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            float sum = l[r];
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            const bool whole = from_start && to_end;
-            const float fo = __uint_as_float((uint32_t)(127 - 28 + eb) << 23);  // undoes pe
-            const float f = !whole ? fo : sum == 0.0f ? 0.0f : fo / sum;
-            const int64_t rec = ((int64_t)(worker * 2 + (from_start ? 1 : 0)) * kMaxRows + g + 8 * r);
-            if (live[r]) {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                float sum = l[n][h];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                const float f = !whole ? fo : sum == 0.0f ? 0.0f : fo / sum;
+                const int row = n * RT + (PAIR ? t : 2 * t + h), rho = s_rt * R + row, j = rho / p.grp;
+                if (j >= s_T) continue;
+                const int64_t tok = s_q0 + j;
+                const int head = s_kvh * p.grp + rho - j * p.grp;
+                const int64_t rec = (int64_t)(worker * 2 + (from_start ? 1 : 0)) * R + row;
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
-                    float x[8];
+                    float x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a = O[G][j][2 * r], b = O[G][j][2 * r + 1];
-                        if constexpr (MODE == 0) {
-                            a += O[G][j][2];
-                            b += O[G][j][3];
-                        }
-                        x[j] = a * f;
-                        x[4 + j] = b * f;
+                    for (int i = 0; i < 4; ++i) {
+                        const float (&o)[4] = O[n][G][i / 2];
+                        const int c = (i & 1) * 2;
+                        x[i] = (PAIR ? o[c] + o[c + 1] : o[c + h]) * f;
                     }
-                    const int el = G * 32 + t * 8;
+                    const int el = G * 32 + g * 4;
                     if (!whole) {
-                        store8<QB_T_F32>(p.part + rec * DP + el, x);
+                        *reinterpret_cast<float4 *>(p.part + rec * DP + el) = make_float4(x[0], x[1], x[2], x[3]);
                     } else if (el < p.a.c.d) {
-                        const int64_t at = otok[r] * p.a.out_stride + (int64_t)ohead[r] * p.a.c.d + el;
-                        if constexpr (MODE == 0) {
-                            store8<QB_T_F32>(static_cast<float *>(p.a.out) + at, x);
+                        const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d + el;
+                        if (PAIR && p.a.type == QB_T_F32) {
+                            *reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
                         } else {
-                            uint16_t *o = static_cast<uint16_t *>(p.a.out) + at;
-                            if (p.a.type == QB_T_F16) store8<QB_T_F16>(o, x); else store8<QB_T_BF16>(o, x);
+                            uint2 u;
+                            if (p.a.type == QB_T_F16) {
+                                u = make_uint2(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
+                            } else {
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+                                u = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                            }
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = u;
                         }
                     }
                 }
-                if (t == 0) {
+                if (g == 0) {
                     if (!whole)
-                        p.stat[rec] = make_float2(m[r], sum);
+                        p.stat[rec] = make_float2(m[n][h], sum);
                     else if (p.a.lse)
-                        p.a.lse[otok[r] * p.a.nh + ohead[r]] = (m[r] + log2f(sum)) * 0.6931471805599453f;
+                        p.a.lse[tok * p.a.nh + head] = (m[n][h] + log2f(sum)) * 0.6931471805599453f;
                 }
             }
-        }
         if (from_start && !to_end && lane == 0) {
-            const long long item_end = end - left + item_left;  // in units of the whole work
-            p.meta[worker * 2] = make_int4((int)((item_end - 1) / share), s_q0, s_T, s_kvh);
+            const int last_unit = count - left + item_left - 1;  // of the item, from this worker's first on
+            p.meta[worker * 2] = make_int4(worker + (int)(last_unit / share), s_q0, s_T, s_kvh);
             p.meta[worker * 2 + 1] = make_int4(s_rt, 0, 0, 0);
         }
         left -= p.nosplit ? 1 : units;
+        if (to_end) step_item<R>(p, tab, base, cur); else cur.u += units;
     }
 }
 
@@ -740,7 +750,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 1) kv4_step_kernel(const Step
 template <int DP, int R>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p) {
     constexpr int E = DP / 32;
-    __shared__ int items[256 * 8];
+    __shared__ int items[kMaxWorkers];
     __shared__ int nitems, warp_n[8];
     __shared__ float red[8][DP], red_l[8];
     pdl_launch_dependents();
@@ -771,7 +781,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p) {
         const int rho = b.x * R + row, j = rho / p.grp;
         if (j >= a.z) continue;  // the same for every thread of the block's task
         const int parts = a.x - w0 + 1;
-        auto rec = [&](int k) { return (int64_t)((w0 + k) * 2 + (k == 0 ? 1 : 0)) * kMaxRows + row; };
+        auto rec = [&](int k) { return (int64_t)((w0 + k) * 2 + (k == 0 ? 1 : 0)) * R + row; };
         float m = -INFINITY;
         for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.stat[rec(k)].x);
 #pragma unroll
@@ -833,20 +843,25 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p) {
 // an item of at most this many keys is not split (and no join is launched)
 constexpr int kNoSplitKeys = 256;
 
-template <int DP, int MODE, int SB>
+template <int DP, bool PAIR, int NT, int SB>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
-    constexpr int smem = kStepWarps * step_stages<DP>() * step_unit_bytes<DP>();
-    auto *f = kv4_step_kernel<DP, MODE, SB>;
+    constexpr int kWarps = step_warps(DP, PAIR, NT), R = step_rows(PAIR, NT);
+    constexpr int smem = kWarps * step_stages(DP, PAIR, NT) * step_unit_bytes(DP);
+    p.nworkers = grid * kWarps;
+    p.part = reinterpret_cast<float *>(p.a.ws);
+    p.stat = reinterpret_cast<float2 *>(p.part + (int64_t)p.nworkers * 2 * R * DP);
+    p.meta = reinterpret_cast<int4 *>(p.stat + (int64_t)p.nworkers * 2 * R);
+    auto *f = kv4_step_kernel<DP, PAIR, NT, SB>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
-    if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kStepWarps * 32), smem, stream, p)) return rc;
+    if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p)) return rc;
     if (p.nosplit) return QB_OK;
-    return launch_pdl(kv4_combine_kernel<DP, step_rows<MODE>()>, dim3((unsigned)grid), dim3(256), 0, stream, p);
+    return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p);
 }
 
-template <int DP, int MODE>
+template <int DP, bool PAIR, int NT>
 static int launch_step_m(StepK &p, int grid, cudaStream_t stream) {
-    return p.a.c.page == 16 ? launch_step_k<DP, MODE, 16>(p, grid, stream)
-                            : launch_step_k<DP, MODE, 32>(p, grid, stream);
+    return p.a.c.page == 16 ? launch_step_k<DP, PAIR, NT, 16>(p, grid, stream)
+                            : launch_step_k<DP, PAIR, NT, 32>(p, grid, stream);
 }
 
 template <int DP>
@@ -854,17 +869,15 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     StepK p = {};
     p.a = a;
     p.grp = a.nh / a.c.nkv;
-    const int grid = std::min(num_sms(), 256);
-    p.nworkers = grid * kStepWarps;
+    const int grid = step_grid();
     p.min_share = 4;
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
-    p.part = reinterpret_cast<float *>(a.ws);
-    p.stat = reinterpret_cast<float2 *>(p.part + (int64_t)p.nworkers * 2 * kMaxRows * DP);
-    p.meta = reinterpret_cast<int4 *>(p.stat + (int64_t)p.nworkers * 2 * kMaxRows);
-    if (a.type == QB_T_F32) return launch_step_m<DP, 0>(p, grid, stream);
-    // rows a sequence and key head, on average
-    if (a.ntok * p.grp <= (int64_t)8 * a.s.nseq) return launch_step_m<DP, 1>(p, grid, stream);
-    return launch_step_m<DP, 2>(p, grid, stream);
+    // rows a sequence and key head, on average: pairs where they fit one column
+    // tile (and for f32 always), two column tiles where one does not hold them
+    const int64_t rows = a.ntok * p.grp, n = a.s.nseq;
+    if (rows <= 4 * n) return launch_step_m<DP, true, 1>(p, grid, stream);
+    if (a.type == QB_T_F32) return launch_step_m<DP, true, 2>(p, grid, stream);
+    return rows <= 8 * n ? launch_step_m<DP, false, 1>(p, grid, stream) : launch_step_m<DP, false, 2>(p, grid, stream);
 }
 
 int launch_kv4_step_64(const Kv4AttnArgs &a, cudaStream_t stream);
