@@ -83,30 +83,49 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// c = a b + d
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, float d0, float d1, float d2, float d3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(d0), "f"(d1), "f"(d2), "f"(d3));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    mma_f16(c, a0, a1, a2, a3, b0, b1, c[0], c[1], c[2], c[3]);
 }
 // An 8 x 8 matrix of f16, a row's two neighbours a lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
-// Codes in the low (or second) four bits of each half, as code - 8.
-__device__ __forceinline__ uint32_t centre_lo(uint32_t w) {
-    uint32_t b = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + c
+// Codes in the low (or second) four bits of each half, as code - 8.  The three
+// constants stay in registers (opaque to the compiler), so that mask and OR are
+// one three-input operation.
+struct CentreK {
+    uint32_t lo, hi, one;
+    __device__ __forceinline__ CentreK() {
+        asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
+        asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(one));  // 1024, twice
+    }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t centre_lo(const CentreK &k, uint32_t w) {
+    uint32_t b = and_or(w, k.lo, k.one);  // 1024 + c
     __half2 &h = *reinterpret_cast<__half2 *>(&b);
     h = __hadd2(h, __float2half2_rn(-1032.0f));
     return b;
 }
-__device__ __forceinline__ uint32_t centre_hi(uint32_t w) {
-    uint32_t b = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 c
+__device__ __forceinline__ uint32_t centre_hi(const CentreK &k, uint32_t w) {
+    uint32_t b = and_or(w, k.hi, k.one);  // 1024 + 16 c
     __half2 &h = *reinterpret_cast<__half2 *>(&b);
     h = __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
     return b;
@@ -366,6 +385,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     const int voff0 = kCodes + kSteps + t * 16 * W + ((g ^ (4 * (t >> 1))) * 2 * W);
     const int voff1 = kCodes + kSteps + (7 - t) * 16 * W + ((g ^ (4 * (1 - (t >> 1)))) * 2 * W);
 
+    const CentreK ck;
     int left = count;
     int slot = 0;
     uint32_t phase = 0;
@@ -494,19 +514,14 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                         const int G = pl * W + gi;
                         float acc[NT][4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            acc[n][0] = acc[n][2] = cinit[n][G][0];
-                            acc[n][1] = acc[n][3] = cinit[n][G][PAIR ? 0 : 1];
-                        }
-#pragma unroll
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t x0 = mm ? w0[gi] >> 8 : w0[gi], x1 = mm ? w1[gi] >> 8 : w1[gi];
                             uint32_t a0, a1, a2, a3;
                             if constexpr (PAIR) {
-                                a0 = centre_lo(x0);
-                                a1 = centre_lo(x1);
-                                a2 = centre_hi(x0);
-                                a3 = centre_hi(x1);
+                                a0 = centre_lo(ck, x0);
+                                a1 = centre_lo(ck, x1);
+                                a2 = centre_hi(ck, x0);
+                                a3 = centre_hi(ck, x1);
                             } else {
                                 a0 = x0 & 0x000F000Fu;
                                 a1 = x1 & 0x000F000Fu;
@@ -514,7 +529,14 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                                 a3 = x1 & 0x00F000F0u;
                             }
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(acc[n], a0, a1, a2, a3, B[n][G][mm][0], B[n][G][mm][1]);
+                            for (int n = 0; n < NT; ++n) {
+                                if (mm == 0) {
+                                    const float c0 = PAIR ? 0.0f : cinit[n][G][0], c1 = PAIR ? 0.0f : cinit[n][G][PAIR ? 0 : 1];
+                                    mma_f16(acc[n], a0, a1, a2, a3, B[n][G][0][0], B[n][G][0][1], c0, c1, c0, c1);
+                                } else {
+                                    mma_f16(acc[n], a0, a1, a2, a3, B[n][G][1][0], B[n][G][1][1]);
+                                }
+                            }
                         }
                         const float2 d0 = unpack_f16(st[0][G / 2]), d1 = unpack_f16(st[1][G / 2]);
                         const float s0 = (G & 1) ? d0.y : d0.x, s1 = (G & 1) ? d1.y : d1.x;
@@ -658,7 +680,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 #pragma unroll
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t v0 = mm ? y0 >> 8 : y0, v1 = mm ? y1 >> 8 : y1;
-                            const uint32_t a0 = centre_lo(v0), a1 = centre_hi(v0), a2 = centre_lo(v1), a3 = centre_hi(v1);
+                            const uint32_t a0 = centre_lo(ck, v0), a1 = centre_hi(ck, v0), a2 = centre_lo(ck, v1), a3 = centre_hi(ck, v1);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) mma_f16(O[n][G][mm], a0, a1, a2, a3, x[n][0], x[n][1]);
                         }
