@@ -12,10 +12,8 @@ int64_t kv4_attn_ws(int nkv, int dp, int nh) {
     (void)nh;
     int64_t most = 0;
     for (int nt = 1; nt <= 2; ++nt)
-        for (int pair = 0; pair < 2; ++pair) {
-            const int64_t workers = (int64_t)step_grid() * step_warps(dp, pair != 0, nt), rows = step_rows(pair != 0, nt);
-            most = std::max(most, workers * 2 * (rows * (4 * dp + 8) + 16));
-        }
+        for (int pair = 0; pair < 2; ++pair)
+            most = std::max(most, step_ws(step_grid(), step_warps(dp, pair != 0, nt), step_rows(pair != 0, nt), dp).end);
     return most;
 }
 

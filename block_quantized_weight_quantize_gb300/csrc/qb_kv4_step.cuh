@@ -30,11 +30,12 @@
 // 7 - t), which keeps both loads free of bank conflicts.
 //
 // Work.  Units of 32 keys of one (sequence, key head, row tile), counted along
-// the whole batch; every warp takes the same number of consecutive units
-// whatever the sequences' lengths are, and streams them through its own ring of
-// bulk copies (a page's block of a head is contiguous), so warps never wait for
-// one another.  A piece of an item that its warp does not hold whole leaves its
-// sums in the workspace, joined by kv4_combine_kernel in the order of the keys.
+// the whole batch; every block takes the same number of consecutive units
+// whatever the sequences' lengths are, its warps the same number of those, and
+// each warp streams its own through a ring of bulk copies (a page's block of a
+// head is contiguous), so warps do not wait for one another until the end.  Then
+// the block joins the pieces of the items that its warps share; an item that
+// blocks share is joined by kv4_combine_kernel, in the order of the keys.
 #pragma once
 
 #include <algorithm>
@@ -57,24 +58,42 @@ __host__ __device__ constexpr int step_rows(bool pair, int nt) { return (pair ? 
 __host__ __device__ constexpr int step_warps(int dp, bool pair, int nt) {
     return dp * nt > 128 ? 8 : pair && nt == 1 ? 16 : 12;
 }
+// Units a warp's ring holds: what the 227 KB a block may have leave beside its tables (2072 bytes, 548 a warp, 8 a unit).
 __host__ __device__ constexpr int step_stages(int dp, bool pair, int nt) {
-    const int n = 221184 / (step_warps(dp, pair, nt) * step_unit_bytes(dp));
+    const int w = step_warps(dp, pair, nt), n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp) + 8));
     return n > 8 ? 8 : n;
 }
 
-constexpr int kMaxGrid = 256, kMaxWorkers = kMaxGrid * 16;
+constexpr int kMaxGrid = 256;
 inline int step_grid() { return std::min(num_sms(), kMaxGrid); }
+
+// Byte offsets of the workspace's parts.
+struct StepWs {
+    int64_t part, stat, cpart, cstat, meta, last, end;
+};
+inline StepWs step_ws(int64_t grid, int64_t warps, int64_t rows, int64_t dp) {
+    StepWs w;
+    w.part = 0;
+    w.cpart = w.part + grid * warps * 2 * rows * dp * 4;
+    w.stat = w.cpart + grid * 2 * rows * dp * 4;
+    w.cstat = w.stat + grid * warps * 2 * rows * 8;
+    w.meta = w.cstat + grid * 2 * rows * 8;
+    w.last = w.meta + grid * 16;
+    w.end = (w.last + grid * 4 + 15) / 16 * 16;
+    return w;
+}
 
 struct StepK {
     Kv4AttnArgs a;
     int grp;          // query heads a key head
-    int nosplit;      // a worker's share is whole items
-    int nworkers;
-    int min_share;    // units
-    float *part;      // [nworkers][2][rows][DP]
-    float2 *stat;     // [nworkers][2][rows] running maximum, sum
-    int4 *meta;       // [nworkers][2] of the item that starts at a worker and goes on: the last worker that
-                      // holds a piece of it (-1: no such item), first token, tokens, key head; row tile
+    int nosplit;      // a block's share is whole items
+    int min_share;    // units a block
+    float *part;      // [grid][warps][2][rows][DP]: a warp's pieces (0: of an item begun before it)
+    float2 *stat;     // [grid][warps][2][rows] running maximum, sum
+    float *cpart;     // [grid][2][rows][DP]: a block's pieces, joined
+    float2 *cstat;
+    int *last;        // [grid] the last block that holds a piece of the item that starts here and goes on; -1: none
+    int4 *meta;       // [grid] that item's first token, tokens, key head, row tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -224,6 +243,23 @@ __device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, in
     step_enter(p, tab, base, x);
 }
 
+// A joined row: E elements a lane from el on, over the sum, to (tok, head); lane 0 its lse.
+template <int E>
+__device__ __forceinline__ void step_store(const StepK &p, const float (&acc)[E], int el, float sum, float m, int tok,
+                                           int head, int lane) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = (int64_t)tok * p.a.out_stride + (int64_t)head * p.a.c.d + el;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (el + e >= p.a.c.d) break;
+        const float y = acc[e] * inv;
+        if (p.a.type == QB_T_F32) static_cast<float *>(p.a.out)[at + e] = y;
+        else if (p.a.type == QB_T_F16) static_cast<__half *>(p.a.out)[at + e] = __float2half_rn(y);
+        else static_cast<__nv_bfloat16 *>(p.a.out)[at + e] = __float2bfloat16_rn(y);
+    }
+    if (lane == 0 && p.a.lse) p.a.lse[(int64_t)tok * p.a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
+}
+
 template <int DP, bool PAIR, int NT, int SB>
 __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_kernel(const StepK p) {
     constexpr int kWarps = step_warps(DP, PAIR, NT), kStages = step_stages(DP, PAIR, NT), kBytes = step_unit_bytes(DP);
@@ -231,16 +267,23 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;         // groups, groups a plane, planes
     constexpr int kSub = kv4_block(SB, DP);                               // a sub-block of SB rows in shared memory
     constexpr int kCodes = SB * DP / 2, kSteps = SB * DP / 16, kPlane = SB * 16 * W;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bars[kWarps][kStages];
     __shared__ long long chunk_sum[8192 / kSeqChunk + 1];
     __shared__ SeqInfo tabs[kWarps][32];  // a warp's sequences, from its first one's chunk on
+    __shared__ int4 piece[kWarps][2];     // a warp's pieces: first token, tokens (0: none), key head, row tile
+    __shared__ int piece_ends[kWarps];    // its piece of an item begun before it ends that item
+    __shared__ int failed, item_last;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t *ring = smem + warp * kStages * kBytes;
     uint64_t *full = full_bars[warp];
-    if (lane < kStages) mbar_init(full + lane, 1);
+    // the pieces that a unit is copied in, a lane each
+    const int pieces = p.a.c.page == 64 ? 2 * (NP + 1) : kUnit / SB;
+    if (lane < kStages) mbar_init(full + lane, pieces);
     fence_mbar_init();
+    if (lane < 2) piece[warp][lane] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) failed = 0;
     __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
@@ -251,7 +294,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const SeqInfo q = seq_info(p.a, c * kSeqChunk + lane, blockIdx.x == 0);
         int u0, nu;
         seq_units(q, p.a.window, u0, nu);
-        long long n = (long long)p.a.c.nkv * ((q.T * p.grp + R - 1) / R) * (p.nosplit ? 1 : nu);
+        long long n = (long long)p.a.c.nkv * ((q.T * p.grp + R - 1) / R) * nu;
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
         if (lane == 0) chunk_sum[c] = n;
@@ -270,31 +313,29 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         __syncthreads();
     }
     const long long total = nchunks > 1 ? chunk_sum[nchunks] : chunk_sum[0];
-    // workers in the order of the units: neighbours are on different multiprocessors
-    const int worker = warp * gridDim.x + blockIdx.x;
-    long long share = (total + p.nworkers - 1) / p.nworkers;
-    if (!p.nosplit && share < p.min_share) share = p.min_share;
-    const long long begin = worker * share, end = min(begin + share, total);
-    if (lane == 0 && !p.nosplit) p.meta[worker * 2].x = -1;
-    if (begin >= end) return;
-
-    const int count = (int)(end - begin);  // units (items) of this worker
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < p.min_share) share = p.min_share;
     SeqInfo *tab = tabs[warp];
-    int base;
-    StepPos cur;
-    {
-        int lo = 0, hi = nchunks;  // the chunk that holds unit `begin`
+    int base = 0;
+    // Finds unit x: its sequence, the item in it and the unit's place in the item.
+    struct Found {
+        int s, nrt, item, u;
+    };
+    auto find = [&](long long x) {
+        int lo = 0, hi = nchunks;  // the chunk that holds it
         while (hi - lo > 1) {
             const int m = (lo + hi) / 2;
-            if (chunk_sum[m] <= begin) lo = m; else hi = m;
+            if (chunk_sum[m] <= x) lo = m; else hi = m;
         }
         base = lo * kSeqChunk;
         const SeqInfo q = seq_info(p.a, base + lane, false);
+        __syncwarp();
         tab[lane] = q;
+        __syncwarp();
         int u0, nu;
         seq_units(q, p.a.window, u0, nu);
         const int nrt = (q.T * p.grp + R - 1) / R;
-        const long long n = (long long)p.a.c.nkv * nrt * (p.nosplit ? 1 : nu);
+        const long long n = (long long)p.a.c.nkv * nrt * nu;
         long long sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -302,75 +343,84 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             if (lane >= o) sum += y;
         }
         const long long before = (nchunks > 1 ? chunk_sum[lo] : 0) + sum - n;
-        // the last lane with units that starts at or before `begin`
-        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= begin);
+        // the last lane with units that starts at or before x
+        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= x);
         const int l = 31 - __clz(ok);
-        const long long rem = begin - __shfl_sync(0xFFFFFFFFu, before, l);
-        const int l_nu = __shfl_sync(0xFFFFFFFFu, nu, l), l_nrt = __shfl_sync(0xFFFFFFFFu, nrt, l);
-        cur.s = base + l;
-        const long long it = p.nosplit ? rem : rem / l_nu;
-        cur.kvh = (int)(it / l_nrt);
-        cur.rt = (int)(it - (long long)cur.kvh * l_nrt);
-        __syncwarp();
+        const long long rem = x - __shfl_sync(0xFFFFFFFFu, before, l);
+        const int l_nu = __shfl_sync(0xFFFFFFFFu, nu, l);
+        Found f;
+        f.s = base + l;
+        f.nrt = __shfl_sync(0xFFFFFFFFu, nrt, l);
+        f.item = rem >> 32 ? (int)(rem / l_nu) : (int)((uint32_t)rem / (uint32_t)l_nu);
+        f.u = (int)(rem - (long long)f.item * l_nu);
+        return f;
+    };
+    // the block's units; where items are not split, from an item's beginning to one
+    long long b0 = min(blockIdx.x * share, total), b1 = min(b0 + share, total);
+    if (p.nosplit) {
+        if (b1 < total) b1 -= find(b1).u;
+        if (b0 < total) b0 -= find(b0).u;
+    }
+    // the warp's
+    const int wshare = (int)((b1 - b0 + kWarps - 1) / kWarps);
+    const int count = max(0, (int)min((long long)wshare, b1 - b0 - (long long)warp * wshare));
+    StepPos cur = {};
+    if (count > 0) {
+        const Found f = find(b0 + (long long)warp * wshare);
+        cur.s = f.s;
+        cur.kvh = f.item / f.nrt;
+        cur.rt = f.item - cur.kvh * f.nrt;
         step_enter(p, tab, base, cur);
-        if (!p.nosplit) cur.u += (int)(rem - it * l_nu);
+        cur.u += f.u;
     }
 
     // ---- the copies, kStages units ahead.  A lane has one piece of a unit:
     // a page (16 or 32 tokens a page), or a part of half a page (64)
-    int sub = 0, src_off = 0, half_mul = 0, dst_off = 0, nbytes = 0;
+    int sub_key = 0, half_mul = 0, dst_off = 0, nbytes = 0;
+    const uint8_t *src = p.a.c.data;
     if (p.a.c.page == 64) {
         constexpr int kC64 = 64 * DP / 2, kS64 = 64 * DP / 16, kP64 = 64 * 16 * W;
-        const int piece = lane % (NP + 1), side = lane / (NP + 1);
+        const int part = lane % (NP + 1), side = lane / (NP + 1);
         if (lane < 2 * (NP + 1)) {
-            const bool steps = piece == NP;
+            const bool steps = part == NP;
             nbytes = steps ? kSteps : kPlane;
-            src_off = side * (kC64 + kS64) + (steps ? kC64 : piece * kP64);
+            src += side * (kC64 + kS64) + (steps ? kC64 : part * kP64);
             half_mul = steps ? kS64 / 2 : kP64 / 2;
-            dst_off = side * (kCodes + kSteps) + (steps ? kCodes : piece * kPlane);
+            dst_off = side * (kCodes + kSteps) + (steps ? kCodes : part * kPlane);
         }
     } else if (lane < kUnit / SB) {
-        sub = lane;
+        sub_key = lane * SB;
         nbytes = kSub;
         dst_off = lane * kSub;
     }
     StepPos ahead = cur;
     int left_ahead = count;
-    int pg = -1;  // this lane's page of the unit at `ahead`; below zero: none
+    int pg = 0;  // this lane's page of the unit at `ahead`
     auto find_page = [&]() {
-        pg = -1;
-        if (left_ahead > 0 && nbytes) {
-            const int pi = p.a.c.page == 64 ? ahead.u >> 1 : p.a.c.page == 32 ? ahead.u : 2 * ahead.u + sub;
-            if ((p.a.c.page == 64 ? ahead.u * kUnit : pi * p.a.c.page) < ahead.len) {
-                pg = p.a.s.tables[(int64_t)ahead.row * p.a.s.maxp + pi];
-                if ((uint32_t)pg >= (uint32_t)p.a.c.npages) pg = INT_MAX;  // reported when its copy is due
-            }
-        }
+        const int key = ahead.u * kUnit + sub_key;
+        if (left_ahead > 0 && nbytes && key < ahead.len)
+            pg = p.a.s.tables[(int64_t)ahead.row * p.a.s.maxp + (key >> p.a.c.pshift)];
     };
     int islot = 0;
     auto issue = [&]() {
         if (left_ahead > 0) {
-            if (pg == INT_MAX) {
-                atomicOr(p.a.fault, kFaultIndex);
-                pg = 0;
+            if (nbytes) {  // each lane announces and issues its own piece
+                if (ahead.u * kUnit + sub_key < ahead.len) {
+                    if ((uint32_t)pg >= (uint32_t)p.a.c.npages) {
+                        atomicOr(p.a.fault, kFaultIndex);
+                        pg = 0;
+                    }
+                    mbar_arrive_expect_tx(full + islot, (uint32_t)nbytes);
+                    bulk_g2s(ring + islot * kBytes + dst_off,
+                             src + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes +
+                                 ((ahead.u & 1) ? half_mul : 0),
+                             (uint32_t)nbytes, full + islot);
+                } else {
+                    mbar_arrive(full + islot);
+                }
             }
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
-            // half a page's pieces make a whole unit; the others are alike
-            if (lane == 0)
-                mbar_arrive_expect_tx(full + islot, !there ? 0u : p.a.c.page == 64 ? (uint32_t)kBytes
-                                                                                   : (uint32_t)(__popc(there) * kSub));
-            __syncwarp();
-            if (pg >= 0)
-                bulk_g2s(ring + islot * kBytes + dst_off,
-                         p.a.c.data + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes + src_off +
-                             ((ahead.u & 1) ? half_mul : 0),
-                         (uint32_t)nbytes, full + islot);
-            bool item_end = false;
-            if (++ahead.u == ahead.u_end) {
-                item_end = true;
-                step_item<R>(p, tab, base, ahead);
-            }
-            left_ahead -= p.nosplit ? (item_end ? 1 : 0) : 1;
+            if (++ahead.u == ahead.u_end) step_item<R>(p, tab, base, ahead);
+            --left_ahead;
             find_page();
         }
         islot = islot + 1 == kStages ? 0 : islot + 1;
@@ -398,7 +448,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         seq_units(sq, p.a.window, u0, nu);
         const bool from_start = cur.u == u0;
         const int item_left = cur.u_end - cur.u;  // units of the item from here on
-        const int units = p.nosplit ? item_left : min(item_left, left);
+        const int units = min(item_left, left);
         const bool to_end = units == item_left;
 
         // the queries as B fragments: column g of tile n is a row (half precision) or a row's high or low part (f32)
@@ -421,13 +471,13 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                     if (p.a.type == QB_T_F16) load8<QB_T_F16>(q, x); else load8<QB_T_BF16>(q, x);
                 }
             };
-            float x[8], top = 0.0f;
+            float xs[NG][8], top = 0.0f;
 #pragma unroll
-            for (int G = 0; G < NG; ++G) {
-                load(G, x);
+            for (int G = 0; G < NG; ++G) load(G, xs[G]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-            }
+            for (int G = 0; G < NG; ++G)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(xs[G][i]));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // the row's largest magnitude into [2^14, 2^15)
@@ -439,7 +489,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             for (int h = 0; h < NH; ++h) cs[n][h] = __shfl_sync(0xFFFFFFFFu, back, PAIR ? 8 * t : 8 * t + 4 * h);
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
-                load(G, x);
+                float (&x)[8] = xs[G];
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -692,7 +742,11 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         for (int u = cur.u; u < cur.u + units; ++u) {
             const int k0 = u * kUnit;
             const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
-            if (!__all_sync(0xFFFFFFFFu, landed)) return;  // a copy never completed: fault word raised
+            if (!__all_sync(0xFFFFFFFFu, landed)) {  // a copy never completed: fault word raised
+                failed = 1;
+                left = 0;
+                break;
+            }
             const uint8_t *ub = ring + slot * kBytes;
             if (k0 + kUnit - 1 > pos_lo || k0 < first_hi)
                 unit(ub, k0, std::true_type());
@@ -703,6 +757,8 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             slot = slot + 1 == kStages ? 0 : slot + 1;
             phase ^= slot == 0 ? 1u : 0u;
         }
+
+        if (left == 0) break;
 
         // ---- the item's rows: out, or this piece's sums
         const bool whole = from_start && to_end;
@@ -719,7 +775,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                 if (j >= s_T) continue;
                 const int64_t tok = s_q0 + j;
                 const int head = s_kvh * p.grp + rho - j * p.grp;
-                const int64_t rec = (int64_t)(worker * 2 + (from_start ? 1 : 0)) * R + row;
+                const int64_t rec = (int64_t)((blockIdx.x * kWarps + warp) * 2 + (from_start ? 1 : 0)) * R + row;
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
                     float x[4];
@@ -755,79 +811,143 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                         p.a.lse[tok * p.a.nh + head] = (m[n][h] + log2f(sum)) * 0.6931471805599453f;
                 }
             }
-        if (from_start && !to_end && lane == 0) {
-            const int last_unit = count - left + item_left - 1;  // of the item, from this worker's first on
-            p.meta[worker * 2] = make_int4(worker + (int)(last_unit / share), s_q0, s_T, s_kvh);
-            p.meta[worker * 2 + 1] = make_int4(s_rt, 0, 0, 0);
+        if (!whole && lane == 0) {
+            piece[warp][from_start ? 1 : 0] = make_int4(s_q0, s_T, s_kvh, s_rt);
+            if (!from_start) piece_ends[warp] = to_end;
+            if (!to_end && warp * wshare + count == (int)(b1 - b0))  // the block that holds the item's last unit
+                item_last = (int)((b0 + (long long)warp * wshare + (count - left) + item_left - 1) / share);
         }
-        left -= p.nosplit ? 1 : units;
+        left -= units;
         if (to_end) step_item<R>(p, tab, base, cur); else cur.u += units;
     }
+
+    // ---- the items that the block's warps share: a warp takes a row of one
+    __syncthreads();
+    if (failed) {
+        if (threadIdx.x == 0) p.last[blockIdx.x] = -1;
+        return;
+    }
+    bool goes_on = false;  // the last item goes on in the next block
+    for (int w = 0, task = 0; w < kWarps; ++w)
+        for (int slot_ = w == 0 ? 0 : 1; slot_ < 2; ++slot_) {
+            const int4 it = piece[w][slot_];
+            if (it.y == 0) continue;
+            // its pieces: w's, then those of the warps after it up to the one that ends it
+            int parts = 1;
+            bool ends = slot_ == 0 && piece_ends[0];
+            while (!ends && w + parts < kWarps && piece[w + parts][0].y != 0) {
+                ends = piece_ends[w + parts];
+                ++parts;
+            }
+            const bool here = ends && slot_ == 1;  // wholly in this block
+            if (slot_ == 1 && !ends) {
+                goes_on = true;
+                if (threadIdx.x == 0) p.meta[blockIdx.x] = it;
+            }
+            for (int row = 0; row < R; ++row) {
+                const int rho = it.w * R + row, j = rho / p.grp;
+                if (j >= it.y) break;
+                if (task++ % kWarps != warp) continue;
+                auto rec = [&](int k) { return (int64_t)((blockIdx.x * kWarps + w + k) * 2 + (k == 0 ? slot_ : 0)) * R + row; };
+                const float2 st = lane < parts ? p.stat[rec(lane)] : make_float2(-INFINITY, 0.0f);
+                float mm = st.x;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+                const float wgt = ex2(st.x - (mm == -INFINITY ? 0.0f : mm));
+                float sum = wgt * st.y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                constexpr int E = DP / 32;
+                float acc[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+                for (int k = 0; k < parts; ++k) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, wgt, k);
+                    const float2 *x = reinterpret_cast<const float2 *>(p.part + rec(k) * DP + lane * E);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const float2 v = x[e];
+                        acc[2 * e] += f * v.x;
+                        acc[2 * e + 1] += f * v.y;
+                    }
+                }
+                if (here) {
+                    step_store<E>(p, acc, lane * E, sum, mm, it.x + j, it.z * p.grp + rho - j * p.grp, lane);
+                } else {
+                    const int64_t cr = (int64_t)(blockIdx.x * 2 + slot_) * R + row;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) p.cpart[cr * DP + lane * E + e] = acc[e];
+                    if (lane == 0) p.cstat[cr] = make_float2(mm, sum);
+                }
+            }
+        }
+    if (threadIdx.x == 0) p.last[blockIdx.x] = goes_on ? item_last : -1;
 }
 
-// Joins the pieces of items that lie with several workers.  Every block lists
-// the items (a worker holds the start of one at most), then a warp, or the whole
-// block where there are few, takes a row: the weights 2^(m_i - m) from the
-// pieces' maxima, their sums added in the order of the keys.
+// Joins the pieces of items that lie in several blocks.  Every block lists the
+// items (a block of the step kernel holds the start of one at most that goes on).
+// A warp takes a row of one: the weights 2^(m_i - m) from the pieces' maxima, their
+// sums added in the order of the keys; where there are few rows, which then have
+// many pieces, a block takes a row, its warps every eighth piece.
 template <int DP, int R>
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p) {
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p, int blocks) {
     constexpr int E = DP / 32;
-    __shared__ int items[kMaxWorkers];
-    __shared__ int nitems, warp_n[8];
+    __shared__ int items[kMaxGrid], lasts[kMaxGrid];
+    __shared__ int4 metas[kMaxGrid];
+    __shared__ int warp_n[8];
     __shared__ float red[8][DP], red_l[8];
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // items in the order of the workers
-    int base = 0;
-    for (int i0 = 0; i0 < p.nworkers; i0 += 256) {
-        const int i = i0 + threadIdx.x;
-        const bool is = i < p.nworkers && p.meta[i * 2].x >= 0;
-        const uint32_t b = __ballot_sync(0xFFFFFFFFu, is);
-        if (lane == 0) warp_n[warp] = __popc(b);
-        __syncthreads();
-        int at = base + __popc(b & ((1u << lane) - 1u));
-        for (int w = 0; w < warp; ++w) at += warp_n[w];
-        if (is) items[at] = i;
-        for (int w = 0; w < 8; ++w) base += warp_n[w];
-        __syncthreads();
+    const int mine = (int)threadIdx.x < blocks ? p.last[threadIdx.x] : -1;
+    const int4 my_meta = (int)threadIdx.x < blocks ? p.meta[threadIdx.x] : make_int4(0, 0, 0, 0);
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+    if (lane == 0) warp_n[warp] = __popc(b);
+    __syncthreads();
+    int at = __popc(b & ((1u << lane) - 1u)), nitems = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) at += warp_n[w];
+        nitems += warp_n[w];
     }
-    if (threadIdx.x == 0) nitems = base;
+    if (mine >= 0) {
+        items[at] = threadIdx.x;
+        lasts[at] = mine;
+        metas[at] = my_meta;
+    }
     __syncthreads();
     const int tasks = nitems * R;
-    const bool block_task = tasks <= (int)gridDim.x * 2;
-    const int step = block_task ? gridDim.x : gridDim.x * 8;
-    for (int i = block_task ? blockIdx.x : blockIdx.x * 8 + warp; i < tasks; i += step) {
-        const int w0 = items[i / R], row = i % R;
-        const int4 a = p.meta[w0 * 2], b = p.meta[w0 * 2 + 1];
-        const int rho = b.x * R + row, j = rho / p.grp;
-        if (j >= a.z) continue;  // the same for every thread of the block's task
-        const int parts = a.x - w0 + 1;
-        auto rec = [&](int k) { return (int64_t)((w0 + k) * 2 + (k == 0 ? 1 : 0)) * R + row; };
+    const bool wide = tasks <= 2 * (int)gridDim.x;  // a block a row
+    for (int i = wide ? blockIdx.x : blockIdx.x + warp * gridDim.x; i < tasks; i += wide ? gridDim.x : 8 * gridDim.x) {
+        const int c0 = items[i / R], row = i % R;
+        const int4 it = metas[i / R];
+        const int rho = it.w * R + row, j = rho / p.grp;
+        if (j >= it.y) continue;
+        const int parts = lasts[i / R] - c0 + 1;
+        auto rec = [&](int k) { return (int64_t)((c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + row; };
         float m = -INFINITY;
-        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.stat[rec(k)].x);
+        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.cstat[rec(k)].x);
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float mm = m == -INFINITY ? 0.0f : m;
         float acc[E], l = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        const int k0 = block_task ? warp : 0, ks = block_task ? 8 : 1;
 #pragma unroll 4
-        for (int k = k0; k < parts; k += ks) {
-            const float2 st = p.stat[rec(k)];
+        for (int k = wide ? warp : 0; k < parts; k += wide ? 8 : 1) {
+            const float2 st = p.cstat[rec(k)];
             const float wgt = ex2(st.x - mm);
             l += wgt * st.y;
-            const float *x = p.part + rec(k) * DP + lane * E;
+            const float2 *x = reinterpret_cast<const float2 *>(p.cpart + rec(k) * DP + lane * E);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(x + e);
-                acc[e] += wgt * v.x;
-                acc[e + 1] += wgt * v.y;
+            for (int e = 0; e < E / 2; ++e) {
+                const float2 v = x[e];
+                acc[2 * e] += wgt * v.x;
+                acc[2 * e + 1] += wgt * v.y;
             }
         }
-        if (block_task) {
-            __syncthreads();  // red of the task before has been read
+        if (wide) {
+            __syncthreads();  // red of the row before has been read
 #pragma unroll
             for (int e = 0; e < E; ++e) red[warp][lane * E + e] = acc[e];
             if (lane == 0) red_l[warp] = l;
@@ -842,21 +962,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p) {
                 for (int e = 0; e < E; ++e) acc[e] += red[w][lane * E + e];
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t tok = a.y + j;
-        const int head = a.w * p.grp + rho - j * p.grp;
-        const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int el = lane * E + e;
-            const float y = acc[e] * inv;
-            if (el < p.a.c.d) {
-                if (p.a.type == QB_T_F32) static_cast<float *>(p.a.out)[at + el] = y;
-                else if (p.a.type == QB_T_F16) static_cast<__half *>(p.a.out)[at + el] = __float2half_rn(y);
-                else static_cast<__nv_bfloat16 *>(p.a.out)[at + el] = __float2bfloat16_rn(y);
-            }
-        }
-        if (lane == 0 && p.a.lse) p.a.lse[tok * p.a.nh + head] = (m + log2f(l)) * 0.6931471805599453f;
+        step_store<E>(p, acc, lane * E, l, m, it.x + j, it.z * p.grp + rho - j * p.grp, lane);
     }
 }
 
@@ -869,15 +975,19 @@ template <int DP, bool PAIR, int NT, int SB>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     constexpr int kWarps = step_warps(DP, PAIR, NT), R = step_rows(PAIR, NT);
     constexpr int smem = kWarps * step_stages(DP, PAIR, NT) * step_unit_bytes(DP);
-    p.nworkers = grid * kWarps;
-    p.part = reinterpret_cast<float *>(p.a.ws);
-    p.stat = reinterpret_cast<float2 *>(p.part + (int64_t)p.nworkers * 2 * R * DP);
-    p.meta = reinterpret_cast<int4 *>(p.stat + (int64_t)p.nworkers * 2 * R);
+    const StepWs w = step_ws(grid, kWarps, R, DP);
+    p.part = reinterpret_cast<float *>(p.a.ws + w.part);
+    p.stat = reinterpret_cast<float2 *>(p.a.ws + w.stat);
+    p.cpart = reinterpret_cast<float *>(p.a.ws + w.cpart);
+    p.cstat = reinterpret_cast<float2 *>(p.a.ws + w.cstat);
+    p.last = reinterpret_cast<int *>(p.a.ws + w.last);
+    p.meta = reinterpret_cast<int4 *>(p.a.ws + w.meta);
     auto *f = kv4_step_kernel<DP, PAIR, NT, SB>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p)) return rc;
     if (p.nosplit) return QB_OK;
-    return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p);
+    return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p,
+                      grid);
 }
 
 template <int DP, bool PAIR, int NT>
@@ -892,7 +1002,7 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.a = a;
     p.grp = a.nh / a.c.nkv;
     const int grid = step_grid();
-    p.min_share = 4;
+    p.min_share = 8;
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
     // rows a sequence and key head, on average: pairs where they fit one column
     // tile (and for f32 always), two column tiles where one does not hold them
