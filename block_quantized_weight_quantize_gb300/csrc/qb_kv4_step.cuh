@@ -30,9 +30,9 @@
 // 7 - t), which keeps both loads free of bank conflicts.
 //
 // Work.  Units of 32 keys of one (sequence, key head, row tile), counted along
-// the whole batch; every block takes the same number of consecutive units
-// whatever the sequences' lengths are, its warps the same number of those, and
-// each warp streams its own through a ring of bulk copies (a page's block of a
+// the whole batch with two more for an item's own cost; every block takes the
+// same count of consecutive units whatever the sequences' lengths are, its warps
+// the same count of those, and each warp streams its own through a ring of bulk copies (a page's block of a
 // head is contiguous), so warps do not wait for one another until the end.  Then
 // the block joins the pieces of the items that its warps share; an item that
 // blocks share is joined by kv4_combine_kernel, in the order of the keys.
@@ -48,6 +48,7 @@ namespace qb {
 
 constexpr int kUnit = 32;       // keys a unit
 constexpr int kSeqChunk = 32;   // sequences summed together in a block's table
+constexpr int kItemCost = 2;    // what an item costs beside its units (its queries, its output), in units
 
 __host__ __device__ constexpr int step_unit_bytes(int dp) { return kv4_block(kUnit, dp); }
 // Rows (token, query head) of a row tile: nt column tiles of 4 rows, as pairs of
@@ -288,90 +289,117 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- the work: units before each chunk of sequences
+    // ---- the work.  An item's place on the line of units: kItemCost, then its own
     const int nseq = p.a.s.nseq, nchunks = (nseq + kSeqChunk - 1) / kSeqChunk;
-    for (int c = warp; c < nchunks; c += kWarps) {
-        const SeqInfo q = seq_info(p.a, c * kSeqChunk + lane, blockIdx.x == 0);
-        int u0, nu;
-        seq_units(q, p.a.window, u0, nu);
-        long long n = (long long)p.a.c.nkv * ((q.T * p.grp + R - 1) / R) * nu;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-        if (lane == 0) chunk_sum[c] = n;
-    }
-    __syncthreads();
-    if (nchunks > 1) {
-        if (threadIdx.x == 0) {
-            long long sum = 0;
-            for (int c = 0; c < nchunks; ++c) {
-                const long long n = chunk_sum[c];
-                chunk_sum[c] = sum;
-                sum += n;
-            }
-            chunk_sum[nchunks] = sum;
-        }
-        __syncthreads();
-    }
-    const long long total = nchunks > 1 ? chunk_sum[nchunks] : chunk_sum[0];
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < p.min_share) share = p.min_share;
     SeqInfo *tab = tabs[warp];
     int base = 0;
-    // Finds unit x: its sequence, the item in it and the unit's place in the item.
+    struct Weight {
+        int nu, nrt;
+        long long n;
+    };
+    auto weight = [&](const SeqInfo &q) {
+        Weight w;
+        int u0;
+        seq_units(q, p.a.window, u0, w.nu);
+        w.nrt = (q.T * p.grp + R - 1) / R;
+        w.n = (long long)p.a.c.nkv * w.nrt * (w.nu + kItemCost);
+        return w;
+    };
+    long long total;
+    if (nchunks == 1) {  // every warp by itself
+        const SeqInfo q = seq_info(p.a, lane, blockIdx.x == 0 && warp == 0);
+        tab[lane] = q;
+        total = weight(q).n;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        __syncwarp();
+    } else {
+        for (int c = warp; c < nchunks; c += kWarps) {
+            long long n = weight(seq_info(p.a, c * kSeqChunk + lane, blockIdx.x == 0)).n;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+            if (lane == 0) chunk_sum[c] = n;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            long long carry = 0;
+            for (int c0 = 0; c0 < nchunks; c0 += 32) {
+                const long long n = c0 + lane < nchunks ? chunk_sum[c0 + lane] : 0;
+                long long sum = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                if (c0 + lane < nchunks) chunk_sum[c0 + lane] = carry + sum - n;
+                carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            if (lane == 0) chunk_sum[nchunks] = carry;
+        }
+        __syncthreads();
+        total = chunk_sum[nchunks];
+    }
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < p.min_share) share = p.min_share;
+    // Finds place x on the line: its sequence, the item in it and the place in the item.
     struct Found {
-        int s, nrt, item, u;
+        int s, nrt, item, at;
     };
     auto find = [&](long long x) {
-        int lo = 0, hi = nchunks;  // the chunk that holds it
-        while (hi - lo > 1) {
-            const int m = (lo + hi) / 2;
-            if (chunk_sum[m] <= x) lo = m; else hi = m;
+        long long before = 0;
+        if (nchunks > 1) {
+            int lo = 0, hi = nchunks;  // the chunk that holds it
+            while (hi - lo > 1) {
+                const int m = (lo + hi) / 2;
+                if (chunk_sum[m] <= x) lo = m; else hi = m;
+            }
+            base = lo * kSeqChunk;
+            before = chunk_sum[lo];
+            const SeqInfo q = seq_info(p.a, base + lane, false);
+            __syncwarp();
+            tab[lane] = q;
+            __syncwarp();
         }
-        base = lo * kSeqChunk;
-        const SeqInfo q = seq_info(p.a, base + lane, false);
-        __syncwarp();
-        tab[lane] = q;
-        __syncwarp();
-        int u0, nu;
-        seq_units(q, p.a.window, u0, nu);
-        const int nrt = (q.T * p.grp + R - 1) / R;
-        const long long n = (long long)p.a.c.nkv * nrt * nu;
-        long long sum = n;
+        const Weight w = weight(tab[lane]);
+        long long sum = w.n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += y;
         }
-        const long long before = (nchunks > 1 ? chunk_sum[lo] : 0) + sum - n;
+        before += sum - w.n;
         // the last lane with units that starts at or before x
-        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= x);
+        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, w.n > 0 && before <= x);
         const int l = 31 - __clz(ok);
         const long long rem = x - __shfl_sync(0xFFFFFFFFu, before, l);
-        const int l_nu = __shfl_sync(0xFFFFFFFFu, nu, l);
+        const int per = __shfl_sync(0xFFFFFFFFu, w.nu, l) + kItemCost;
         Found f;
         f.s = base + l;
-        f.nrt = __shfl_sync(0xFFFFFFFFu, nrt, l);
-        f.item = rem >> 32 ? (int)(rem / l_nu) : (int)((uint32_t)rem / (uint32_t)l_nu);
-        f.u = (int)(rem - (long long)f.item * l_nu);
+        f.nrt = __shfl_sync(0xFFFFFFFFu, w.nrt, l);
+        f.item = rem >> 32 ? (int)(rem / per) : (int)((uint32_t)rem / (uint32_t)per);
+        f.at = (int)(rem - (long long)f.item * per);
         return f;
     };
-    // the block's units; where items are not split, from an item's beginning to one
+    // the block's share; where items are not split, from an item's beginning to one
     long long b0 = min(blockIdx.x * share, total), b1 = min(b0 + share, total);
     if (p.nosplit) {
-        if (b1 < total) b1 -= find(b1).u;
-        if (b0 < total) b0 -= find(b0).u;
+        if (b1 < total) b1 -= find(b1).at;
+        if (b0 < total) b0 -= find(b0).at;
     }
-    // the warp's
+    // the warp's: `count` places from x0 on
     const int wshare = (int)((b1 - b0 + kWarps - 1) / kWarps);
-    const int count = max(0, (int)min((long long)wshare, b1 - b0 - (long long)warp * wshare));
+    const long long x0 = b0 + (long long)warp * wshare;
+    int count = max(0, (int)min((long long)wshare, b1 - x0));
     StepPos cur = {};
+    int place = 0;  // of the unit at `cur`, from x0 on
     if (count > 0) {
-        const Found f = find(b0 + (long long)warp * wshare);
+        const Found f = find(x0);
         cur.s = f.s;
         cur.kvh = f.item / f.nrt;
         cur.rt = f.item - cur.kvh * f.nrt;
         step_enter(p, tab, base, cur);
-        cur.u += f.u;
+        cur.u += max(0, f.at - kItemCost);
+        place = max(0, kItemCost - f.at);
     }
 
     // ---- the copies, kStages units ahead.  A lane has one piece of a unit:
@@ -394,22 +422,41 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         dst_off = lane * kSub;
     }
     StepPos ahead = cur;
-    int left_ahead = count;
-    int pg = 0;  // this lane's page of the unit at `ahead`
-    auto find_page = [&]() {
-        const int key = ahead.u * kUnit + sub_key;
-        if (left_ahead > 0 && nbytes && key < ahead.len)
-            pg = p.a.s.tables[(int64_t)ahead.row * p.a.s.maxp + (key >> p.a.c.pshift)];
+    int place_ahead = place;
+    // page numbers of the sequence at `ahead`: lane l has the one of page pbase + l
+    int pbase = 0, pcache = 0;
+    auto find_pages = [&](bool fresh) {
+        const int pi = (ahead.u * kUnit) >> p.a.c.pshift;
+        if (!fresh && pi + 1 < pbase + 32) return;
+        pbase = pi;
+        pcache = 0;
+        if (((int64_t)(pi + lane) << p.a.c.pshift) < ahead.len) {
+            pcache = p.a.s.tables[(int64_t)ahead.row * p.a.s.maxp + pi + lane];
+            if ((uint32_t)pcache >= (uint32_t)p.a.c.npages) {
+                atomicOr(p.a.fault, kFaultIndex);
+                pcache = 0;
+            }
+        }
+    };
+    // the next item's queries, into the cache before they are needed
+    auto prefetch_queries = [&]() {
+        const SeqInfo q = step_seq(p, tab, base, ahead.s);
+        const int bytes = p.a.c.d * (p.a.type == QB_T_F32 ? 4 : 2), lines = (bytes + 127) / 128;
+        for (int i = lane; i < R * lines; i += 32) {
+            const int rho = ahead.rt * R + i / lines, j = rho / p.grp;
+            if (j < q.T) {
+                const int64_t at = (int64_t)(q.q0 + j) * p.a.q_stride + (int64_t)(ahead.kvh * p.grp + rho - j * p.grp) * p.a.c.d;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint8_t *>(p.a.q) +
+                                                             at * (p.a.type == QB_T_F32 ? 4 : 2) + (i % lines) * 128));
+            }
+        }
     };
     int islot = 0;
     auto issue = [&]() {
-        if (left_ahead > 0) {
+        if (place_ahead < count) {
+            const int pg = __shfl_sync(0xFFFFFFFFu, pcache, ((ahead.u * kUnit + sub_key) >> p.a.c.pshift) - pbase);
             if (nbytes) {  // each lane announces and issues its own piece
                 if (ahead.u * kUnit + sub_key < ahead.len) {
-                    if ((uint32_t)pg >= (uint32_t)p.a.c.npages) {
-                        atomicOr(p.a.fault, kFaultIndex);
-                        pg = 0;
-                    }
                     mbar_arrive_expect_tx(full + islot, (uint32_t)nbytes);
                     bulk_g2s(ring + islot * kBytes + dst_off,
                              src + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes +
@@ -419,13 +466,24 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                     mbar_arrive(full + islot);
                 }
             }
-            if (++ahead.u == ahead.u_end) step_item<R>(p, tab, base, ahead);
-            --left_ahead;
-            find_page();
+            ++place_ahead;
+            if (++ahead.u == ahead.u_end) {
+                step_item<R>(p, tab, base, ahead);
+                place_ahead += kItemCost;
+                if (place_ahead < count) {
+                    find_pages(true);
+                    prefetch_queries();
+                }
+            } else {
+                find_pages(false);
+            }
         }
         islot = islot + 1 == kStages ? 0 : islot + 1;
     };
-    find_page();
+    if (place_ahead < count) {
+        find_pages(true);
+        prefetch_queries();
+    }
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue();
 
@@ -436,11 +494,10 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     const int voff1 = kCodes + kSteps + (7 - t) * 16 * W + ((g ^ (4 * (1 - (t >> 1)))) * 2 * W);
 
     const CentreK ck;
-    int left = count;
     int slot = 0;
     uint32_t phase = 0;
-    while (left > 0) {
-        // ---- an item, or this worker's piece of it
+    while (place < count) {
+        // ---- an item, or this warp's piece of it
         const int s_kvh = cur.kvh, s_rt = cur.rt, s_len = cur.len;
         const SeqInfo sq = step_seq(p, tab, base, cur.s);
         const int s_q0 = sq.q0, s_T = sq.T;
@@ -448,7 +505,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         seq_units(sq, p.a.window, u0, nu);
         const bool from_start = cur.u == u0;
         const int item_left = cur.u_end - cur.u;  // units of the item from here on
-        const int units = min(item_left, left);
+        const int units = min(item_left, count - place);
         const bool to_end = units == item_left;
 
         // the queries as B fragments: column g of tile n is a row (half precision) or a row's high or low part (f32)
@@ -744,7 +801,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
             if (!__all_sync(0xFFFFFFFFu, landed)) {  // a copy never completed: fault word raised
                 failed = 1;
-                left = 0;
+                count = -1;
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
@@ -758,7 +815,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             phase ^= slot == 0 ? 1u : 0u;
         }
 
-        if (left == 0) break;
+        if (count < 0) break;
 
         // ---- the item's rows: out, or this piece's sums
         const bool whole = from_start && to_end;
@@ -814,11 +871,16 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         if (!whole && lane == 0) {
             piece[warp][from_start ? 1 : 0] = make_int4(s_q0, s_T, s_kvh, s_rt);
             if (!from_start) piece_ends[warp] = to_end;
-            if (!to_end && warp * wshare + count == (int)(b1 - b0))  // the block that holds the item's last unit
-                item_last = (int)((b0 + (long long)warp * wshare + (count - left) + item_left - 1) / share);
+            if (!to_end && x0 + count == b1)  // the block that holds the item's last unit
+                item_last = (int)((x0 + place + item_left - 1) / share);
         }
-        left -= units;
-        if (to_end) step_item<R>(p, tab, base, cur); else cur.u += units;
+        place += units;
+        if (to_end) {
+            step_item<R>(p, tab, base, cur);
+            place += kItemCost;
+        } else {
+            cur.u += units;
+        }
     }
 
     // ---- the items that the block's warps share: a warp takes a row of one
@@ -827,62 +889,67 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         if (threadIdx.x == 0) p.last[blockIdx.x] = -1;
         return;
     }
-    bool goes_on = false;  // the last item goes on in the next block
-    for (int w = 0, task = 0; w < kWarps; ++w)
-        for (int slot_ = w == 0 ? 0 : 1; slot_ < 2; ++slot_) {
-            const int4 it = piece[w][slot_];
-            if (it.y == 0) continue;
-            // its pieces: w's, then those of the warps after it up to the one that ends it
-            int parts = 1;
-            bool ends = slot_ == 0 && piece_ends[0];
-            while (!ends && w + parts < kWarps && piece[w + parts][0].y != 0) {
-                ends = piece_ends[w + parts];
-                ++parts;
-            }
-            const bool here = ends && slot_ == 1;  // wholly in this block
-            if (slot_ == 1 && !ends) {
-                goes_on = true;
-                if (threadIdx.x == 0) p.meta[blockIdx.x] = it;
-            }
-            for (int row = 0; row < R; ++row) {
-                const int rho = it.w * R + row, j = rho / p.grp;
-                if (j >= it.y) break;
-                if (task++ % kWarps != warp) continue;
-                auto rec = [&](int k) { return (int64_t)((blockIdx.x * kWarps + w + k) * 2 + (k == 0 ? slot_ : 0)) * R + row; };
-                const float2 st = lane < parts ? p.stat[rec(lane)] : make_float2(-INFINITY, 0.0f);
-                float mm = st.x;
+    // warps that hold the start of an item that goes on, a piece of one begun before them, one that ends it
+    const bool in = lane < kWarps;
+    const uint32_t starts = __ballot_sync(0xFFFFFFFFu, in && piece[in ? lane : 0][1].y != 0);
+    const uint32_t goes = __ballot_sync(0xFFFFFFFFu, in && piece[in ? lane : 0][0].y != 0);
+    const uint32_t ends = __ballot_sync(0xFFFFFFFFu, in && piece[in ? lane : 0][0].y != 0 && piece_ends[in ? lane : 0]);
+    const int carried = goes & 1;  // the block's first item was begun by another block
+    const int nshared = carried + __popc(starts);
+    int goes_on = 0;  // the last item goes on in the next block
+    if (starts) {
+        const int w = 31 - __clz(starts);
+        goes_on = (ends >> w >> 1) == 0;
+    }
+    for (int task = warp; task < nshared * R; task += kWarps) {
+        const int k0 = task / R, row = task - k0 * R;
+        const int slot_ = k0 >= carried ? 1 : 0;
+        const int w = slot_ ? __fns(starts, 0, k0 - carried + 1) : 0;
+        const int4 it = piece[w][slot_];
+        const int rho = it.w * R + row, j = rho / p.grp;
+        if (j >= it.y) continue;
+        // its pieces: w's, then those of the warps after it up to the one that ends it
+        const uint32_t e = slot_ ? ends >> w >> 1 : ends, g1 = goes >> w >> 1;
+        const int run = __ffs(~g1) - 1;  // warps after w with a piece of an item begun before them
+        const bool done = e != 0 && (slot_ ? __ffs(e) <= run : __ffs(e) - 1 <= run);
+        const int parts = done ? (slot_ ? __ffs(e) + 1 : __ffs(e)) : run + 1;
+        auto rec = [&](int k) { return (int64_t)((blockIdx.x * kWarps + w + k) * 2 + (k == 0 ? slot_ : 0)) * R + row; };
+        constexpr int E = DP / 32;
+        const float2 st = lane < parts ? p.stat[rec(lane)] : make_float2(-INFINITY, 0.0f);
+        float mm = st.x;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-                const float wgt = ex2(st.x - (mm == -INFINITY ? 0.0f : mm));
-                float sum = wgt * st.y;
+        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+        const float wgt = ex2(st.x - (mm == -INFINITY ? 0.0f : mm));
+        float sum = wgt * st.y;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                constexpr int E = DP / 32;
-                float acc[E];
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        float acc[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
 #pragma unroll 4
-                for (int k = 0; k < parts; ++k) {
-                    const float f = __shfl_sync(0xFFFFFFFFu, wgt, k);
-                    const float2 *x = reinterpret_cast<const float2 *>(p.part + rec(k) * DP + lane * E);
+        for (int k = 0; k < parts; ++k) {
+            const float f = __shfl_sync(0xFFFFFFFFu, wgt, k);
+            const float2 *x = reinterpret_cast<const float2 *>(p.part + rec(k) * DP + lane * E);
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        const float2 v = x[e];
-                        acc[2 * e] += f * v.x;
-                        acc[2 * e + 1] += f * v.y;
-                    }
-                }
-                if (here) {
-                    step_store<E>(p, acc, lane * E, sum, mm, it.x + j, it.z * p.grp + rho - j * p.grp, lane);
-                } else {
-                    const int64_t cr = (int64_t)(blockIdx.x * 2 + slot_) * R + row;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) p.cpart[cr * DP + lane * E + e] = acc[e];
-                    if (lane == 0) p.cstat[cr] = make_float2(mm, sum);
-                }
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 v = x[i];
+                acc[2 * i] += f * v.x;
+                acc[2 * i + 1] += f * v.y;
             }
         }
-    if (threadIdx.x == 0) p.last[blockIdx.x] = goes_on ? item_last : -1;
+        if (slot_ && done) {  // wholly in this block
+            step_store<E>(p, acc, lane * E, sum, mm, it.x + j, it.z * p.grp + rho - j * p.grp, lane);
+        } else {
+            const int64_t cr = (int64_t)(blockIdx.x * 2 + slot_) * R + row;
+#pragma unroll
+            for (int i = 0; i < E; ++i) p.cpart[cr * DP + lane * E + i] = acc[i];
+            if (lane == 0) p.cstat[cr] = make_float2(mm, sum);
+        }
+    }
+    if (threadIdx.x == 0) {
+        p.last[blockIdx.x] = goes_on ? item_last : -1;
+        if (goes_on) p.meta[blockIdx.x] = piece[31 - __clz(starts)][1];
+    }
 }
 
 // Joins the pieces of items that lie in several blocks.  Every block lists the
