@@ -548,27 +548,38 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             for (int G = 0; G < NG; ++G) {
                 float (&x)[8] = xs[G];
                 float sum = 0.0f;
+                uint32_t h2[4];
+                // a pair's high part is cut to f16's 11 bits, its low part what is left
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float y = x[i] * f, hi = __half2float(__float2half_rn(y));
-                    x[i] = PAIR && (g & 1) ? y - hi : hi;
-                    sum += x[i];
+                    const float y = x[i] * f;
+                    const float hi = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
+                    x[i] = !PAIR ? y : (g & 1) ? y - hi : hi;
                 }
-                if constexpr (PAIR) {
-                    cinit[n][G][0] = 0.0f;
-                } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h2[i] = pack_f16(x[i], x[i + 4]);
+                if constexpr (!PAIR) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 u = unpack_f16(h2[i]);
+                        sum += u.x + u.y;
+                    }
                     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
                     sum *= -8.0f / 16777216.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) cinit[n][G][h] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * h);
+                    // as subnormals, every second code stands as 16 c * 2^-24
+#pragma unroll
+                    for (int i = 1; i < 4; i += 2) {
+                        __half2 &u = *reinterpret_cast<__half2 *>(&h2[i]);
+                        u = __hmul2(u, __float2half2_rn(0.0625f));
+                    }
                 }
-                // as subnormals, every second code stands as 16 c * 2^-24
-                const float odd = PAIR ? 1.0f : 0.0625f;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    B[n][G][m][0] = pack_f16(x[2 * m], x[2 * m + 4]);
-                    B[n][G][m][1] = pack_f16(x[2 * m + 1] * odd, x[2 * m + 5] * odd);
+                    B[n][G][m][0] = h2[2 * m];
+                    B[n][G][m][1] = h2[2 * m + 1];
                 }
             }
         }
