@@ -29,8 +29,8 @@
 // Rows of 8 are keys in the order 0 7 1 6 2 5 3 4 (row 2t: key t, 2t + 1: key
 // 7 - t), which keeps both loads free of bank conflicts.
 //
-// Work.  Units of 32 keys of one (sequence, key head, row tile), counted along
-// the whole batch with two more for an item's own cost; every block takes the
+// Work.  Units of 32 or 64 keys of one (sequence, key head, row tile), counted along
+// the whole batch with 64 keys' worth more for an item's own cost; every block takes the
 // same count of consecutive units whatever the sequences' lengths are, its warps
 // the same count of those, and each warp streams its own through a ring of bulk copies (a page's block of a
 // head is contiguous), so warps do not wait for one another until the end.  Then
@@ -46,25 +46,22 @@
 
 namespace qb {
 
-constexpr int kUnit = 32;       // keys a unit
 constexpr int kSeqChunk = 32;   // sequences summed together in a block's table
-constexpr int kItemCost = 2;    // what an item costs beside its units (its queries, its output), in units
 
-__host__ __device__ constexpr int step_unit_bytes(int dp) { return kv4_block(kUnit, dp); }
 // Rows (token, query head) of a row tile: nt column tiles of 4 rows, as pairs of
 // high and low part, or of 8 rows.
 __host__ __device__ constexpr int step_rows(bool pair, int nt) { return (pair ? 4 : 8) * nt; }
-// Warps of a block (one a multiprocessor), by the registers that a lane's sums
-// (dp / 4 * nt of them), queries and scores take.
-__host__ __device__ constexpr int step_warps(int dp, bool pair, int nt) {
-    return dp * nt > 128 ? 8 : pair && nt == 1 ? 16 : 12;
-}
+// Keys of a unit, and warps of a block (one a multiprocessor), by the registers
+// that a lane's sums (dp / 4 * nt of them), queries and scores take.
+__host__ __device__ constexpr int step_unit(int dp, bool pair, int nt) { return pair && dp * nt <= 128 ? 64 : 32; }
+__host__ __device__ constexpr int step_warps(int dp, bool pair, int nt) { return dp * nt > 128 ? 8 : 12; }
+__host__ __device__ constexpr int step_unit_bytes(int dp, bool pair, int nt) { return kv4_block(step_unit(dp, pair, nt), dp); }
 // Units a warp's ring holds: what the 227 KB a block may have leave beside its tables (2072 bytes, 548 a warp, 8 a unit).
 __host__ __device__ constexpr int step_stages(int dp, bool pair, int nt) {
-    const int w = step_warps(dp, pair, nt), n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp) + 8));
+    const int w = step_warps(dp, pair, nt);
+    const int n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp, pair, nt) + 8));
     return n > 8 ? 8 : n;
 }
-
 constexpr int kMaxGrid = 256;
 inline int step_grid() { return std::min(num_sms(), kMaxGrid); }
 
@@ -199,11 +196,12 @@ __device__ __forceinline__ SeqInfo seq_info(const Kv4AttnArgs &a, int s, bool re
     return r;
 }
 
-// units of one item of the sequence: from the unit of its first seen key to its end (one at least)
+// units of U keys of one item of the sequence: from the unit of its first seen key to its end (one at least)
+template <int U>
 __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0, int &nu) {
     const int first = window ? max(0, q.len - q.T - window + 1) : 0;
-    u0 = first / kUnit;
-    nu = max(1, (q.len + kUnit - 1) / kUnit - u0);
+    u0 = first / U;
+    nu = max(1, (q.len + U - 1) / U - u0);
 }
 
 // A place in the call's work: sequence, key head, row tile, unit of the key axis.
@@ -219,11 +217,12 @@ __device__ __forceinline__ SeqInfo step_seq(const StepK &p, const SeqInfo *tab, 
 }
 
 // Enters the first sequence from x.s on that has new tokens.
+template <int U>
 __device__ __forceinline__ SeqInfo step_enter(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
     SeqInfo q = step_seq(p, tab, base, x.s);
     while (q.T == 0 && x.s < p.a.s.nseq) q = step_seq(p, tab, base, ++x.s);
     int nu;
-    seq_units(q, p.a.window, x.u, nu);
+    seq_units<U>(q, p.a.window, x.u, nu);
     x.u_end = x.u + nu;
     x.row = q.row;
     x.len = q.len;
@@ -231,7 +230,7 @@ __device__ __forceinline__ SeqInfo step_enter(const StepK &p, const SeqInfo *tab
 }
 
 // The item after the one that x is in; u at its beginning.
-template <int R>
+template <int R, int U>
 __device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
     const SeqInfo q = step_seq(p, tab, base, x.s);
     if (++x.rt == (q.T * p.grp + R - 1) / R) {
@@ -241,7 +240,7 @@ __device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, in
             ++x.s;
         }
     }
-    step_enter(p, tab, base, x);
+    step_enter<U>(p, tab, base, x);
 }
 
 // A joined row: E elements a lane from el on, over the sum, to (tok, head); lane 0 its lse.
@@ -263,7 +262,9 @@ __device__ __forceinline__ void step_store(const StepK &p, const float (&acc)[E]
 
 template <int DP, bool PAIR, int NT, int SB>
 __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_kernel(const StepK p) {
-    constexpr int kWarps = step_warps(DP, PAIR, NT), kStages = step_stages(DP, PAIR, NT), kBytes = step_unit_bytes(DP);
+    constexpr int kWarps = step_warps(DP, PAIR, NT), kStages = step_stages(DP, PAIR, NT);
+    constexpr int U = step_unit(DP, PAIR, NT), kBytes = step_unit_bytes(DP, PAIR, NT), NB = U / 16;
+    constexpr int kItemCost = 64 / U;  // what an item costs beside its units (its queries, its output), in units
     constexpr int R = step_rows(PAIR, NT), RT = R / NT, NH = PAIR ? 1 : 2;  // rows: of a tile, a column tile, a lane's
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;         // groups, groups a plane, planes
     constexpr int kSub = kv4_block(SB, DP);                               // a sub-block of SB rows in shared memory
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     uint8_t *ring = smem + warp * kStages * kBytes;
     uint64_t *full = full_bars[warp];
     // the pieces that a unit is copied in, a lane each
-    const int pieces = p.a.c.page == 64 ? 2 * (NP + 1) : kUnit / SB;
+    const int pieces = SB < p.a.c.page ? 2 * (NP + 1) : U / SB;
     if (lane < kStages) mbar_init(full + lane, pieces);
     fence_mbar_init();
     if (lane < 2) piece[warp][lane] = make_int4(0, 0, 0, 0);
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     auto weight = [&](const SeqInfo &q) {
         Weight w;
         int u0;
-        seq_units(q, p.a.window, u0, w.nu);
+        seq_units<U>(q, p.a.window, u0, w.nu);
         w.nrt = (q.T * p.grp + R - 1) / R;
         w.n = (long long)p.a.c.nkv * w.nrt * (w.nu + kItemCost);
         return w;
@@ -397,16 +398,16 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         cur.s = f.s;
         cur.kvh = f.item / f.nrt;
         cur.rt = f.item - cur.kvh * f.nrt;
-        step_enter(p, tab, base, cur);
+        step_enter<U>(p, tab, base, cur);
         cur.u += max(0, f.at - kItemCost);
         place = max(0, kItemCost - f.at);
     }
 
-    // ---- the copies, kStages units ahead.  A lane has one piece of a unit:
-    // a page (16 or 32 tokens a page), or a part of half a page (64)
+    // ---- the copies, kStages units ahead.  A lane has one piece of a unit: a
+    // page, or a part of half a page (64 tokens a page and units of 32)
     int sub_key = 0, half_mul = 0, dst_off = 0, nbytes = 0;
     const uint8_t *src = p.a.c.data;
-    if (p.a.c.page == 64) {
+    if (SB < p.a.c.page) {
         constexpr int kC64 = 64 * DP / 2, kS64 = 64 * DP / 16, kP64 = 64 * 16 * W;
         const int part = lane % (NP + 1), side = lane / (NP + 1);
         if (lane < 2 * (NP + 1)) {
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             half_mul = steps ? kS64 / 2 : kP64 / 2;
             dst_off = side * (kCodes + kSteps) + (steps ? kCodes : part * kPlane);
         }
-    } else if (lane < kUnit / SB) {
+    } else if (lane < U / SB) {
         sub_key = lane * SB;
         nbytes = kSub;
         dst_off = lane * kSub;
@@ -426,8 +427,8 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     // page numbers of the sequence at `ahead`: lane l has the one of page pbase + l
     int pbase = 0, pcache = 0;
     auto find_pages = [&](bool fresh) {
-        const int pi = (ahead.u * kUnit) >> p.a.c.pshift;
-        if (!fresh && pi + 1 < pbase + 32) return;
+        const int pi = (ahead.u * U) >> p.a.c.pshift;
+        if (!fresh && pi + 3 < pbase + 32) return;  // a unit has four pages at most
         pbase = pi;
         pcache = 0;
         if (((int64_t)(pi + lane) << p.a.c.pshift) < ahead.len) {
@@ -454,9 +455,9 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
     int islot = 0;
     auto issue = [&]() {
         if (place_ahead < count) {
-            const int pg = __shfl_sync(0xFFFFFFFFu, pcache, ((ahead.u * kUnit + sub_key) >> p.a.c.pshift) - pbase);
+            const int pg = __shfl_sync(0xFFFFFFFFu, pcache, ((ahead.u * U + sub_key) >> p.a.c.pshift) - pbase);
             if (nbytes) {  // each lane announces and issues its own piece
-                if (ahead.u * kUnit + sub_key < ahead.len) {
+                if (ahead.u * U + sub_key < ahead.len) {
                     mbar_arrive_expect_tx(full + islot, (uint32_t)nbytes);
                     bulk_g2s(ring + islot * kBytes + dst_off,
                              src + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes +
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             }
             ++place_ahead;
             if (++ahead.u == ahead.u_end) {
-                step_item<R>(p, tab, base, ahead);
+                step_item<R, U>(p, tab, base, ahead);
                 place_ahead += kItemCost;
                 if (place_ahead < count) {
                     find_pages(true);
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const SeqInfo sq = step_seq(p, tab, base, cur.s);
         const int s_q0 = sq.q0, s_T = sq.T;
         int u0, nu;
-        seq_units(sq, p.a.window, u0, nu);
+        seq_units<U>(sq, p.a.window, u0, nu);
         const bool from_start = cur.u == u0;
         const int item_left = cur.u_end - cur.u;  // units of the item from here on
         const int units = min(item_left, count - place);
@@ -606,10 +607,10 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 
         auto unit = [&](const uint8_t *ub, int k0, auto masked) {
             // ---- scores: key krow + 16 b + 8 i, this lane's rows
-            float z[NT][2][2][NH];
-            uint32_t vs[2][2][NG / 2];  // the values' steps of the same keys
+            float z[NT][NB][2][NH];
+            uint32_t vs[NB][2][NG / 2];  // the values' steps of the same keys
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 const uint8_t *kb = ub + (b * 16 / SB) * kSub;
                 const int r0 = (b * 16) % SB;
                 uint32_t st[2][NG / 2];
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             uint32_t seen[NT][NH];  // bit 2 b + i: the row sees that key
             if constexpr (masked) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         if (k0 + 16 * b + 8 * i + krow >= s_len) {  // a place that holds no key may hold anything
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                         const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
                         seen[n][h] = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 2 * NB; ++k) {
                             const int key = k0 + 8 * k + krow;
                             if (key >= first && key <= pos) seen[n][h] |= 1u << k;
                         }
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
             // ---- the running maximum and the steps' largest exponent; both rarely move
             __half2 top2 = __float2half2_rn(0.0f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2 * NB; ++k)
 #pragma unroll
                 for (int h = 0; h < NG / 2; ++h)
                     top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&vs[k >> 1][k & 1][h])));
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                 for (int h = 0; h < NH; ++h) {
                     top[n][h] = m[n][h];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2 * NB; ++k) {
                         float y = z[n][k >> 1][k & 1][h] * cs[n][h];
                         if constexpr (masked) {
                             if (!(seen[n][h] >> k & 1)) y = -INFINITY;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                 for (int h = 0; h < NH; ++h) {
                     const float mm = m[n][h] == -INFINITY ? 0.0f : m[n][h];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2 * NB; ++k) {
                         const float e = ex2(z[n][k >> 1][k & 1][h] - mm);
                         l[n][h] += e;
                         z[n][k >> 1][k & 1][h] = e * pe;
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 
             // ---- the values' codes times probabilities times steps
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 const uint8_t *va = ub + (b * 16 / SB) * kSub + ((b * 16) % SB) * 16 * W, *vb = va + 8 * 16 * W;
 #pragma unroll
                 for (int pl = 0; pl < NP; ++pl) {
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         };
 
         for (int u = cur.u; u < cur.u + units; ++u) {
-            const int k0 = u * kUnit;
+            const int k0 = u * U;
             const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
             if (!__all_sync(0xFFFFFFFFu, landed)) {  // a copy never completed: fault word raised
                 failed = 1;
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
-            if (k0 + kUnit - 1 > pos_lo || k0 < first_hi)
+            if (k0 + U - 1 > pos_lo || k0 < first_hi)
                 unit(ub, k0, std::true_type());
             else
                 unit(ub, k0, std::false_type());
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         }
         place += units;
         if (to_end) {
-            step_item<R>(p, tab, base, cur);
+            step_item<R, U>(p, tab, base, cur);
             place += kItemCost;
         } else {
             cur.u += units;
@@ -1052,7 +1053,8 @@ constexpr int kNoSplitKeys = 256;
 template <int DP, bool PAIR, int NT, int SB>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     constexpr int kWarps = step_warps(DP, PAIR, NT), R = step_rows(PAIR, NT);
-    constexpr int smem = kWarps * step_stages(DP, PAIR, NT) * step_unit_bytes(DP);
+    constexpr int smem = kWarps * step_stages(DP, PAIR, NT) * step_unit_bytes(DP, PAIR, NT);
+    p.min_share = 256 / step_unit(DP, PAIR, NT);
     const StepWs w = step_ws(grid, kWarps, R, DP);
     p.part = reinterpret_cast<float *>(p.a.ws + w.part);
     p.stat = reinterpret_cast<float2 *>(p.a.ws + w.stat);
@@ -1070,8 +1072,10 @@ static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
 
 template <int DP, bool PAIR, int NT>
 static int launch_step_m(StepK &p, int grid, cudaStream_t stream) {
-    return p.a.c.page == 16 ? launch_step_k<DP, PAIR, NT, 16>(p, grid, stream)
-                            : launch_step_k<DP, PAIR, NT, 32>(p, grid, stream);
+    constexpr int U = step_unit(DP, PAIR, NT);
+    return p.a.c.page == 16                ? launch_step_k<DP, PAIR, NT, 16>(p, grid, stream)
+           : p.a.c.page == 32 || U == 32   ? launch_step_k<DP, PAIR, NT, 32>(p, grid, stream)
+                                           : launch_step_k<DP, PAIR, NT, U>(p, grid, stream);
 }
 
 template <int DP>
@@ -1080,7 +1084,6 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.a = a;
     p.grp = a.nh / a.c.nkv;
     const int grid = step_grid();
-    p.min_share = 8;
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
     // rows a sequence and key head, on average: pairs where they fit one column
     // tile (and for f32 always), two column tiles where one does not hold them
