@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from . import _check, _stream, lib, QbError
+from . import _check, lib, QbError
 
 T_F32, T_F16, T_BF16 = 0, 1, 2  # QB_T_*
 _TYPE = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
@@ -61,6 +61,12 @@ class _Calls:
 
 
 _c = _Calls()
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, t) -> int:
+    """Handle of `stream`, or of the current stream of t's device."""
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _bytes(n: int, where: str) -> int:
@@ -84,12 +90,13 @@ def _rows(t, heads: int, d: int, what: str):
     """Address and token stride of [n, heads, d] rows whose last two axes are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{what}: device memory expected, got a CPU tensor")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{what}: [n, {heads}, {d}] expected, got {tuple(shape)}")
-    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+    n, h, e = t.shape if t.dim() == 3 else (0, 0, 0)
+    if h != heads or e != d:
+        raise ValueError(f"{what}: [n, {heads}, {d}] expected, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
         raise ValueError(f"{what}: the last two axes must be contiguous")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
+    return t.data_ptr(), s0 if n > 1 else heads * d
 
 
 def kv4_block_bytes(page: int, d: int) -> int:
@@ -159,7 +166,7 @@ def kv4_append(cache: Kv4, k, v, slots, stream=None) -> None:
     if k.dtype is not v.dtype or k.dtype not in _TYPE or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
         raise ValueError("k, v: float32, float16 or bfloat16 rows of one type, one slot each, expected")
     _check(_c.kv4_append(cache.ref, _TYPE[k.dtype], kp, ks, vp, vs, _dev(slots, torch.int32, "slots"), k.shape[0],
-                         _stream(stream)), "kv4_append")
+                         _stream(stream, k)), "kv4_append")
 
 
 def kv4_read(cache: Kv4, slots, k, v, stream=None) -> None:
@@ -169,7 +176,7 @@ def kv4_read(cache: Kv4, slots, k, v, stream=None) -> None:
     if k.dtype is not v.dtype or k.dtype not in _TYPE or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
         raise ValueError("k, v: float32, float16 or bfloat16 rows of one type, one slot each, expected")
     _check(_c.kv4_read(cache.ref, _TYPE[k.dtype], _dev(slots, torch.int32, "slots"), k.shape[0], kp, ks, vp, vs,
-                       _stream(stream)), "kv4_read")
+                       _stream(stream, k)), "kv4_read")
 
 
 def kv4_attn_workspace_bytes(cache: Kv4, q, seqs: KvSeqs = None) -> int:
@@ -195,7 +202,7 @@ def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: i
         workspace = torch.empty(kv4_attn_workspace_bytes(cache, q), dtype=torch.uint8, device=q.device)
     _check(_c.kv4_attn(cache.ref, seqs.ref, _TYPE[q.dtype], qp, qs, q.shape[0], nh, scale, window, op, os_, lp,
                        _dev(workspace, what="workspace"), workspace.numel() * workspace.element_size(),
-                       _stream(stream)), "kv4_attn")
+                       _stream(stream, q)), "kv4_attn")
 
 
 # ------------------------------------------------------------------ pages
@@ -221,7 +228,7 @@ def _page_ws(pages, workspace):
 
 def kv_pages_reset(pages: KvPages, stream=None) -> None:
     """Every page free, every sequence empty."""
-    _check(_c.kv_pages_reset(pages.ref, _stream(stream)), "kv_pages_reset")
+    _check(_c.kv_pages_reset(pages.ref, _stream(stream, pages.refs)), "kv_pages_reset")
 
 
 def kv_pages_extend(pages: KvPages, rows, counts, slots, status, stream=None) -> None:
@@ -232,7 +239,7 @@ def kv_pages_extend(pages: KvPages, rows, counts, slots, status, stream=None) ->
         raise ValueError("counts, status: one entry a row expected")
     _check(_c.kv_pages_extend(pages.ref, _dev(rows, i32, "rows"), _dev(counts, i32, "counts"), n,
                               _dev(slots, i32, "slots"), slots.numel(), _dev(status, i32, "status"),
-                              _stream(stream)), "kv_pages_extend")
+                              _stream(stream, pages.refs)), "kv_pages_extend")
 
 
 def kv_pages_fork(pages: KvPages, data, parents, children, status, workspace=None, stream=None) -> None:
@@ -244,13 +251,13 @@ def kv_pages_fork(pages: KvPages, data, parents, children, status, workspace=Non
     dp, layers, pb = _pool(data, pages.c.npages)
     ws, wb = _page_ws(pages, workspace)
     _check(_c.kv_pages_fork(pages.ref, dp, layers, pb, _dev(parents, i32, "parents"), _dev(children, i32, "children"),
-                            n, _dev(status, i32, "status"), _dev(ws, what="workspace"), wb, _stream(stream)),
+                            n, _dev(status, i32, "status"), _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
            "kv_pages_fork")
 
 
 def kv_pages_free(pages: KvPages, rows, stream=None) -> None:
     """Sequences rows (int32) become empty; pages nobody holds go back to the stack."""
-    _check(_c.kv_pages_free(pages.ref, _dev(rows, torch.int32, "rows"), rows.numel(), _stream(stream)),
+    _check(_c.kv_pages_free(pages.ref, _dev(rows, torch.int32, "rows"), rows.numel(), _stream(stream, pages.refs)),
            "kv_pages_free")
 
 
@@ -258,7 +265,7 @@ def kv_pages_compact(pages: KvPages, data, workspace=None, stream=None) -> None:
     """Moves the held pages to the pool's beginning, in every layer of data."""
     dp, layers, pb = _pool(data, pages.c.npages)
     ws, wb = _page_ws(pages, workspace)
-    _check(_c.kv_pages_compact(pages.ref, dp, layers, pb, _dev(ws, what="workspace"), wb, _stream(stream)),
+    _check(_c.kv_pages_compact(pages.ref, dp, layers, pb, _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
            "kv_pages_compact")
 
 
@@ -269,4 +276,4 @@ def kv_pages_copy(data, npages: int, src, dst, stream=None) -> None:
         raise ValueError("src, dst: as many destinations as sources expected")
     dp, layers, pb = _pool(data, npages)
     _check(_c.kv_pages_copy(dp, layers, npages, pb, _dev(src, torch.int32, "src"), _dev(dst, torch.int32, "dst"), n,
-                            _stream(stream)), "kv_pages_copy")
+                            _stream(stream, src)), "kv_pages_copy")
