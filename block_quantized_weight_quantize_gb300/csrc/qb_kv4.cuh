@@ -94,7 +94,7 @@ __device__ __forceinline__ void store8(void *p, const float (&x)[8]) {
 
 __host__ __device__ constexpr int type_bytes(int type) { return type == QB_T_F32 ? 4 : 2; }
 
-// Launchers (qb_kv4_rows.cu, qb_kv4_attn.cu, qb_kv_pages.cu); arguments checked by the C entries.
+// Launchers; arguments checked by the C entries (qb_kv4_api.cu).
 int launch_kv4_append(const Kv4View &c, int type, const void *k, int64_t ks, const void *v, int64_t vs,
                       const int32_t *slots, int64_t n, cudaStream_t stream);
 int launch_kv4_read(const Kv4View &c, int type, const int32_t *slots, int64_t n, void *k, int64_t ks, void *v,
@@ -116,8 +116,40 @@ struct Kv4AttnArgs {
     uint8_t *ws;
     int *fault;
 };
+// A sequence of the call: its table row, length, new tokens and first new token.
+struct SeqInfo {
+    int row, len, T, q0;
+};
+__device__ __forceinline__ SeqInfo seq_info(const Kv4AttnArgs &a, int s, bool report) {
+    SeqInfo r = {0, 0, 0, 0};
+    if (s >= a.s.nseq) return r;
+    r.row = a.s.rows ? a.s.rows[s] : s;
+    int64_t q0 = s, q1 = s + 1;
+    if (a.s.q_start) {
+        q0 = a.s.q_start[s];
+        q1 = a.s.q_start[s + 1];
+    }
+    q0 = min(max(q0, (int64_t)0), a.ntok);
+    q1 = min(max(q1, q0), a.ntok);
+    r.q0 = (int)q0;
+    r.T = (int)(q1 - q0);
+    if (r.row < 0 || r.row >= a.s.nrows) {
+        if (report) atomicOr(a.fault, kFaultIndex);
+        r.row = 0;
+    } else {
+        r.len = (int)min((int64_t)max(a.s.lens[r.row], 0), (int64_t)a.s.maxp * a.c.page);
+    }
+    return r;
+}
+
 int64_t kv4_attn_ws(int nkv, int dp, int nh);
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream);
+// A few tokens a sequence (qb_kv4_step.cuh), many (qb_kv4_prompt.cuh); by padded head size.
+int launch_kv4_step_64(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_step_128(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_step_256(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_64(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_128(const Kv4AttnArgs &a, cudaStream_t stream);
 
 int64_t kv_pages_ws(int npages, int nrows);
 int launch_kv_pages_reset(const qb_kv_pages &p, cudaStream_t stream);

@@ -17,7 +17,13 @@ int64_t kv4_attn_ws(int nkv, int dp, int nh) {
     return most;
 }
 
+// Rows (token, query head) a sequence and key head, on average, from which the
+// prompt kernel takes a half-precision call.
+constexpr int kPromptFrom = 64;
+
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
+    if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)
+        return a.c.dp == 64 ? launch_kv4_prompt_64(a, stream) : launch_kv4_prompt_128(a, stream);
     return a.c.dp == 64 ? launch_kv4_step_64(a, stream)
            : a.c.dp == 128 ? launch_kv4_step_128(a, stream) : launch_kv4_step_256(a, stream);
 }

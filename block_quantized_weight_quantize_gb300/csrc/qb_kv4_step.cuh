@@ -170,32 +170,6 @@ __device__ __forceinline__ void lds(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
-// A sequence of the call: its table row, length, new tokens and first new token.
-struct SeqInfo {
-    int row, len, T, q0;
-};
-__device__ __forceinline__ SeqInfo seq_info(const Kv4AttnArgs &a, int s, bool report) {
-    SeqInfo r = {0, 0, 0, 0};
-    if (s >= a.s.nseq) return r;
-    r.row = a.s.rows ? a.s.rows[s] : s;
-    int64_t q0 = s, q1 = s + 1;
-    if (a.s.q_start) {
-        q0 = a.s.q_start[s];
-        q1 = a.s.q_start[s + 1];
-    }
-    q0 = min(max(q0, (int64_t)0), a.ntok);
-    q1 = min(max(q1, q0), a.ntok);
-    r.q0 = (int)q0;
-    r.T = (int)(q1 - q0);
-    if (r.row < 0 || r.row >= a.s.nrows) {
-        if (report) atomicOr(a.fault, kFaultIndex);
-        r.row = 0;
-    } else {
-        r.len = (int)min((int64_t)max(a.s.lens[r.row], 0), (int64_t)a.s.maxp * a.c.page);
-    }
-    return r;
-}
-
 // units of U keys of one item of the sequence: from the unit of its first seen key to its end (one at least)
 template <int U>
 __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0, int &nu) {
@@ -1092,9 +1066,5 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     if (a.type == QB_T_F32) return launch_step_m<DP, true, 2>(p, grid, stream);
     return rows <= 8 * n ? launch_step_m<DP, false, 1>(p, grid, stream) : launch_step_m<DP, false, 2>(p, grid, stream);
 }
-
-int launch_kv4_step_64(const Kv4AttnArgs &a, cudaStream_t stream);
-int launch_kv4_step_128(const Kv4AttnArgs &a, cudaStream_t stream);
-int launch_kv4_step_256(const Kv4AttnArgs &a, cudaStream_t stream);
 
 }  // namespace qb
