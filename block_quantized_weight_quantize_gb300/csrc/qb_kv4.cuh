@@ -92,6 +92,35 @@ __device__ __forceinline__ void store8(void *p, const float (&x)[8]) {
     }
 }
 
+// Codes in the low (or second) four bits of each half, as code - 8.  The three
+// constants stay in registers (opaque to the compiler), so that mask and OR are
+// one three-input operation.
+struct CentreK {
+    uint32_t lo, hi, one;
+    __device__ __forceinline__ CentreK() {
+        asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
+        asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(one));  // 1024, twice
+    }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t centre_lo(const CentreK &k, uint32_t w) {
+    uint32_t b = and_or(w, k.lo, k.one);  // 1024 + c
+    __half2 &h = *reinterpret_cast<__half2 *>(&b);
+    h = __hadd2(h, __float2half2_rn(-1032.0f));
+    return b;
+}
+__device__ __forceinline__ uint32_t centre_hi(const CentreK &k, uint32_t w) {
+    uint32_t b = and_or(w, k.hi, k.one);  // 1024 + 16 c
+    __half2 &h = *reinterpret_cast<__half2 *>(&b);
+    h = __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
+    return b;
+}
+
 __host__ __device__ constexpr int type_bytes(int type) { return type == QB_T_F32 ? 4 : 2; }
 
 // Launchers; arguments checked by the C entries (qb_kv4_api.cu).

@@ -70,24 +70,102 @@ __device__ __forceinline__ float prompt_ex2(float x) {
 __device__ __forceinline__ uint32_t prompt_half2(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 
 // Eight codes as f16 pairs (0,4) (1,5) (2,6) (3,7) of a word's nibbles: (code - 8) * step.
-__device__ __forceinline__ uint4 prompt_decode(uint32_t w, __half2 step) {
+__device__ __forceinline__ uint4 prompt_decode(const CentreK &ck, uint32_t w, __half2 step) {
+    const uint32_t b[4] = {centre_lo(ck, w), centre_hi(ck, w), centre_lo(ck, w >> 8), centre_hi(ck, w >> 8)};
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = i < 2 ? w : w >> 8;
-        uint32_t b = (x & ((i & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-        __half2 &h = *reinterpret_cast<__half2 *>(&b);
-        h = (i & 1) ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f))
-                    : __hadd2(h, __float2half2_rn(-1032.0f));
-        h = __hmul2(h, step);
-        o[i] = b;
-    }
+    for (int i = 0; i < 4; ++i) o[i] = prompt_half2(__hmul2(*reinterpret_cast<const __half2 *>(&b[i]), step));
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The whole warp's wait: false (for all of it) if any lane's ran out.
 __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, int *fault) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_sleep(bar, parity, fault));
+}
+
+// Two f32 operations in one.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair_f32(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The groups that are not finite among the keys lo..hi of a tile.
+static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
+    uint32_t bad = 0;
+    for (int i = max(lo, 0); i <= min(hi, kPromptTile - 1); ++i) bad |= flags[i] >> 8;
+    return bad;
+}
+
+// A tile's row of 128 scores in tensor memory, 32 at a time: MASKED, those
+// outside columns lo..hi count as -infinity; ODD, flagged keys' are 16 times larger.
+template <bool MASKED, bool ODD>
+__device__ __forceinline__ void prompt_scores(uint32_t tS, int c, const uint16_t *flags, int lo, int hi, uint32_t (&s)[32]) {
+    tc_ld32(tS + 32 * c, s);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (ODD && (flags[32 * c + i] & 1)) s[i] = __float_as_uint(__uint_as_float(s[i]) * 16.0f);
+        if (MASKED && (32 * c + i > hi || 32 * c + i < lo)) s[i] = 0xFF800000u;
+    }
+}
+
+// The largest of a row's scores.
+template <bool MASKED, bool ODD>
+__device__ __forceinline__ float prompt_max(uint32_t tS, const uint16_t *flags, int lo, int hi) {
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll(ODD ? 1 : 4)
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        prompt_scores<MASKED, ODD>(tS, c, flags, lo, hi, s);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            t0 = fmaxf(t0, __uint_as_float(s[i]));
+            t1 = fmaxf(t1, __uint_as_float(s[i + 1]));
+        }
+    }
+    return fmaxf(t0, t1);
+}
+
+// The probabilities 2^(s cs - m) of a row as f16 over its scores (32 scores'
+// columns have been read when the 16 columns of their probabilities are written), and their sum.
+template <bool MASKED, bool ODD>
+__device__ __forceinline__ float prompt_exp(uint32_t tS, const uint16_t *flags, int lo, int hi, float cs, float m) {
+    const uint64_t cs2 = pair_f32(cs, cs), m2 = pair_f32(-m, -m);
+    uint64_t sum = 0;  // (0, 0)
+#pragma unroll(ODD ? 1 : 4)
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[32], pk[16];
+        prompt_scores<MASKED, ODD>(tS, c, flags, lo, hi, s);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float2 z = unpair_f32(fma_f32x2(pair_f32(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cs2, m2));
+            float e0 = prompt_ex2(z.x), e1 = prompt_ex2(z.y);
+            sum = add_f32x2(sum, pair_f32(e0, e1));
+            if (ODD) {
+                if (flags[32 * c + i] & 2) e0 *= 16.0f;
+                if (flags[32 * c + i + 1] & 2) e1 *= 16.0f;
+            }
+            pk[i / 2] = prompt_half2(__floats2half2_rn(e0, e1));
+        }
+        tc_st16(tS + 16 * c, pk);
+    }
+    const float2 t = unpair_f32(sum);
+    return t.x + t.y;
 }
 
 template <int DP>
@@ -252,35 +330,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 const bool odd = (sm.any[sl][0] | sm.any[sl][1] | sm.any[sl][2] | sm.any[sl][3]) != 0;
                 const bool masked = k0 + kPromptTile - 1 > pos_lo || k0 < first_hi;
                 const int hi = pos - k0, lo = first - k0;  // columns lo..hi are seen
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
-                    tc_ld32(tS + 32 * c, s);
-                    if (odd) {
-#pragma unroll
-                        for (int i2 = 0; i2 < 32; ++i2) {
-                            const uint32_t fl = sm.flags[sl][32 * c + i2];
-                            if (fl & 1) s[i2] = __float_as_uint(__uint_as_float(s[i2]) * 16.0f);
-                            if (32 * c + i2 <= hi && 32 * c + i2 >= lo) bad |= fl >> 8;
-                        }
-                    }
-                    if (masked || odd) {
-#pragma unroll
-                        for (int i2 = 0; i2 < 32; ++i2) {
-                            if (32 * c + i2 > hi || 32 * c + i2 < lo) s[i2] = 0xFF800000u;
-                        }
-                        tc_st32(tS + 32 * c, s);
-                    }
-                    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                    for (int i2 = 0; i2 < 32; i2 += 2) {
-                        t0 = fmaxf(t0, __uint_as_float(s[i2]));
-                        t1 = fmaxf(t1, __uint_as_float(s[i2 + 1]));
-                    }
-                    top = fmaxf(top, fmaxf(t0, t1));
+                const uint16_t *flags = sm.flags[sl];
+                float top;
+                if (odd) {
+                    bad |= prompt_bad(flags, lo, hi);
+                    top = prompt_max<true, true>(tS, flags, lo, hi);
+                } else {
+                    top = masked ? prompt_max<true, false>(tS, flags, lo, hi) : prompt_max<false, false>(tS, flags, lo, hi);
                 }
-                if (masked || odd) tc_wait_st();
                 const float z = top * cs;
                 if (__any_sync(0xFFFFFFFFu, z > m + 8.0f)) {
                     const float mn = z > m + 8.0f ? z : m;
@@ -288,7 +345,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     if (i > 0) {
                         if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP / 32; ++c) {
                             uint32_t o[32];
                             tc_ld32(tO + 32 * c, o);
@@ -301,26 +358,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     m = mn;
                 }
                 const float mm = m == -INFINITY ? 0.0f : m;
-                float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32], pk[16];
-                    tc_ld32(tS + 32 * c, s);
-#pragma unroll
-                    for (int i2 = 0; i2 < 32; i2 += 2) {
-                        float e0 = prompt_ex2(fmaf(__uint_as_float(s[i2]), cs, -mm));
-                        float e1 = prompt_ex2(fmaf(__uint_as_float(s[i2 + 1]), cs, -mm));
-                        l0 += e0;
-                        l1 += e1;
-                        if (odd) {
-                            if (sm.flags[sl][32 * c + i2] & 2) e0 *= 16.0f;
-                            if (sm.flags[sl][32 * c + i2 + 1] & 2) e1 *= 16.0f;
-                        }
-                        pk[i2 / 2] = prompt_half2(__floats2half2_rn(e0, e1));
-                    }
-                    tc_st16(tS + 16 * c, pk);
-                }
-                l += l0 + l1;
+                if (odd)
+                    l += prompt_exp<true, true>(tS, flags, lo, hi, cs, mm);
+                else
+                    l += masked ? prompt_exp<true, false>(tS, flags, lo, hi, cs, mm)
+                                : prompt_exp<false, false>(tS, flags, lo, hi, cs, mm);
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_ready[q]);
@@ -372,6 +414,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         }
     } else if (warp < 12) {
         // ================================================= decoders: a thread a key
+        const CentreK ck;
         const int r = threadIdx.x - 8 * 32, dw = warp - 8;
         const int page = p.a.c.page, code_bytes = page * DP / 2, step_bytes = page * DP / 16;
         uint32_t kt = 0;
@@ -464,7 +507,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                         const uint32_t w = wi % 4 == 0 ? u.x : wi % 4 == 1 ? u.y : wi % 4 == 2 ? u.z : u.w;
                         const __half2 sp = *reinterpret_cast<const __half2 *>(&kst[gi / 2]);
                         *reinterpret_cast<uint4 *>(dst + (gi * 4 + t) * kOctStride) =
-                            prompt_decode(w, (gi & 1) ? __high2half2(sp) : __low2half2(sp));
+                            prompt_decode(ck, w, (gi & 1) ? __high2half2(sp) : __low2half2(sp));
                     }
                 fence_async_shared();
                 __syncwarp();
@@ -480,7 +523,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                         const uint4 &u = vc[wi / 4];
                         const uint32_t w = wi % 4 == 0 ? u.x : wi % 4 == 1 ? u.y : wi % 4 == 2 ? u.z : u.w;
                         *reinterpret_cast<uint4 *>(dst + ((c ^ swz) * (W / 2) + u2) * kOctStride) =
-                            prompt_decode(w, *reinterpret_cast<const __half2 *>(&vst[u2]));
+                            prompt_decode(ck, w, *reinterpret_cast<const __half2 *>(&vst[u2]));
                     }
                 fence_async_shared();
                 __syncwarp();
