@@ -11,13 +11,14 @@
 //
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
 // head + head) of one sequence and key head; a block takes items, the longest
-// first.  Roles of a block's 13 warps:
-//   0-3, 4-7  softmax of tile 0, 1: a thread a row; scores from tensor memory
-//             in two passes (maximum; exponentials), P back over the scores
+// first.  Roles of a block's 12 warps:
+//   0-3, 4-7  softmax of tile 0, 1: a thread a row, 32 scores at a time from
+//             tensor memory, P back over the scores; then one thread issues the
+//             tile's products, PV(i) and S(i+1), which run under the other
+//             tile's softmax
 //   8-11      decoders: a thread a key, rows loaded a tile ahead into
 //             registers, f16 core matrices (8 rows of 16 bytes) to shared memory
-//   12        issues the products: S0(i+1) follows PV0(i), S1(i+1) PV1(i), so
-//             that one tile's softmax runs under the other tile's products
+// (12 warps, not 13: a sub-partition's fourth warp would leave 128 registers a thread.)
 // Core matrices: K [dims/8][128 keys][8 dims] (K-major), V the same (dims along
 // N: MN-major), Q like K; the order of dims within and of groups of eight is the one
 // that unpacking gives, and is undone in Q's rows and the output's columns.
@@ -36,7 +37,7 @@ namespace qb {
 constexpr int kPromptTile = 128;    // keys a tile, rows a tile
 constexpr int kPromptQ = 2;         // row tiles an item
 constexpr int kPromptRows = kPromptTile * kPromptQ;
-constexpr int kPromptThreads = 13 * 32;
+constexpr int kPromptThreads = 12 * 32;
 
 struct PromptK {
     Kv4AttnArgs a;
@@ -112,49 +113,101 @@ static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo
     return bad;
 }
 
-// A tile's row of 128 scores in tensor memory, 32 at a time: MASKED, those
-// outside columns lo..hi count as -infinity; ODD, flagged keys' are 16 times larger.
-template <bool MASKED, bool ODD>
-__device__ __forceinline__ void prompt_scores(uint32_t tS, int c, const uint16_t *flags, int lo, int hi, uint32_t (&s)[32]) {
-    tc_ld32(tS + 32 * c, s);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (ODD && (flags[32 * c + i] & 1)) s[i] = __float_as_uint(__uint_as_float(s[i]) * 16.0f);
-        if (MASKED && (32 * c + i > hi || 32 * c + i < lo)) s[i] = 0xFF800000u;
-    }
-}
+// What a row's softmax carries from tile to tile.
+struct PromptRow {
+    float cs, m, l;   // factor of the scores, running maximum, sum
+    int lo, hi;       // columns lo..hi of the tile are seen
+};
 
-// The largest of a row's scores.
-template <bool MASKED, bool ODD>
-__device__ __forceinline__ float prompt_max(uint32_t tS, const uint16_t *flags, int lo, int hi) {
-    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll(ODD ? 1 : 4)
-    for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        prompt_scores<MASKED, ODD>(tS, c, flags, lo, hi, s);
+// The maximum rises to mn in lanes where that is more than m: O (DP columns, if
+// any products were added), the `done` columns of this tile's probabilities and the sum shrink.
+template <int DP>
+static __device__ __noinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
+                                                   bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
+    const float al = mn == m ? 1.0f : prompt_ex2(m - mn);
+    l *= al;
+    m = mn;
+    if (have_o) {
+        if (!prompt_wait(o_done, parity, fault)) return false;
+        tc_fence_after();
+        for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            tc_ld32(tO + 32 * c, o);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            t0 = fmaxf(t0, __uint_as_float(s[i]));
-            t1 = fmaxf(t1, __uint_as_float(s[i + 1]));
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tc_st32(tO + 32 * c, o);
         }
     }
-    return fmaxf(t0, t1);
+    if (done) {
+        tc_wait_st();
+        const __half2 a2 = __float2half2_rn(al);
+        for (int c = 0; c < done; c += 32) {  // 16 or 48 columns: the rest of the last 32 is scores, kept
+            uint32_t o[32];
+            tc_ld32(tS + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < done) o[i] = prompt_half2(__hmul2(*reinterpret_cast<const __half2 *>(&o[i]), a2));
+            if (done - c >= 32) {
+                tc_st32(tS + c, o);
+            } else {
+                uint32_t h[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) h[i] = o[i];
+                tc_st16(tS + c, h);
+            }
+        }
+    }
+    return true;
 }
 
-// The probabilities 2^(s cs - m) of a row as f16 over its scores (32 scores'
-// columns have been read when the 16 columns of their probabilities are written), and their sum.
-template <bool MASKED, bool ODD>
-__device__ __forceinline__ float prompt_exp(uint32_t tS, const uint16_t *flags, int lo, int hi, float cs, float m) {
-    const uint64_t cs2 = pair_f32(cs, cs), m2 = pair_f32(-m, -m);
+// A tile's row: 128 scores in tensor memory, 32 at a time (the next ones on
+// their way), become probabilities 2^(s cs - m) as f16 over them (32 scores'
+// columns have been read when the 16 columns of their probabilities are
+// written).  MASKED: scores outside columns lo..hi count as -infinity; ODD:
+// flagged keys' scores or probabilities are 16 times larger.
+template <int DP, bool MASKED, bool ODD>
+__device__ __forceinline__ bool prompt_tile(uint32_t tS, uint32_t tO, PromptRow &row, const uint16_t *flags, bool have_o,
+                                            uint64_t *o_done, uint32_t parity, int *fault) {
+    uint32_t s[2][32];
+    const uint64_t cs2 = pair_f32(row.cs, row.cs);
     uint64_t sum = 0;  // (0, 0)
-#pragma unroll(ODD ? 1 : 4)
+    bool ok = true;
+    tc_ld32_begin(tS, s[0]);
+#pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint32_t s[32], pk[16];
-        prompt_scores<MASKED, ODD>(tS, c, flags, lo, hi, s);
+        uint32_t (&x)[32] = s[c & 1];
+        tc_ld_wait(x);
+        if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), s[(c + 1) & 1]);
+        if (ODD || MASKED) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (ODD && (flags[32 * c + i] & 1)) x[i] = __float_as_uint(__uint_as_float(x[i]) * 16.0f);
+                if (32 * c + i > row.hi || 32 * c + i < row.lo) x[i] = 0xFF800000u;
+            }
+        }
+        float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+#pragma unroll
+        for (int i = 2; i < 32; i += 2) {
+            t0 = fmaxf(t0, __uint_as_float(x[i]));
+            t1 = fmaxf(t1, __uint_as_float(x[i + 1]));
+        }
+        const float z = fmaxf(t0, t1) * row.cs;
+        if (__any_sync(0xFFFFFFFFu, z > row.m + 8.0f)) {
+            if (c < 3) tc_ld_wait(s[(c + 1) & 1]);
+            const float2 part = unpair_f32(sum);
+            float l = row.l + (part.x + part.y), m = row.m;
+            sum = 0;
+            ok = prompt_rescale<DP>(tS, tO, 16 * c, m, l, z > m + 8.0f ? z : m, have_o, o_done, parity, fault) && ok;
+            row.l = l;
+            row.m = m;
+        }
+        const float mm = row.m == -INFINITY ? 0.0f : -row.m;
+        const uint64_t m2 = pair_f32(mm, mm);
+        uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            const float2 z = unpair_f32(fma_f32x2(pair_f32(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cs2, m2));
-            float e0 = prompt_ex2(z.x), e1 = prompt_ex2(z.y);
+            const float2 y = unpair_f32(fma_f32x2(pair_f32(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cs2, m2));
+            float e0 = prompt_ex2(y.x), e1 = prompt_ex2(y.y);
             sum = add_f32x2(sum, pair_f32(e0, e1));
             if (ODD) {
                 if (flags[32 * c + i] & 2) e0 *= 16.0f;
@@ -164,8 +217,9 @@ __device__ __forceinline__ float prompt_exp(uint32_t tS, const uint16_t *flags, 
         }
         tc_st16(tS + 16 * c, pk);
     }
-    const float2 t = unpair_f32(sum);
-    return t.x + t.y;
+    const float2 part = unpair_f32(sum);
+    row.l += part.x + part.y;
+    return ok;
 }
 
 template <int DP>
@@ -185,13 +239,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
-            mbar_init(&sm.k_free[i], 1);
+            mbar_init(&sm.k_free[i], kPromptQ);
             mbar_init(&sm.v_full[i], 4);
-            mbar_init(&sm.v_free[i], 1);
+            mbar_init(&sm.v_free[i], kPromptQ);
         }
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 0) {
         tc_alloc(&sm.tmem, 512);
         tc_relinquish();
     }
@@ -269,8 +323,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         const int q = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tb + lanes + 128u * q, tO = tb + lanes + 256u + (uint32_t)DP * q;
-        uint32_t tiles = 0;  // of this row tile so far
+        uint32_t tiles = 0, items = 0;  // of this row tile so far
         bool ok = true;
+        const bool issuer = (warp & 3) == 0;  // its elected lane issues the tile's products
+        const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
+        // S = Q K^T with the block's key tile kt
+        auto scores = [&](uint32_t kt) {
+            const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[kt & 1]);
+            if (!prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
+                              tc_desc(ka + 2 * s * kOctStride, kOctStride, 128), idS, s != 0);
+                tc_commit(&sm.s_full[q]);
+                tc_commit(&sm.k_free[kt & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // O (+)= P V
+        auto outputs = [&](uint32_t kt, bool first) {
+            const uint32_t va = smem_u32(sm.v[kt & 1]);
+            if (!prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < kPromptTile / 16; ++s)
+                    tc_mma_ts(tb + 256u + (uint32_t)DP * q, tb + 128u * q + 8u * s, tc_desc(va + 256 * s, 128, kOctStride),
+                              idO, !first || s != 0);
+                tc_commit(&sm.o_done[q]);
+                tc_commit(&sm.v_free[kt & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
         for (int k = 0; ok && item_at(k, it); ++k) {
             const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
             const bool live = j < it.T;
@@ -314,59 +402,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 }
                 fence_async_shared();
                 mbar_arrive(&sm.q_full[q]);
+                if (issuer && !(ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault) && scores(tiles))) break;
+                ++items;
             }
             // tiles whose keys all of this row tile's rows see need no mask
             const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
             const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
             const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : -1;
             const int first_hi = p.a.window ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
-            float m = -INFINITY, l = 0.0f;
+            PromptRow row = {cs, -INFINITY, 0.0f, 0, 0};
             uint32_t bad = 0;
             for (int i = 0; i < it.n; ++i, ++tiles) {
                 const int k0 = (it.t0 + i) * kPromptTile;
                 if (!(ok = prompt_wait(&sm.s_full[q], tiles & 1, p.a.fault))) break;
                 tc_fence_after();
-                const uint32_t sl = tiles & 3;
+                const uint32_t sl = tiles & 3, par = (tiles - 1) & 1;
                 const bool odd = (sm.any[sl][0] | sm.any[sl][1] | sm.any[sl][2] | sm.any[sl][3]) != 0;
                 const bool masked = k0 + kPromptTile - 1 > pos_lo || k0 < first_hi;
-                const int hi = pos - k0, lo = first - k0;  // columns lo..hi are seen
                 const uint16_t *flags = sm.flags[sl];
-                float top;
+                row.hi = pos - k0;
+                row.lo = first - k0;
                 if (odd) {
-                    bad |= prompt_bad(flags, lo, hi);
-                    top = prompt_max<true, true>(tS, flags, lo, hi);
+                    bad |= prompt_bad(flags, row.lo, row.hi);
+                    ok = prompt_tile<DP, true, true>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                } else if (masked) {
+                    ok = prompt_tile<DP, true, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else {
-                    top = masked ? prompt_max<true, false>(tS, flags, lo, hi) : prompt_max<false, false>(tS, flags, lo, hi);
+                    ok = prompt_tile<DP, false, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 }
-                const float z = top * cs;
-                if (__any_sync(0xFFFFFFFFu, z > m + 8.0f)) {
-                    const float mn = z > m + 8.0f ? z : m;
-                    const float al = mn == m ? 1.0f : prompt_ex2(m - mn);
-                    if (i > 0) {
-                        if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < DP / 32; ++c) {
-                            uint32_t o[32];
-                            tc_ld32(tO + 32 * c, o);
-#pragma unroll
-                            for (int i2 = 0; i2 < 32; ++i2) o[i2] = __float_as_uint(__uint_as_float(o[i2]) * al);
-                            tc_st32(tO + 32 * c, o);
-                        }
-                    }
-                    l *= al;
-                    m = mn;
-                }
-                const float mm = m == -INFINITY ? 0.0f : m;
-                if (odd)
-                    l += prompt_exp<true, true>(tS, flags, lo, hi, cs, mm);
-                else
-                    l += masked ? prompt_exp<true, false>(tS, flags, lo, hi, cs, mm)
-                                : prompt_exp<false, false>(tS, flags, lo, hi, cs, mm);
+                if (!ok) break;
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_ready[q]);
+                if (issuer && !(ok = prompt_wait(&sm.p_ready[q], tiles & 1, p.a.fault) && outputs(tiles, i == 0) &&
+                                     (i + 1 == it.n || scores(tiles + 1))))
+                    break;
             }
+            const float m = row.m, l = row.l;
             if (!ok) break;
             if (it.n > 0) {
                 if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
@@ -412,7 +484,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             __syncwarp();
             tc_fence_before();  // the reads of O, before the next item's products
         }
-    } else if (warp < 12) {
+    } else {
         // ================================================= decoders: a thread a key
         const CentreK ck;
         const int r = threadIdx.x - 8 * 32, dw = warp - 8;
@@ -530,69 +602,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 if (lane == 0) mbar_arrive(&sm.v_full[slot]);
             }
         }
-    } else {
-        // ================================================= products
-        const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
-        uint32_t kt = 0, items = 0;
-        bool ok = true;
-        auto scores = [&](int q, int slot) {
-            const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[slot]);
-#pragma unroll
-            for (int s = 0; s < DP / 16; ++s) {
-                if (elect_one())
-                    tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
-                              tc_desc(ka + 2 * s * kOctStride, kOctStride, 128), idS, s != 0);
-                __syncwarp();
-            }
-            if (elect_one()) {
-                tc_commit(&sm.s_full[q]);
-                if (q == kPromptQ - 1) tc_commit(&sm.k_free[slot]);
-            }
-            __syncwarp();
-        };
-        for (int k = 0; ok && item_at(k, it); ++k) {
-            if (it.n == 0) continue;
-            for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
-            ++items;
-            if (!ok || !(ok = prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
-            __syncwarp();
-            tc_fence_after();
-            for (int q = 0; q < kPromptQ; ++q) scores(q, kt & 1);
-            for (int i = 0; ok && i < it.n; ++i, ++kt) {
-                const int slot = kt & 1;
-                const uint32_t ph = (kt >> 1) & 1;
-                if (!(ok = prompt_wait(&sm.v_full[slot], ph, p.a.fault))) break;
-                for (int q = 0; q < kPromptQ; ++q) {
-                    if (!(ok = prompt_wait(&sm.p_ready[q], kt & 1, p.a.fault))) break;
-                    __syncwarp();
-                    tc_fence_after();
-                    const uint32_t va = smem_u32(sm.v[slot]);
-#pragma unroll
-                    for (int s = 0; s < kPromptTile / 16; ++s) {
-                        if (elect_one())
-                            tc_mma_ts(tb + 256u + (uint32_t)DP * q, tb + 128u * q + 8u * s,
-                                      tc_desc(va + 256 * s, 128, kOctStride), idO, i != 0 || s != 0);
-                        __syncwarp();
-                    }
-                    if (elect_one()) {
-                        tc_commit(&sm.o_done[q]);
-                        if (q == kPromptQ - 1) tc_commit(&sm.v_free[slot]);
-                    }
-                    __syncwarp();
-                    if (i + 1 < it.n) {
-                        if (q == 0 && !(ok = prompt_wait(&sm.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, p.a.fault))) break;
-                        __syncwarp();
-                        tc_fence_after();
-                        scores(q, (kt + 1) & 1);
-                    }
-                }
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) tc_dealloc(tb, 512);
+    if (warp == 0) tc_dealloc(tb, 512);
 }
 
 template <int DP>
