@@ -11,14 +11,14 @@
 //
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
 // head + head) of one sequence and key head; a block takes items, the longest
-// first.  Roles of a block's 12 warps:
+// first.  Roles of a block's 16 warps:
 //   0-3, 4-7  softmax of tile 0, 1: a thread a row, 32 scores at a time from
-//             tensor memory, P back over the scores; then one thread issues the
-//             tile's products, PV(i) and S(i+1), which run under the other
-//             tile's softmax
+//             tensor memory, P back over the scores
 //   8-11      decoders: a thread a key, rows loaded a tile ahead into
 //             registers, f16 core matrices (8 rows of 16 bytes) to shared memory
-// (12 warps, not 13: a sub-partition's fourth warp would leave 128 registers a thread.)
+//   12        issues the products: PV0(i), S0(i+1), then PV1(i), S1(i+1), so that
+//             one tile's softmax runs under the other tile's products
+// (Registers: 152 a softmax thread, 104 another's.)
 // Core matrices: K [dims/8][128 keys][8 dims] (K-major), V the same (dims along
 // N: MN-major), Q like K; the order of dims within and of groups of eight is the one
 // that unpacking gives, and is undone in Q's rows and the output's columns.
@@ -37,7 +37,7 @@ namespace qb {
 constexpr int kPromptTile = 128;    // keys a tile, rows a tile
 constexpr int kPromptQ = 2;         // row tiles an item
 constexpr int kPromptRows = kPromptTile * kPromptQ;
-constexpr int kPromptThreads = 12 * 32;
+constexpr int kPromptThreads = 16 * 32;
 
 struct PromptK {
     Kv4AttnArgs a;
@@ -81,7 +81,8 @@ __device__ __forceinline__ uint4 prompt_decode(const CentreK &ck, uint32_t w, __
 
 // The whole warp's wait: false (for all of it) if any lane's ran out.
 __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, int *fault) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_sleep(bar, parity, fault));
+    const bool ok = mbar_try_wait(bar, parity) || mbar_wait_sleep(bar, parity, fault);
+    return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // Two f32 operations in one.
@@ -106,7 +107,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// The groups that are not finite among the keys lo..hi of a tile.
+// The groups that are not finite among the keys lo..hi of a step.
 static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
     uint32_t bad = 0;
     for (int i = max(lo, 0); i <= min(hi, kPromptTile - 1); ++i) bad |= flags[i] >> 8;
@@ -116,11 +117,11 @@ static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo
 // What a row's softmax carries from tile to tile.
 struct PromptRow {
     float cs, m, l;   // factor of the scores, running maximum, sum
-    int lo, hi;       // columns lo..hi of the tile are seen
+    int lo, hi;       // columns lo..hi of the step are seen
 };
 
 // The maximum rises to mn in lanes where that is more than m: O (DP columns, if
-// any products were added), the `done` columns of this tile's probabilities and the sum shrink.
+// any products were added), the `done` columns of this step's probabilities and the sum shrink.
 template <int DP>
 static __device__ __noinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
                                                    bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
@@ -160,13 +161,13 @@ static __device__ __noinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int
     return true;
 }
 
-// A tile's row: 128 scores in tensor memory, 32 at a time (the next ones on
+// A step's row: 64 scores in tensor memory, 32 at a time (the next ones on
 // their way), become probabilities 2^(s cs - m) as f16 over them (32 scores'
 // columns have been read when the 16 columns of their probabilities are
 // written).  MASKED: scores outside columns lo..hi count as -infinity; ODD:
 // flagged keys' scores or probabilities are 16 times larger.
 template <int DP, bool MASKED, bool ODD>
-__device__ __forceinline__ bool prompt_tile(uint32_t tS, uint32_t tO, PromptRow &row, const uint16_t *flags, bool have_o,
+__device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow &row, const uint16_t *flags, bool have_o,
                                             uint64_t *o_done, uint32_t parity, int *fault) {
     uint32_t s[2][32];
     const uint64_t cs2 = pair_f32(row.cs, row.cs);
@@ -174,10 +175,10 @@ __device__ __forceinline__ bool prompt_tile(uint32_t tS, uint32_t tO, PromptRow 
     bool ok = true;
     tc_ld32_begin(tS, s[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kPromptTile / 32; ++c) {
         uint32_t (&x)[32] = s[c & 1];
         tc_ld_wait(x);
-        if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), s[(c + 1) & 1]);
+        if (c + 1 < kPromptTile / 32) tc_ld32_begin(tS + 32 * (c + 1), s[(c + 1) & 1]);
         if (ODD || MASKED) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -193,7 +194,7 @@ __device__ __forceinline__ bool prompt_tile(uint32_t tS, uint32_t tO, PromptRow 
         }
         const float z = fmaxf(t0, t1) * row.cs;
         if (__any_sync(0xFFFFFFFFu, z > row.m + 8.0f)) {
-            if (c < 3) tc_ld_wait(s[(c + 1) & 1]);
+            if (c + 1 < kPromptTile / 32) tc_ld_wait(s[(c + 1) & 1]);
             const float2 part = unpair_f32(sum);
             float l = row.l + (part.x + part.y), m = row.m;
             sum = 0;
@@ -239,13 +240,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
-            mbar_init(&sm.k_free[i], kPromptQ);
+            mbar_init(&sm.k_free[i], 1);
             mbar_init(&sm.v_full[i], 4);
-            mbar_init(&sm.v_free[i], kPromptQ);
+            mbar_init(&sm.v_free[i], 1);
         }
         fence_mbar_init();
     }
-    if (warp == 0) {
+    if (warp == 12) {
         tc_alloc(&sm.tmem, 512);
         tc_relinquish();
     }
@@ -318,47 +319,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
     };
 
     PromptItem it;
+    // 128 registers a thread of 4 warpgroups at launch: 152 + 152 + 104 + 104 = 4 * 128
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         // ================================================= softmax
         const int q = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tb + lanes + 128u * q, tO = tb + lanes + 256u + (uint32_t)DP * q;
-        uint32_t tiles = 0, items = 0;  // of this row tile so far
+        uint32_t tiles = 0;  // of this row tile so far
         bool ok = true;
-        const bool issuer = (warp & 3) == 0;  // its elected lane issues the tile's products
-        const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
-        // S = Q K^T with the block's key tile kt
-        auto scores = [&](uint32_t kt) {
-            const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[kt & 1]);
-            if (!prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s)
-                    tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
-                              tc_desc(ka + 2 * s * kOctStride, kOctStride, 128), idS, s != 0);
-                tc_commit(&sm.s_full[q]);
-                tc_commit(&sm.k_free[kt & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        // O (+)= P V
-        auto outputs = [&](uint32_t kt, bool first) {
-            const uint32_t va = smem_u32(sm.v[kt & 1]);
-            if (!prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < kPromptTile / 16; ++s)
-                    tc_mma_ts(tb + 256u + (uint32_t)DP * q, tb + 128u * q + 8u * s, tc_desc(va + 256 * s, 128, kOctStride),
-                              idO, !first || s != 0);
-                tc_commit(&sm.o_done[q]);
-                tc_commit(&sm.v_free[kt & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
         for (int k = 0; ok && item_at(k, it); ++k) {
             const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
             const bool live = j < it.T;
@@ -402,8 +371,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 }
                 fence_async_shared();
                 mbar_arrive(&sm.q_full[q]);
-                if (issuer && !(ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault) && scores(tiles))) break;
-                ++items;
             }
             // tiles whose keys all of this row tile's rows see need no mask
             const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
@@ -424,19 +391,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 row.lo = first - k0;
                 if (odd) {
                     bad |= prompt_bad(flags, row.lo, row.hi);
-                    ok = prompt_tile<DP, true, true>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, true>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else if (masked) {
-                    ok = prompt_tile<DP, true, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else {
-                    ok = prompt_tile<DP, false, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, false, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 }
                 if (!ok) break;
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_ready[q]);
-                if (issuer && !(ok = prompt_wait(&sm.p_ready[q], tiles & 1, p.a.fault) && outputs(tiles, i == 0) &&
-                                     (i + 1 == it.n || scores(tiles + 1))))
-                    break;
             }
             const float m = row.m, l = row.l;
             if (!ok) break;
@@ -484,7 +448,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             __syncwarp();
             tc_fence_before();  // the reads of O, before the next item's products
         }
-    } else {
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // ================================================= decoders: a thread a key
         const CentreK ck;
         const int r = threadIdx.x - 8 * 32, dw = warp - 8;
@@ -602,11 +567,67 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 if (lane == 0) mbar_arrive(&sm.v_full[slot]);
             }
         }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // ================================================= products
+        const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
+        uint32_t kt = 0, items = 0;  // key tiles, items so far
+        bool ok = warp == 12;
+        // S = Q K^T with key tile t
+        auto scores = [&](int q, uint32_t t) {
+            const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[t & 1]);
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
+                              tc_desc(ka + 2 * s * kOctStride, kOctStride, 128), idS, s != 0);
+                tc_commit(&sm.s_full[q]);
+                if (q == kPromptQ - 1) tc_commit(&sm.k_free[t & 1]);
+            }
+            __syncwarp();
+        };
+        // O (+)= P V
+        auto outputs = [&](int q, uint32_t t, bool first) {
+            const uint32_t va = smem_u32(sm.v[t & 1]);
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < kPromptTile / 16; ++s)
+                    tc_mma_ts(tb + 256u + (uint32_t)DP * q, tb + 128u * q + 8u * s, tc_desc(va + 256 * s, 128, kOctStride),
+                              idO, !first || s != 0);
+                tc_commit(&sm.o_done[q]);
+                if (q == kPromptQ - 1) tc_commit(&sm.v_free[t & 1]);
+            }
+            __syncwarp();
+        };
+        for (int k = 0; ok && item_at(k, it); ++k) {
+            if (it.n == 0) continue;
+            for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
+            ++items;
+            if (!ok || !(ok = prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
+            tc_fence_after();
+            for (int q = 0; q < kPromptQ; ++q) scores(q, kt);
+            for (int i = 0; ok && i < it.n; ++i, ++kt) {
+                const bool more = i + 1 < it.n;
+                if (!(ok = prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
+                if (more && !(ok = prompt_wait(&sm.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, p.a.fault))) break;
+                for (int q = 0; q < kPromptQ; ++q) {
+                    if (!(ok = prompt_wait(&sm.p_ready[q], kt & 1, p.a.fault))) break;
+                    tc_fence_after();
+                    outputs(q, kt, i == 0);
+                    if (!more) continue;
+                    // products with different accumulators are not ordered: the next scores,
+                    // which go where P is, wait until it has been read
+                    if (!(ok = prompt_wait(&sm.o_done[q], kt & 1, p.a.fault))) break;
+                    tc_fence_after();
+                    scores(q, kt + 1);
+                }
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tc_dealloc(tb, 512);
+    if (warp == 12) tc_dealloc(tb, 512);
 }
 
 template <int DP>
