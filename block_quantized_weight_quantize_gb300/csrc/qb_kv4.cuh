@@ -34,18 +34,6 @@ inline Kv4View kv4_view(const qb_kv4 &c) {
     return v;
 }
 
-// Byte offset in a block of `page` rows of the word that holds elements
-// 8*oct .. 8*oct+7 of a key row, and of the two halves (4 elements each) of a
-// value row (half h of 0, 1); w = groups a plane.
-__device__ __forceinline__ int kv4_key_word(int page, int w, int r, int oct) {
-    const int G = oct >> 2, t = oct & 3;
-    return ((((G >> 2) * page + r) * 4 + t) * w + (G & 3)) * 4;
-}
-__device__ __forceinline__ int kv4_value_half(int page, int w, int r, int oct, int h) {
-    const int G = oct >> 2, c = (2 * (oct & 3) + h) ^ (4 * ((r >> 1) & 1));
-    return ((((G >> 2) * page + r) * 8 + c) * w + (G & 3)) * 2;
-}
-
 // Eight consecutive elements of `type` as f32; p is aligned to their size (16 or 32 bytes).
 template <int TYPE>
 __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
@@ -119,6 +107,33 @@ __device__ __forceinline__ uint32_t centre_hi(const CentreK &k, uint32_t w) {
     __half2 &h = *reinterpret_cast<__half2 *>(&b);
     h = __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
     return b;
+}
+
+// Two f32 operations in one.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair_f32(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __host__ __device__ constexpr int type_bytes(int type) { return type == QB_T_F32 ? 4 : 2; }

@@ -34,8 +34,6 @@ int check_rows(const qb_kv4 *c, qb_type type, const void *k, int64_t ks, const v
     const int64_t width = (int64_t)c->nkv * c->d;
     const int es = type_bytes(type);
     if (rows_bad(k, ks, width, es) || rows_bad(v, vs, width, es)) return QB_E_ARG;
-    // one thread a 1/(dp/8) of a row, a grid's first axis holds 2^31 - 1 blocks of 256
-    if (n * c->nkv * (kv4_padded(c->d) / 8) / 256 >= 0x7FFFFFFF) return QB_E_ARG;
     return QB_OK;
 }
 

@@ -85,28 +85,6 @@ __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, int 
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// Two f32 operations in one.
-__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair_f32(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // The groups that are not finite among the keys lo..hi of a step.
 static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
     uint32_t bad = 0;

@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const int pos_lo = s_len - s_T + (s_rt * R) / p.grp;
         const int pos_hi = s_len - s_T + min(s_T - 1, (s_rt * R + R - 1) / p.grp);
         const int first_hi = p.a.window ? max(0, pos_hi - p.a.window + 1) : 0;
+        const int first_lo = p.a.window ? max(0, pos_lo - p.a.window + 1) : 0;
 
         float O[NT][NG][2][4];
         float m[NT][NH], l[NT][NH];
@@ -762,7 +763,9 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
-            if (k0 + U - 1 > pos_lo || k0 < first_hi)
+            if (k0 > pos_hi || k0 + U <= first_lo)
+                ;  // no row sees it: the sequence's other row tiles do
+            else if (k0 + U - 1 > pos_lo || k0 < first_hi)
                 unit(ub, k0, std::true_type());
             else
                 unit(ub, k0, std::false_type());
