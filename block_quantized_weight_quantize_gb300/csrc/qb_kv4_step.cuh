@@ -650,6 +650,17 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                     top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&vs[k >> 1][k & 1][h])));
             top2 = __hmax2(top2, __lowhigh2highlow(top2));
             uint32_t tb = *reinterpret_cast<const uint32_t *>(&top2) & 0xFFFFu;
+            if (tb >= 0x7C00u) {  // a step that is not finite says nothing about the others
+                tb = 0;
+#pragma unroll
+                for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                    for (int h = 0; h < NG / 2; ++h) {
+                        const uint32_t lo = vs[k >> 1][k & 1][h] & 0x7FFFu, hi = vs[k >> 1][k & 1][h] >> 16 & 0x7FFFu;
+                        if (lo < 0x7C00u) tb = max(tb, lo);
+                        if (hi < 0x7C00u) tb = max(tb, hi);
+                    }
+            }
             bool moved = (int)(tb >> 10) > eb;
             float top[NT][NH];
 #pragma unroll

@@ -488,3 +488,122 @@ def test_a_serving_loop():
     held[0] = []
     qb.kv_pages_compact(st.h, st.pool)
     grow([1, 0, 4], [2, 18, 1])
+
+
+# ---------------------------------------------------------------- prompts out of the ordinary
+
+def _fill(b, k, v):
+    """Writes rows k, v [n, nkv, d] over a one-sequence batch's cache and takes what they read back as."""
+    import torch
+    n = b.lens[0]
+    slots = _i32(b.tables[0, np.arange(n) // b.page] * b.page + np.arange(n) % b.page)
+    kt, vt = (torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda() for x in (k, v))
+    qb.kv4_append(b.cache, kt, vt, slots)
+    kb, vb = torch.empty_like(kt), torch.empty_like(vt)
+    qb.kv4_read(b.cache, slots, kb, vb)
+    b.k, b.v = kb.double().cpu().numpy(), vb.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_large_steps(name, d):
+    """Steps past 2^12 in single keys, values and groups, small ones beside them."""
+    b = Batch(31, [300], [200], 4, 2, d, 16, name)
+    k, v = b.k.copy(), b.v.copy()
+    v[40:44, 0] *= 8e4
+    v[150, 1, 32:40] = 3e5
+    k[77, 1] *= 6e4 * np.sign(np.arange(d) - 9.5)
+    b.q *= 0.001
+    _fill(b, k, v)
+    assert np.isfinite(b.k).all() and np.isfinite(b.v).all()
+    b.check()
+
+
+@pytest.mark.parametrize("name", ["f32", "f16"])
+@pytest.mark.parametrize("nh,nkv,d,T", [(4, 2, 64, 200), (2, 1, 128, 170), (2, 1, 128, 3)])
+def test_unreadable_rows_in_prompts(name, nh, nkv, d, T):
+    """An infinite value makes its group's outputs NaN in the rows that see it, an infinite key every output; rows before them and other heads stay."""
+    import torch
+    n = 260
+    b = Batch(32, [n], [T], nh, nkv, d, 32, name)
+    clean, clean_lse = b.run(0.125)
+    k, v = b.k.copy(), b.v.copy()
+    kv, kk = n - T // 2 - 1, n - T // 4 - 1     # places of the bad value and of the bad key
+    v[kv, 0, d - 1] = np.inf
+    k[kk, nkv - 1, 5] = -np.inf
+    _fill(b, k, v)
+    out, lse = b.run(0.125)
+    grp = nh // nkv
+    pos = n - T + np.arange(T)
+    for h in range(nh):
+        saw_v = (pos >= kv) & (h // grp == 0)
+        saw_k = (pos >= kk) & (h // grp == nkv - 1)
+        o, c = out[:, h].float().cpu().numpy(), clean[:, h].float().cpu().numpy()
+        same = ~(saw_v | saw_k)
+        assert np.array_equal(o[same], c[same])
+        assert np.isnan(o[saw_k]).all() and lse[:, h].isnan().cpu().numpy()[saw_k].all()
+        only_v = saw_v & ~saw_k
+        last = np.arange(d) >= (d - 1) // 32 * 32
+        assert np.isnan(o[only_v][:, last]).all() and not np.isnan(o[only_v][:, ~last]).any()
+        assert torch.equal(lse[:, h][torch.from_numpy(only_v).cuda()], clean_lse[:, h][torch.from_numpy(only_v).cuda()])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3e-6])
+@pytest.mark.parametrize("T", [1, 150])
+def test_scales(name, scale, T):
+    """Negative, zero and small factors: the largest score is the one after the factor."""
+    Batch(33, [190], [T], 4, 2, 64, 64, name).check(scale=scale)
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+def test_prompt_sharp_scores(name):
+    """Scores that rise by hundreds along the keys: the maximum moves within and between tiles."""
+    b = Batch(34, [520], [400], 4, 2, 128, 16, name, offset=0.0)
+    ramp = np.linspace(0.0, 30.0, 520)[:, None, None]
+    _fill(b, b.k * 0.1 + ramp, b.v)
+    b.q.abs_()
+    b.check()
+
+
+@pytest.mark.parametrize("name", ["f32", "f16"])
+def test_prompts_of_many_sequences(name):
+    """More than a table's 64 sequences, some empty, some without new tokens, tables chosen by rows."""
+    import torch
+    rng = np.random.default_rng(35)
+    lens = [int(x) for x in rng.integers(0, 150, 90)]
+    news = [int(rng.integers(0, 80)) if i % 7 else 0 for i in range(90)]
+    b = Batch(35, lens, news, 4, 2, 64, 16, name)
+    b.check()
+    perm = rng.permutation(90)
+    seqs = qb.KvSeqs(_i32(b.tables), _i32(lens), rows=_i32(perm), q_start=_i32(np.concatenate([[0], np.cumsum(np.array(news)[perm])])))
+    out, _ = b.run(0.125)
+    pick = np.concatenate([np.arange(b.q_start[s], b.q_start[s + 1]) for s in perm]).astype(np.int64)
+    q = b.q[torch.from_numpy(pick).cuda()].contiguous()
+    got = torch.empty_like(q)
+    qb.kv4_attn(b.cache, q, seqs, 0.125, got)
+    want = out[torch.from_numpy(pick).cuda()]
+    # which keys a warp holds depends on the order: the same up to the sums' rounding
+    tol = 2.0 ** -17 if name == "f32" else 2.0 ** -9
+    assert (got.float() - want.float()).abs().max() <= tol * max(1.0, float(want.float().abs().max()))
+
+
+def test_prompt_same_bits_twice():
+    import torch
+    b = Batch(36, [700, 300], [400, 300], 8, 2, 128, 16, "bf16")
+    one, l1 = b.run(0.1)
+    two, l2 = b.run(0.1)
+    assert torch.equal(one, two) and torch.equal(l1, l2)
+
+
+def test_prompt_strided_and_window_and_page_32():
+    import torch
+    b = Batch(37, [400], [300], 4, 2, 64, 32, "f16")
+    want, _ = b.run(0.125, window=130)
+    wide_q = torch.zeros((300, 8, 64), dtype=torch.float16, device="cuda")
+    wide_o = torch.full((300, 6, 64), 3.0, dtype=torch.float16, device="cuda")
+    wide_q[:, 4:] = b.q
+    seqs = qb.KvSeqs(_i32(b.tables), _i32(b.lens), q_start=_i32(b.q_start))
+    qb.kv4_attn(b.cache, wide_q[:, 4:], seqs, 0.125, wide_o[:, 1:5], window=130)
+    assert torch.equal(wide_o[:, 1:5], want) and (wide_o[:, 0] == 3).all() and (wide_o[:, 5] == 3).all()
+    b.check(window=130)
