@@ -34,6 +34,23 @@ inline Kv4View kv4_view(const qb_kv4 &c) {
     return v;
 }
 
+// Eight half-precision elements of `type` as f32.
+template <int TYPE>
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == QB_T_F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        } else {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
 // Eight consecutive elements of `type` as f32; p is aligned to their size (16 or 32 bytes).
 template <int TYPE>
 __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
@@ -42,19 +59,7 @@ __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     } else {
-        const uint4 u = *static_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (TYPE == QB_T_F16) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                x[2 * i] = f.x;
-                x[2 * i + 1] = f.y;
-            } else {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        }
+        unpack8<TYPE>(*static_cast<const uint4 *>(p), x);
     }
 }
 
@@ -185,6 +190,10 @@ __device__ __forceinline__ SeqInfo seq_info(const Kv4AttnArgs &a, int s, bool re
     }
     return r;
 }
+
+// Blocks of the attention kernels: one a multiprocessor.
+constexpr int kAttnMaxGrid = 256;
+inline int attn_grid() { return num_sms() < kAttnMaxGrid ? num_sms() : kAttnMaxGrid; }
 
 int64_t kv4_attn_ws(int nkv, int dp, int nh);
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream);

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "qb_kv4_prompt.cuh"
 #include "qb_kv4_step.cuh"
 
 namespace qb {
@@ -13,7 +14,8 @@ int64_t kv4_attn_ws(int nkv, int dp, int nh) {
     int64_t most = 0;
     for (int nt = 1; nt <= 2; ++nt)
         for (int pair = 0; pair < 2; ++pair)
-            most = std::max(most, step_ws(step_grid(), step_warps(dp, pair != 0, nt), step_rows(pair != 0, nt), dp).end);
+            most = std::max(most, step_ws(attn_grid(), step_warps(dp, pair != 0, nt), step_rows(pair != 0, nt), dp).end);
+    if (dp <= 128) most = std::max(most, prompt_ws(attn_grid(), dp).end);
     return most;
 }
 

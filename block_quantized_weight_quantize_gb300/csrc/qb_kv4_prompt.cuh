@@ -10,15 +10,19 @@
 // factor 2^8 fits f16), when O is rescaled in tensor memory; sums in f32.
 //
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
-// head + head) of one sequence and key head; a block takes items, the longest
-// first.  Roles of a block's 16 warps:
+// head + head) of one sequence and key head, over the tiles of 128 keys that they
+// see.  Tiles are counted along all items, one more for an item's own cost; every
+// block takes the same count of consecutive ones.  An item that blocks share
+// leaves its rows' sums in the workspace, joined by kv4_prompt_join_kernel.
+// (Whole items to a block: 258 us for 2048 tokens on 8192 keys, 32 heads of 128,
+// 256 items on 152 multiprocessors; @JOIN@.)
+// Roles of a block's 13 warps (128 registers a thread):
 //   0-3, 4-7  softmax of tile 0, 1: a thread a row, 32 scores at a time from
 //             tensor memory, P back over the scores
 //   8-11      decoders: a thread a key, rows loaded a tile ahead into
 //             registers, f16 core matrices (8 rows of 16 bytes) to shared memory
 //   12        issues the products: PV0(i), S0(i+1), then PV1(i), S1(i+1), so that
 //             one tile's softmax runs under the other tile's products
-// (Registers: 152 a softmax thread, 104 another's.)
 // Core matrices: K [dims/8][128 keys][8 dims] (K-major), V the same (dims along
 // N: MN-major), Q like K; the order of dims within and of groups of eight is the one
 // that unpacking gives, and is undone in Q's rows and the output's columns.
@@ -42,12 +46,25 @@ constexpr int kPromptThreads = 16 * 32;
 struct PromptK {
     Kv4AttnArgs a;
     int grp;
+    int min_share;  // tiles a block
+    float *part;    // [grid][2][kPromptRows][DP]: a block's pieces (0: of an item begun before it)
+    float2 *stat;   // [grid][2][kPromptRows] running maximum, sum
+    int *last;      // [grid] the last block that holds a piece of the item that starts here and goes on; -1: none
+    int4 *meta;     // [grid] that item's first token, tokens, key head, row pair
 };
 
+// A block's piece of an item: tiles t0 .. t0 + n - 1.  Every warp has its own in
+// shared memory, so that walking along the block's share costs the loops no registers.
 struct PromptItem {
-    int row, len, T, q0, kvh, rp;
-    int t0, n;  // first key tile, tiles
+    int s, row, len, T, q0, kvh, rp;
+    int u;               // the piece's first tile, from the item's first on
+    int t0, n;
+    int place, rest;     // of the piece's first tile in the block's share; tiles of the item from there on
+    int count;           // places of the block's share
+    int from_start;
 };
+
+constexpr int kPromptCost = 1;  // what an item costs beside its tiles, in tiles
 
 template <int DP>
 struct PromptSmem {
@@ -60,7 +77,9 @@ struct PromptSmem {
     uint64_t q_full[kPromptQ], s_full[kPromptQ], p_ready[kPromptQ], o_done[kPromptQ];
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
     uint32_t tmem;
-    int chunk_sum[8192 / 32 + 1];
+    long long chunk_sum[8192 / 32 + 1];
+    long long x0, share;             // the block's share: its first place, its places
+    PromptItem it[kPromptThreads / 32];
 };
 
 __device__ __forceinline__ float prompt_ex2(float x) {
@@ -86,7 +105,7 @@ __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, int 
 }
 
 // The groups that are not finite among the keys lo..hi of a step.
-static __device__ __noinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
+__device__ __forceinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
     uint32_t bad = 0;
     for (int i = max(lo, 0); i <= min(hi, kPromptTile - 1); ++i) bad |= flags[i] >> 8;
     return bad;
@@ -101,7 +120,7 @@ struct PromptRow {
 // The maximum rises to mn in lanes where that is more than m: O (DP columns, if
 // any products were added), the `done` columns of this step's probabilities and the sum shrink.
 template <int DP>
-static __device__ __noinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
+__device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
                                                    bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
     const float al = mn == m ? 1.0f : prompt_ex2(m - mn);
     l *= al;
@@ -139,31 +158,33 @@ static __device__ __noinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int
     return true;
 }
 
-// A step's row: 64 scores in tensor memory, 32 at a time (the next ones on
+// A tile's row: 128 scores in tensor memory, 32 at a time (the next ones on
 // their way), become probabilities 2^(s cs - m) as f16 over them (32 scores'
 // columns have been read when the 16 columns of their probabilities are
 // written).  MASKED: scores outside columns lo..hi count as -infinity; ODD:
 // flagged keys' scores or probabilities are 16 times larger.
+// (The loop over pairs of 32 is not unrolled: its body stays in the instruction cache.)
 template <int DP, bool MASKED, bool ODD>
 __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow &row, const uint16_t *flags, bool have_o,
                                             uint64_t *o_done, uint32_t parity, int *fault) {
-    uint32_t s[2][32];
+    uint32_t s0[32], s1[32];
     const uint64_t cs2 = pair_f32(row.cs, row.cs);
     uint64_t sum = 0;  // (0, 0)
     bool ok = true;
-    tc_ld32_begin(tS, s[0]);
-#pragma unroll
-    for (int c = 0; c < kPromptTile / 32; ++c) {
-        uint32_t (&x)[32] = s[c & 1];
-        tc_ld_wait(x);
-        if (c + 1 < kPromptTile / 32) tc_ld32_begin(tS + 32 * (c + 1), s[(c + 1) & 1]);
+    auto special = [&](uint32_t (&x)[32], int c) {
         if (ODD || MASKED) {
+            const int lo = row.lo - 32 * c, hi = row.hi - 32 * c;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 if (ODD && (flags[32 * c + i] & 1)) x[i] = __float_as_uint(__uint_as_float(x[i]) * 16.0f);
-                if (32 * c + i > row.hi || 32 * c + i < row.lo) x[i] = 0xFF800000u;
+                if (i > hi || i < lo) x[i] = 0xFF800000u;
             }
         }
+    };
+    auto chunk = [&](uint32_t (&x)[32], uint32_t (&next)[32], int c) {
+        tc_ld_wait(x);
+        if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), next);
+        special(x, c);
         float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
         for (int i = 2; i < 32; i += 2) {
@@ -172,13 +193,16 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
         }
         const float z = fmaxf(t0, t1) * row.cs;
         if (__any_sync(0xFFFFFFFFu, z > row.m + 8.0f)) {
-            if (c + 1 < kPromptTile / 32) tc_ld_wait(s[(c + 1) & 1]);
+            // no score stays in a register meanwhile: they are read again
+            tc_ld_wait(next);
             const float2 part = unpair_f32(sum);
-            float l = row.l + (part.x + part.y), m = row.m;
+            row.l += part.x + part.y;
             sum = 0;
-            ok = prompt_rescale<DP>(tS, tO, 16 * c, m, l, z > m + 8.0f ? z : m, have_o, o_done, parity, fault) && ok;
-            row.l = l;
-            row.m = m;
+            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, z > row.m + 8.0f ? z : row.m, have_o, o_done, parity, fault) && ok;
+            tc_ld32_begin(tS + 32 * c, x);
+            tc_ld_wait(x);
+            if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), next);
+            special(x, c);
         }
         const float mm = row.m == -INFINITY ? 0.0f : -row.m;
         const uint64_t m2 = pair_f32(mm, mm);
@@ -195,10 +219,168 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
             pk[i / 2] = prompt_half2(__floats2half2_rn(e0, e1));
         }
         tc_st16(tS + 16 * c, pk);
+    };
+    tc_ld32_begin(tS, s0);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s1[i] = 0u;  // begun below; named here for the compiler
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        chunk(s0, s1, c);
+        chunk(s1, s0, c + 1);
     }
     const float2 part = unpair_f32(sum);
     row.l += part.x + part.y;
     return ok;
+}
+
+// ---- the work.  An item's place on the line of tiles: kPromptCost, then its own
+
+__device__ __forceinline__ int prompt_pairs(const PromptK &p, int T) { return (T * p.grp + kPromptRows - 1) / kPromptRows; }
+
+// An item's first tile and its tiles (one at least, should it see no key).
+__device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, int rp, int &t0) {
+    const int j_lo = rp * kPromptRows / p.grp, j_hi = min(T - 1, (rp * kPromptRows + kPromptRows - 1) / p.grp);
+    const int pos_lo = len - T + j_lo, pos_hi = len - T + j_hi;
+    t0 = (p.a.window ? max(0, pos_lo - p.a.window + 1) : 0) / kPromptTile;
+    return max(1, pos_hi < 0 ? 0 : pos_hi / kPromptTile + 1 - t0);
+}
+
+// The places of a chunk of 32 sequences, a lane's own, by the whole warp.
+__device__ __forceinline__ long long prompt_places(const PromptK &p, int c, int lane, bool report, SeqInfo &q) {
+    q = seq_info(p.a, c * 32 + lane, report);
+    long long mine = 0;
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, q.T > 0); left; left &= left - 1) {
+        const int l = __ffs(left) - 1;
+        const int len = __shfl_sync(0xFFFFFFFFu, q.len, l), T = __shfl_sync(0xFFFFFFFFu, q.T, l);
+        long long n = 0;
+        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) {
+            int t0;
+            n += prompt_tiles(p, len, T, rp, t0) + kPromptCost;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        if (lane == l) mine = n * p.a.c.nkv;
+    }
+    return mine;
+}
+
+__device__ __forceinline__ void prompt_count(const PromptK &p, int c, int lane, long long *chunk_sum) {
+    SeqInfo q;
+    long long n = prompt_places(p, c, lane, blockIdx.x == 0, q);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    if (lane == 0) chunk_sum[c] = n;
+}
+
+// By warp 0: the chunks' sums become their first places, and the block's share begins
+// at a tile of an item.
+__device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchunks, long long *chunk_sum,
+                                                long long &x0_out, long long &share_out, PromptItem &out) {
+    long long total = 0;
+    for (int c0 = 0; c0 < nchunks; c0 += 32) {
+        const long long n = c0 + lane < nchunks ? chunk_sum[c0 + lane] : 0;
+        long long sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (c0 + lane < nchunks) chunk_sum[c0 + lane] = total + sum - n;
+        total += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    __syncwarp();
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < p.min_share) share = p.min_share;
+    const long long x0 = min(blockIdx.x * share, total);
+    PromptItem it = {};
+    it.count = (int)(min(x0 + share, total) - x0);
+    if (it.count > 0) {
+        int lo = 0, hi = nchunks;  // the chunk that holds place x0
+        while (hi - lo > 1) {
+            const int m = (lo + hi) / 2;
+            if (chunk_sum[m] <= x0) lo = m; else hi = m;
+        }
+        SeqInfo q;
+        const long long n = prompt_places(p, lo, lane, false, q);
+        long long sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const long long before = chunk_sum[lo] + sum - n;
+        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= x0);
+        const int l = 31 - __clz(ok);
+        long long rem = x0 - __shfl_sync(0xFFFFFFFFu, before, l);
+        it.s = lo * 32 + l;
+        it.row = __shfl_sync(0xFFFFFFFFu, q.row, l);
+        it.len = __shfl_sync(0xFFFFFFFFu, q.len, l);
+        it.T = __shfl_sync(0xFFFFFFFFu, q.T, l);
+        it.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, l);
+        const long long per_head = __shfl_sync(0xFFFFFFFFu, n, l) / p.a.c.nkv;
+        it.kvh = (int)(rem / per_head);
+        rem -= it.kvh * per_head;
+        for (int rp0 = 0; rp0 < prompt_pairs(p, it.T); rp0 += 32) {  // the row pair, 32 at a time
+            int t0;
+            const int w = rp0 + lane < prompt_pairs(p, it.T) ? prompt_tiles(p, it.len, it.T, rp0 + lane, t0) + kPromptCost : 0;
+            long long end = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, end, o);
+                if (lane >= o) end += y;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, end > rem);
+            if (past) {
+                const int l2 = __ffs(past) - 1;
+                rem -= __shfl_sync(0xFFFFFFFFu, end - w, l2);
+                it.rp = rp0 + l2;
+                break;
+            }
+            rem -= __shfl_sync(0xFFFFFFFFu, end, 31);
+        }
+        // now `rem` is the place in the item
+        it.u = max(0, (int)rem - kPromptCost);
+        it.place = max(0, kPromptCost - (int)rem);
+    }
+    if (lane == 0) {
+        x0_out = x0;
+        share_out = share;
+        out = it;
+    }
+}
+
+// The block's next piece (n = 0 before the first): false when its share is done.
+__device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptItem &io) {
+    PromptItem it = io;
+    __syncwarp();
+    if (it.place + it.n >= it.count) return false;
+    if (it.n) {  // past the piece before, which ended its item
+        it.place += it.n + kPromptCost;
+        if (it.place >= it.count) return false;
+        it.u = 0;
+        if (++it.rp == prompt_pairs(p, it.T)) {
+            it.rp = 0;
+            if (++it.kvh == p.a.c.nkv) {
+                it.kvh = 0;
+                SeqInfo q;
+                do q = seq_info(p.a, ++it.s, false);
+                while (q.T == 0 && it.s < p.a.s.nseq);
+                it.row = q.row;
+                it.len = q.len;
+                it.T = q.T;
+                it.q0 = q.q0;
+            }
+        }
+    }
+    int t0;
+    const int tiles = prompt_tiles(p, it.len, it.T, it.rp, t0);
+    it.t0 = t0 + it.u;
+    it.rest = tiles - it.u;
+    it.n = min(it.rest, it.count - it.place);
+    it.from_start = it.u == 0;
+    if (lane == 0) io = it;
+    __syncwarp();
+    return true;
 }
 
 template <int DP>
@@ -231,72 +413,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- the items: an item's number counts sequences, row pairs, key heads
-    const int nseq = p.a.s.nseq, nchunks = (nseq + 31) / 32;
-    auto info = [&](int s, bool report) {
-        SeqInfo r = {0, 0, 0, 0};
-        if (s < nseq) r = seq_info(p.a, s, report);
-        return r;
-    };
-    auto row_pairs = [&](int T) { return (T * p.grp + kPromptRows - 1) / kPromptRows; };
-    for (int c = warp; c < nchunks; c += kPromptThreads / 32) {
-        int n = p.a.c.nkv * row_pairs(info(c * 32 + lane, blockIdx.x == 0).T);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-        if (lane == 0) sm.chunk_sum[c] = n;
-    }
+    // ---- the work: the block's share of the line of tiles
+    const int nchunks = (p.a.s.nseq + 31) / 32;
+    for (int c = warp; c < nchunks; c += kPromptThreads / 32) prompt_count(p, c, lane, sm.chunk_sum);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0) {
-        int sum = 0;
-        for (int c = 0; c < nchunks; ++c) {
-            const int n = sm.chunk_sum[c];
-            sm.chunk_sum[c] = sum;
-            sum += n;
-        }
-        sm.chunk_sum[nchunks] = sum;
-    }
+    if (warp == 0) prompt_find(p, lane, nchunks, sm.chunk_sum, sm.x0, sm.share, sm.it[0]);
     __syncthreads();
-    const int total = sm.chunk_sum[nchunks];
+    if (warp > 0 && lane == 0) sm.it[warp] = sm.it[0];
+    __syncthreads();  // warp 0 goes on in its own after the others have copied it
     const uint32_t tb = sm.tmem;
-    // this block's k-th item, the longest first (a sequence's last rows see the most keys), to and fro
-    auto item_at = [&](int k, PromptItem &it) {
-        const int64_t x = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (x >= total) return false;
-        const int idx = total - 1 - (int)x;
-        int lo = 0, hi = nchunks;
-        while (hi - lo > 1) {
-            const int m = (lo + hi) / 2;
-            if (sm.chunk_sum[m] <= idx) lo = m; else hi = m;
-        }
-        const SeqInfo q = info(lo * 32 + lane, false);
-        const int n = p.a.c.nkv * row_pairs(q.T);
-        int sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const int before = sm.chunk_sum[lo] + sum - n;
-        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, n > 0 && before <= idx);
-        const int l = 31 - __clz(ok);
-        const int rem = idx - __shfl_sync(0xFFFFFFFFu, before, l);
-        it.row = __shfl_sync(0xFFFFFFFFu, q.row, l);
-        it.len = __shfl_sync(0xFFFFFFFFu, q.len, l);
-        it.T = __shfl_sync(0xFFFFFFFFu, q.T, l);
-        it.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, l);
-        it.rp = rem / p.a.c.nkv;
-        it.kvh = rem - it.rp * p.a.c.nkv;
-        const int j_lo = it.rp * kPromptRows / p.grp, j_hi = min(it.T - 1, (it.rp * kPromptRows + kPromptRows - 1) / p.grp);
-        const int pos_lo = it.len - it.T + j_lo, pos_hi = it.len - it.T + j_hi;
-        const int first = p.a.window ? max(0, pos_lo - p.a.window + 1) : 0;
-        it.t0 = first / kPromptTile;
-        it.n = pos_hi < 0 ? 0 : pos_hi / kPromptTile + 1 - it.t0;
-        return true;
-    };
-
-    PromptItem it;
+    PromptItem &it = sm.it[warp];
     // 128 registers a thread of 4 warpgroups at launch: 152 + 152 + 104 + 104 = 4 * 128
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
@@ -305,8 +433,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tb + lanes + 128u * q, tO = tb + lanes + 256u + (uint32_t)DP * q;
         uint32_t tiles = 0;  // of this row tile so far
+        int goes_on = -1;
         bool ok = true;
-        for (int k = 0; ok && item_at(k, it); ++k) {
+        while (ok && prompt_next(p, lane, it)) {
             const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
             const bool live = j < it.T;
             const int pos = live ? it.len - it.T + j : -1;
@@ -314,17 +443,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int64_t tok = it.q0 + j;
             const int head = it.kvh * p.grp + rho - j * p.grp;
             float cs = 0.0f;
-            if (it.n > 0) {
+            {
                 // the row's queries as f16, its largest magnitude scaled into [2^14, 2^15)
                 const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + tok * p.a.q_stride + (int64_t)head * p.a.c.d;
-                auto load = [&](int o, float (&x)[8]) {
+                uint4 raw[DP / 8];  // the whole row's loads under way together
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-                    if (!live || o * 8 >= p.a.c.d) return;
-                    if (p.a.type == QB_T_F16) load8<QB_T_F16>(src + o * 8, x); else load8<QB_T_BF16>(src + o * 8, x);
+                for (int o = 0; o < DP / 8; ++o) {
+                    raw[o] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && o * 8 < p.a.c.d) raw[o] = *reinterpret_cast<const uint4 *>(src + o * 8);
+                }
+                const bool f16 = p.a.type == QB_T_F16;
+                auto load = [&](int o, float (&x)[8]) {
+                    if (f16) unpack8<QB_T_F16>(raw[o], x); else unpack8<QB_T_BF16>(raw[o], x);
                 };
                 float top = 0.0f;
-#pragma unroll 4
+#pragma unroll
                 for (int o = 0; o < DP / 8; ++o) {
                     float x[8];
                     load(o, x);
@@ -336,7 +469,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 // not zero, so that a score that is masked stays -inf
                 cs = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f * exp2f((float)(e - 8)), 1e-37f);
                 uint8_t *dst = sm.q[q] + r * 16;
-#pragma unroll 4
+#pragma unroll
                 for (int o = 0; o < DP / 8; ++o) {
                     float x[8];
                     load(o, x);
@@ -357,8 +490,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int first_hi = p.a.window ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
             PromptRow row = {cs, -INFINITY, 0.0f, 0, 0};
             uint32_t bad = 0;
-            for (int i = 0; i < it.n; ++i, ++tiles) {
-                const int k0 = (it.t0 + i) * kPromptTile;
+            const int n_tiles = it.n, t_first = it.t0;
+            for (int i = 0; i < n_tiles; ++i, ++tiles) {
+                const int k0 = (t_first + i) * kPromptTile;
                 if (!(ok = prompt_wait(&sm.s_full[q], tiles & 1, p.a.fault))) break;
                 tc_fence_after();
                 const uint32_t sl = tiles & 3, par = (tiles - 1) & 1;
@@ -382,23 +516,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             }
             const float m = row.m, l = row.l;
             if (!ok) break;
-            if (it.n > 0) {
-                if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
-                tc_fence_after();
-            }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
+            tc_fence_after();
+            const bool whole = it.from_start && it.n == it.rest;
+            const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t rec = (int64_t)(blockIdx.x * 2 + (it.from_start ? 1 : 0)) * kPromptRows + q * kPromptTile + r;
             uint16_t *out = static_cast<uint16_t *>(p.a.out) + tok * p.a.out_stride + (int64_t)head * p.a.c.d;
             // 32 columns are chunks 2kk, 2kk + 1 (W = 4; all four of W = 2's eight dims): eight dims of every group
 #pragma unroll
             for (int kk = 0; kk < DP / 32; ++kk) {
                 uint32_t o[32];
                 __syncwarp();
-                if (it.n > 0) {
-                    tc_ld32(tO + 32 * kk, o);
-                } else {
-#pragma unroll
-                    for (int i2 = 0; i2 < 32; ++i2) o[i2] = 0u;
-                }
+                tc_ld32(tO + 32 * kk, o);
                 // column (c * (W / 2) + u) * 8 + 2 j + h is dim (2 u + h) * 32 + 4 c + j
                 constexpr int CPL = 8 / W;  // chunks in 32 columns
                 if (live) {
@@ -415,17 +544,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                         const int el = G * 32 + kk * 4 * CPL;
 #pragma unroll
                         for (int h = 0; h < 4 * CPL; h += 8) {
-                            if (el + h >= p.a.c.d) continue;
                             const float (&y)[8] = *reinterpret_cast<const float (*)[8]>(&x[h]);
+                            if (!whole) {
+                                store8<QB_T_F32>(p.part + rec * DP + el + h, y);
+                                continue;
+                            }
+                            if (el + h >= p.a.c.d) continue;
                             if (p.a.type == QB_T_F16) store8<QB_T_F16>(out + el + h, y); else store8<QB_T_BF16>(out + el + h, y);
                         }
                     }
                 }
             }
-            if (live && p.a.lse) p.a.lse[tok * p.a.nh + head] = (m + log2f(l)) * 0.6931471805599453f;
+            if (live && !whole) p.stat[rec] = make_float2(m, l);
+            if (live && whole && p.a.lse) p.a.lse[tok * p.a.nh + head] = (m + log2f(l)) * 0.6931471805599453f;
+            if (threadIdx.x == 0 && it.from_start && !whole) {
+                goes_on = (int)((sm.x0 + it.place + it.rest - 1) / sm.share);  // the block that holds the item's last tile
+                p.meta[blockIdx.x] = make_int4(it.q0, it.T, it.kvh, it.rp);
+            }
             __syncwarp();
             tc_fence_before();  // the reads of O, before the next item's products
         }
+        if (threadIdx.x == 0) p.last[blockIdx.x] = ok ? goes_on : -1;
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // ================================================= decoders: a thread a key
@@ -437,7 +576,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         constexpr int NV = DP / 32;  // 16-byte pieces of a row's codes
         uint4 kx[NV], vx[NV];
         uint32_t ks[NG / 2], vs[NG / 2];
-        for (int k = 0; ok && item_at(k, it); ++k) {
+        while (ok && prompt_next(p, lane, it)) {
             auto load = [&](int tile, uint4 (&kc)[NV], uint32_t (&kst)[NG / 2], uint4 (&vc)[NV], uint32_t (&vst)[NG / 2]) {
                 const int key = tile * kPromptTile + r;
                 if (key < it.len) {
@@ -469,7 +608,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     for (int i = 0; i < NG / 2; ++i) kst[i] = vst[i] = 0u;
                 }
             };
-            if (it.n > 0) load(it.t0, kx, ks, vx, vs);
+            load(it.t0, kx, ks, vx, vs);
             for (int i = 0; i < it.n; ++i, ++kt) {
                 const int slot = kt & 1;
                 const uint32_t ph = (kt >> 1) & 1;
@@ -577,8 +716,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             }
             __syncwarp();
         };
-        for (int k = 0; ok && item_at(k, it); ++k) {
-            if (it.n == 0) continue;
+        while (ok && prompt_next(p, lane, it)) {
             for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
             ++items;
             if (!ok || !(ok = prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
@@ -608,16 +746,111 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
     if (warp == 12) tc_dealloc(tb, 512);
 }
 
+constexpr int kJoinRows = 16;  // rows a block of the join
+
+// Joins an item's pieces: block (b, y) has the item that starts at block b of the
+// prompt kernel and goes on, its rows 16 y .. 16 y + 15, two to a warp, their loads
+// under way together; weights 2^(m_i - m), sums in the order of the keys.
+template <int DP>
+__global__ void __launch_bounds__(256, 6) kv4_prompt_join_kernel(const PromptK p) {
+    constexpr int E = DP / 32, RW = kJoinRows / 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    const int last = p.last[b];
+    if (last < 0) return;
+    const int4 it = p.meta[b];
+    const int parts = last - b + 1, row0 = blockIdx.y * kJoinRows + warp * RW;
+    if ((it.w * kPromptRows + row0) / p.grp >= it.y) return;
+    auto rec = [&](int k, int r) { return (int64_t)((b + k) * 2 + (k == 0 ? 1 : 0)) * kPromptRows + row0 + r; };
+    float m[RW], l[RW], acc[RW][E];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = 0.0f;
+    }
+    for (int k = lane; k < parts; k += 32)
+#pragma unroll
+        for (int r = 0; r < RW; ++r) m[r] = fmaxf(m[r], p.stat[rec(k, r)].x);
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m[r] = fmaxf(m[r], __shfl_xor_sync(0xFFFFFFFFu, m[r], o));
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+        float2 st[RW], x[RW][E / 2];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            st[r] = p.stat[rec(k, r)];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                x[r][e] = reinterpret_cast<const float2 *>(p.part + rec(k, r) * DP + lane * E)[e];
+        }
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const float w = prompt_ex2(st[r].x - (m[r] == -INFINITY ? 0.0f : m[r]));
+            l[r] += w * st[r].y;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                acc[r][2 * e] += w * x[r][e].x;
+                acc[r][2 * e + 1] += w * x[r][e].y;
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        const int rho = it.w * kPromptRows + row0 + r, j = rho / p.grp;
+        if (j >= it.y) continue;
+        const int64_t tok = it.x + j;
+        const int head = it.z * p.grp + rho - j * p.grp;
+        const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+        uint16_t *out = static_cast<uint16_t *>(p.a.out) + tok * p.a.out_stride + (int64_t)head * p.a.c.d + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            if (lane * E + e >= p.a.c.d) continue;
+            const float y0 = acc[r][e] * inv, y1 = acc[r][e + 1] * inv;
+            if (p.a.type == QB_T_F16)
+                *reinterpret_cast<__half2 *>(out + e) = __floats2half2_rn(y0, y1);
+            else
+                *reinterpret_cast<__nv_bfloat162 *>(out + e) = __floats2bfloat162_rn(y0, y1);
+        }
+        if (lane == 0 && p.a.lse) p.a.lse[tok * p.a.nh + head] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
+    }
+}
+
+// Byte offsets of the workspace's parts.
+struct PromptWs {
+    int64_t part, stat, meta, last, end;
+};
+inline PromptWs prompt_ws(int64_t grid, int64_t dp) {
+    PromptWs w;
+    w.part = 0;
+    w.stat = w.part + grid * 2 * kPromptRows * dp * 4;
+    w.meta = w.stat + grid * 2 * kPromptRows * 8;
+    w.last = w.meta + grid * 16;
+    w.end = (w.last + grid * 4 + 15) / 16 * 16;
+    return w;
+}
+
 template <int DP>
 int launch_kv4_prompt(const Kv4AttnArgs &a, cudaStream_t stream) {
     PromptK p;
     p.a = a;
     p.grp = a.nh / a.c.nkv;
+    p.min_share = 4;
+    const int grid = attn_grid();
+    const PromptWs w = prompt_ws(grid, DP);
+    p.part = reinterpret_cast<float *>(a.ws + w.part);
+    p.stat = reinterpret_cast<float2 *>(a.ws + w.stat);
+    p.meta = reinterpret_cast<int4 *>(a.ws + w.meta);
+    p.last = reinterpret_cast<int *>(a.ws + w.last);
     constexpr int smem = (int)sizeof(PromptSmem<DP>) + 128;
     auto *f = kv4_prompt_kernel<DP>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
-    return launch_pdl(f, dim3((unsigned)num_sms()), dim3(kPromptThreads), smem, stream, p);
+    if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kPromptThreads), smem, stream, p)) return rc;
+    return launch_pdl(kv4_prompt_join_kernel<DP>, dim3((unsigned)grid, kPromptRows / kJoinRows), dim3(256), 0, stream, p);
 }
 
 }  // namespace qb
-

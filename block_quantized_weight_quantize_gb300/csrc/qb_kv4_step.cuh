@@ -62,9 +62,6 @@ __host__ __device__ constexpr int step_stages(int dp, bool pair, int nt) {
     const int n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp, pair, nt) + 8));
     return n > 8 ? 8 : n;
 }
-constexpr int kMaxGrid = 256;
-inline int step_grid() { return std::min(num_sms(), kMaxGrid); }
-
 // Byte offsets of the workspace's parts.
 struct StepWs {
     int64_t part, stat, cpart, cstat, meta, last, end;
@@ -931,8 +928,8 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 template <int DP, int R>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p, int blocks) {
     constexpr int E = DP / 32;
-    __shared__ int items[kMaxGrid], lasts[kMaxGrid];
-    __shared__ int4 metas[kMaxGrid];
+    __shared__ int items[kAttnMaxGrid], lasts[kAttnMaxGrid];
+    __shared__ int4 metas[kAttnMaxGrid];
     __shared__ int warp_n[8];
     __shared__ float red[8][DP], red_l[8];
     pdl_launch_dependents();
@@ -1042,7 +1039,7 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     StepK p = {};
     p.a = a;
     p.grp = a.nh / a.c.nkv;
-    const int grid = step_grid();
+    const int grid = attn_grid();
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
     // rows a sequence and key head, on average: pairs where they fit one column
     // tile (and for f32 always), two column tiles where one does not hold them
