@@ -195,7 +195,7 @@ __device__ __forceinline__ SeqInfo seq_info(const Kv4AttnArgs &a, int s, bool re
 constexpr int kAttnMaxGrid = 256;
 inline int attn_grid() { return num_sms() < kAttnMaxGrid ? num_sms() : kAttnMaxGrid; }
 
-int64_t kv4_attn_ws(int nkv, int dp, int nh);
+int64_t kv4_attn_ws(int dp);
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream);
 // A few tokens a sequence (qb_kv4_step.cuh), many (qb_kv4_prompt.cuh); by padded head size.
 int launch_kv4_step_64(const Kv4AttnArgs &a, cudaStream_t stream);

@@ -81,7 +81,7 @@ int64_t kv4_attn_workspace_bytes(const qb_kv4 *cache, int nh) {
     if (!cache || cache->nkv < 1 || cache->nkv > 1024 || cache->d < 8 || cache->d > 256 || cache->d % 8 != 0 ||
         nh < 1 || nh > 4096 || nh % cache->nkv != 0)
         return QB_E_ARG;
-    return kv4_attn_ws(cache->nkv, kv4_padded(cache->d), nh);
+    return kv4_attn_ws(kv4_padded(cache->d));
 }
 
 int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void *q, int64_t q_stride,
@@ -95,7 +95,9 @@ int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const vo
         (int64_t)seqs->maxp * cache->page >= (int64_t(1) << 31))
         return QB_E_ARG;
     if (!seqs->rows && seqs->nseq > seqs->nrows) return QB_E_ARG;
-    if (nh < 1 || nh > 4096 || nh % cache->nkv != 0 || ntok < 0 || ntok > (int64_t(1) << 24)) return QB_E_ARG;
+    if (nh < 1 || nh > 4096 || nh % cache->nkv != 0 || ntok < 0 || ntok > (int64_t(1) << 24) ||
+        ntok * nh >= (int64_t(1) << 31))
+        return QB_E_ARG;
     if (!seqs->q_start && ntok != seqs->nseq) return QB_E_ARG;
     const int64_t width = (int64_t)nh * cache->d;
     const int es = type_bytes(type);

@@ -8,9 +8,7 @@
 
 namespace qb {
 
-int64_t kv4_attn_ws(int nkv, int dp, int nh) {
-    (void)nkv;
-    (void)nh;
+int64_t kv4_attn_ws(int dp) {
     int64_t most = 0;
     for (int nt = 1; nt <= 2; ++nt)
         for (int pair = 0; pair < 2; ++pair)

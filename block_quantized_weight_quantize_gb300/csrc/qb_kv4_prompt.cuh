@@ -9,20 +9,31 @@
 // m a running maximum that moves only when it has to rise by more than 8 (the
 // factor 2^8 fits f16), when O is rescaled in tensor memory; sums in f32.
 //
+// A rounded key moves a score by 2^-12 of its terms, which averages out over many
+// keys but not over few: lse is off by 1e-5 to 2e-5 of itself at 100 keys, 3e-6 at
+// 500.  Where a row of an item sees fewer than kPromptFine keys, what the rounding
+// leaves is decoded too (one multiply-add, exact) and multiplied by Q into the same
+// scores: 1e-7 then.  It costs 5 to 10% (2048 tokens by themselves, 32 heads of
+// 128: 98 -> 108 us; 512 on 4096 keys 68 -> 82); the output keeps the error of
+// values and probabilities in f16, 3.4e-4 of an f16 output, 2.1e-4 of it the output's own
+// rounding.
+//
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
 // head + head) of one sequence and key head, over the tiles of 128 keys that they
 // see.  Tiles are counted along all items, one more for an item's own cost; every
 // block takes the same count of consecutive ones.  An item that blocks share
 // leaves its rows' sums in the workspace, joined by kv4_prompt_join_kernel.
 // (Whole items to a block: 258 us for 2048 tokens on 8192 keys, 32 heads of 128,
-// 256 items on 152 multiprocessors; @JOIN@.)
-// Roles of a block's 13 warps (128 registers a thread):
+// 256 items on 152 multiprocessors; shared ones 254 us with their join.  With few
+// items it is what fills the card.)
+// Roles of a block's 16 warps (152 registers a thread in warps 0-7, 104 in the
+// others: 2 * 152 + 2 * 104 = the 4 * 128 of the launch):
 //   0-3, 4-7  softmax of tile 0, 1: a thread a row, 32 scores at a time from
 //             tensor memory, P back over the scores
 //   8-11      decoders: a thread a key, rows loaded a tile ahead into
 //             registers, f16 core matrices (8 rows of 16 bytes) to shared memory
 //   12        issues the products: PV0(i), S0(i+1), then PV1(i), S1(i+1), so that
-//             one tile's softmax runs under the other tile's products
+//             one tile's softmax runs under the other tile's products; 13-15 idle
 // Core matrices: K [dims/8][128 keys][8 dims] (K-major), V the same (dims along
 // N: MN-major), Q like K; the order of dims within and of groups of eight is the one
 // that unpacking gives, and is undone in Q's rows and the output's columns.
@@ -32,6 +43,8 @@
 // is not finite is decoded as zeros and marks the rows that see it, whose
 // outputs of that group are NaN.
 #pragma once
+
+#include <type_traits>
 
 #include "qb_kv4.cuh"
 #include "qb_tcgen05.cuh"
@@ -62,8 +75,10 @@ struct PromptItem {
     int place, rest;     // of the piece's first tile in the block's share; tiles of the item from there on
     int count;           // places of the block's share
     int from_start;
+    int fine;            // keys as two f16
 };
 
+constexpr int kPromptFine = 4096;  // keys; see above
 constexpr int kPromptCost = 1;  // what an item costs beside its tiles, in tiles
 
 template <int DP>
@@ -94,7 +109,19 @@ __device__ __forceinline__ uint4 prompt_decode(const CentreK &ck, uint32_t w, __
     const uint32_t b[4] = {centre_lo(ck, w), centre_hi(ck, w), centre_lo(ck, w >> 8), centre_hi(ck, w >> 8)};
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = prompt_half2(__hmul2(*reinterpret_cast<const __half2 *>(&b[i]), step));
+    for (int i = 0; i < 4; ++i) o[i] = prompt_half2(__hmul2_rn(*reinterpret_cast<const __half2 *>(&b[i]), step));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// What that rounding left, exactly.
+__device__ __forceinline__ uint4 prompt_decode_rest(const CentreK &ck, uint32_t w, __half2 step) {
+    const uint32_t b[4] = {centre_lo(ck, w), centre_hi(ck, w), centre_lo(ck, w >> 8), centre_hi(ck, w >> 8)};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 c = *reinterpret_cast<const __half2 *>(&b[i]);
+        o[i] = prompt_half2(__hfma2(c, step, __hneg2(__hmul2_rn(c, step))));
+    }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -378,6 +405,8 @@ __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptIt
     it.rest = tiles - it.u;
     it.n = min(it.rest, it.count - it.place);
     it.from_start = it.u == 0;
+    const int seen = it.len - it.T + it.rp * kPromptRows / p.grp + 1;  // by the first row
+    it.fine = (p.a.window ? min(seen, p.a.window) : seen) < kPromptFine;
     if (lane == 0) io = it;
     __syncwarp();
     return true;
@@ -571,7 +600,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         const CentreK ck;
         const int r = threadIdx.x - 8 * 32, dw = warp - 8;
         const int page = p.a.c.page, code_bytes = page * DP / 2, step_bytes = page * DP / 16;
-        uint32_t kt = 0;
+        uint32_t kt = 0, fill = 0;  // key tiles, fills of K's buffers so far
         bool ok = true;
         constexpr int NV = DP / 32;  // 16-byte pieces of a row's codes
         uint4 kx[NV], vx[NV];
@@ -609,6 +638,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 }
             };
             load(it.t0, kx, ks, vx, vs);
+            const bool fine = it.fine != 0;
             for (int i = 0; i < it.n; ++i, ++kt) {
                 const int slot = kt & 1;
                 const uint32_t ph = (kt >> 1) & 1;
@@ -646,26 +676,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                         if (fl & 2u) b = __hmul2(b, sixteenth);
                     }
                 }
-                if (!(ok = prompt_wait(&sm.k_free[slot], ph ^ 1u, p.a.fault))) break;
+                if (!(ok = prompt_wait(&sm.k_free[fill & 1], (fill >> 1 & 1) ^ 1u, p.a.fault))) break;
                 // the tile's flags: three tiles at most are in use, four are held
                 sm.flags[kt & 3][r] = (uint16_t)fl;
                 const uint32_t any = __ballot_sync(0xFFFFFFFFu, fl != 0);
                 if (lane == 0) sm.any[kt & 3][dw] = any;
-                uint8_t *dst = sm.k[slot] + r * 16;
+                uint8_t *dst = sm.k[fill & 1] + r * 16;
+                auto keys = [&](auto rest) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int gi = 0; gi < W; ++gi) {
-                        const int wi = t * W + gi;  // the row's word: elements 8 t .. of group gi
-                        const uint4 &u = kc[wi / 4];
-                        const uint32_t w = wi % 4 == 0 ? u.x : wi % 4 == 1 ? u.y : wi % 4 == 2 ? u.z : u.w;
-                        const __half2 sp = *reinterpret_cast<const __half2 *>(&kst[gi / 2]);
-                        *reinterpret_cast<uint4 *>(dst + (gi * 4 + t) * kOctStride) =
-                            prompt_decode(ck, w, (gi & 1) ? __high2half2(sp) : __low2half2(sp));
+                        for (int gi = 0; gi < W; ++gi) {
+                            const int wi = t * W + gi;  // the row's word: elements 8 t .. of group gi
+                            const uint4 &u = kc[wi / 4];
+                            const uint32_t w = wi % 4 == 0 ? u.x : wi % 4 == 1 ? u.y : wi % 4 == 2 ? u.z : u.w;
+                            const __half2 sp = *reinterpret_cast<const __half2 *>(&kst[gi / 2]);
+                            const __half2 step = (gi & 1) ? __high2half2(sp) : __low2half2(sp);
+                            *reinterpret_cast<uint4 *>(dst + (gi * 4 + t) * kOctStride) =
+                                decltype(rest)::value ? prompt_decode_rest(ck, w, step) : prompt_decode(ck, w, step);
+                        }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.k_full[fill & 1]);
+                    ++fill;
+                };
+                keys(std::false_type());
+                if (fine) {
+                    if (!(ok = prompt_wait(&sm.k_free[fill & 1], (fill >> 1 & 1) ^ 1u, p.a.fault))) break;
+                    dst = sm.k[fill & 1] + r * 16;
+                    if (fl & 1u) {  // an infinite step leaves nothing
+#pragma unroll
+                        for (int h = 0; h < NG / 2; ++h) {
+                            if ((kst[h] & 0x7C00u) == 0x7C00u) kst[h] &= 0xFFFF0000u;
+                            if ((kst[h] & 0x7C000000u) == 0x7C000000u) kst[h] &= 0x0000FFFFu;
+                        }
                     }
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.k_full[slot]);
+                    // decoded anew: what is common to both passes would not fit the registers
+#pragma unroll
+                    for (int t = 0; t < NV; ++t)
+                        asm volatile("" : "+r"(kc[t].x), "+r"(kc[t].y), "+r"(kc[t].z), "+r"(kc[t].w));
+                    keys(std::true_type());
+                }
                 if (!(ok = prompt_wait(&sm.v_free[slot], ph ^ 1u, p.a.fault))) break;
                 dst = sm.v[slot] + r * 16;
                 const int swz = 4 * ((rr >> 1) & 1);
@@ -688,20 +739,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // ================================================= products
         const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
-        uint32_t kt = 0, items = 0;  // key tiles, items so far
+        uint32_t kt = 0, fill = 0, items = 0;  // key tiles, fills of K's buffers, items so far
         bool ok = warp == 12;
-        // S = Q K^T with key tile t
-        auto scores = [&](int q, uint32_t t) {
-            const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[t & 1]);
+        // S = Q K^T with the key tile of fill f (and f + 1, what its rounding left)
+        auto scores = [&](int q, uint32_t f, auto fine_t) {
+            constexpr bool fine = decltype(fine_t)::value;
+            const uint32_t qa = smem_u32(sm.q[q]);
             if (elect_one()) {
+                const uint32_t ka = smem_u32(sm.k[f & 1]);
 #pragma unroll
                 for (int s = 0; s < DP / 16; ++s)
                     tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
                               tc_desc(ka + 2 * s * kOctStride, kOctStride, 128), idS, s != 0);
+                if (fine) {
+                    const uint32_t kb = smem_u32(sm.k[(f + 1) & 1]);
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s)
+                        tc_mma_ss(tb + 128u * q, tc_desc(qa + 2 * s * kOctStride, kOctStride, 128),
+                                  tc_desc(kb + 2 * s * kOctStride, kOctStride, 128), idS, true);
+                }
                 tc_commit(&sm.s_full[q]);
-                if (q == kPromptQ - 1) tc_commit(&sm.k_free[t & 1]);
+                if (q == kPromptQ - 1) {
+                    tc_commit(&sm.k_free[f & 1]);
+                    if (fine) tc_commit(&sm.k_free[(f + 1) & 1]);
+                }
             }
             __syncwarp();
+        };
+        auto keys_there = [&](uint32_t f, auto fine_t) {
+            return prompt_wait(&sm.k_full[f & 1], f >> 1 & 1, p.a.fault) &&
+                   (!decltype(fine_t)::value || prompt_wait(&sm.k_full[(f + 1) & 1], (f + 1) >> 1 & 1, p.a.fault));
         };
         // O (+)= P V
         auto outputs = [&](int q, uint32_t t, bool first) {
@@ -716,28 +783,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             }
             __syncwarp();
         };
-        while (ok && prompt_next(p, lane, it)) {
-            for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
-            ++items;
-            if (!ok || !(ok = prompt_wait(&sm.k_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
+        auto item = [&](auto fine) {
+            constexpr uint32_t step = decltype(fine)::value ? 2 : 1;
+            if (!(ok = keys_there(fill, fine))) return;
             tc_fence_after();
-            for (int q = 0; q < kPromptQ; ++q) scores(q, kt);
-            for (int i = 0; ok && i < it.n; ++i, ++kt) {
+            for (int q = 0; q < kPromptQ; ++q) scores(q, fill, fine);
+            for (int i = 0; i < it.n; ++i, ++kt, fill += step) {
                 const bool more = i + 1 < it.n;
-                if (!(ok = prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault))) break;
-                if (more && !(ok = prompt_wait(&sm.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, p.a.fault))) break;
+                if (!(ok = prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault))) return;
+                if (more && !(ok = keys_there(fill + step, fine))) return;
                 for (int q = 0; q < kPromptQ; ++q) {
-                    if (!(ok = prompt_wait(&sm.p_ready[q], kt & 1, p.a.fault))) break;
+                    if (!(ok = prompt_wait(&sm.p_ready[q], kt & 1, p.a.fault))) return;
                     tc_fence_after();
                     outputs(q, kt, i == 0);
                     if (!more) continue;
                     // products with different accumulators are not ordered: the next scores,
                     // which go where P is, wait until it has been read
-                    if (!(ok = prompt_wait(&sm.o_done[q], kt & 1, p.a.fault))) break;
+                    if (!(ok = prompt_wait(&sm.o_done[q], kt & 1, p.a.fault))) return;
                     tc_fence_after();
-                    scores(q, kt + 1);
+                    scores(q, fill + step, fine);
                 }
             }
+        };
+        while (ok && prompt_next(p, lane, it)) {
+            for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
+            ++items;
+            if (!ok) break;
+            if (it.fine) item(std::true_type());
+            else item(std::false_type());
         }
     }
     tc_fence_before();

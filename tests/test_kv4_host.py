@@ -96,6 +96,16 @@ def test_attention_arguments():
     assert k is not None
 
 
+def test_attention_refuses_more_rows_than_an_int_counts():
+    c = ctypes.addressof(k := _cache())
+    s = _seqs(q_start=A)
+    need = kv4._c.kv4_attn_workspace_bytes(c, 4096)
+    assert need > 0
+    for ntok, nh in ((1 << 24, 128), ((1 << 24) + 1, 4), (1 << 19, 4096)):
+        assert kv4._c.kv4_attn(c, ctypes.addressof(s), 0, A, nh * 64, ntok, nh, 1.0, 0, A, nh * 64, None, A, need, None) == qb.QB_E_ARG
+    assert k is not None
+
+
 def test_page_arguments():
     good = _pages()
     p = ctypes.addressof(good)
