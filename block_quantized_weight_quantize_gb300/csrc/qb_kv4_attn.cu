@@ -10,16 +10,24 @@ namespace qb {
 
 int64_t kv4_attn_ws(int dp) {
     int64_t most = 0;
-    for (int nt = 1; nt <= 2; ++nt)
-        for (int pair = 0; pair < 2; ++pair)
-            most = std::max(most, step_ws(attn_grid(), step_warps(dp, pair != 0, nt), step_rows(pair != 0, nt), dp).end);
+    for (int pair = 0; pair < 2; ++pair)
+        most = std::max(most, step_ws(attn_grid(), step_warps(dp), step_rows(pair != 0), dp).end);
     if (dp <= 128) most = std::max(most, prompt_ws(attn_grid(), dp).end);
     return most;
 }
 
 // Rows (token, query head) a sequence and key head, on average, from which the
-// prompt kernel takes a half-precision call.
-constexpr int kPromptFrom = 64;
+// prompt kernel takes a half-precision call: its items have 256 rows, the step
+// kernel's 8, which read and decode the keys anew.  Step against prompt kernel, us,
+// heads of 128, 32 on 8 key heads, in bf16:
+//     rows                        64          96          128         192
+//     1 sequence of 2000 keys     18 / 33     20 / 35     22 / 36     27 / 38
+//     1 of 8000                   30 / 32     38 / 33     45 / 34     61 / 36
+//     8 of 2000                   37 / 58     51 / 59     58 / 60     90 / 61
+//     8 of 8000                   99 / 96     149 / 99    176 / 101   290 / 106
+//     64 of 300                   55 / 127    77 / 115    96 / 114    122 / 114
+//     64 of 2000                  191 / 324   277 / 327   339 / 326   509 / 311
+constexpr int kPromptFrom = 128;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)

@@ -11,7 +11,8 @@
 //
 // Operands.  The codes are the A side (16 keys, or 16 of the value's elements, by
 // 16), the rows the 8 columns of the B side, since a step has few rows: 4 rows as
-// pairs (high part, low part) in f32 or where there are no more, else 8 rows.  Codes become f16
+// pairs (high part, low part) in f32 or where there are no more, else 8 rows; of more rows
+// there are more tiles, each with the keys anew.  Codes become f16
 // without a conversion: a code in the low bits of an f16 is the subnormal
 // c * 2^-24, exact, and 1024 + c is one OR away.  Half-precision keys take the
 // first where there are 8 rows, with -8 * sum of the queries as the sums'
@@ -29,7 +30,7 @@
 // Rows of 8 are keys in the order 0 7 1 6 2 5 3 4 (row 2t: key t, 2t + 1: key
 // 7 - t), which keeps both loads free of bank conflicts.
 //
-// Work.  Units of 32 or 64 keys of one (sequence, key head, row tile), counted along
+// Work.  Units of 32 keys of one (sequence, key head, row tile), counted along
 // the whole batch with 64 keys' worth more for an item's own cost; every block takes the
 // same count of consecutive units whatever the sequences' lengths are, its warps
 // the same count of those, and each warp streams its own through a ring of bulk copies (a page's block of a
@@ -48,18 +49,19 @@ namespace qb {
 
 constexpr int kSeqChunk = 32;   // sequences summed together in a block's table
 
-// Rows (token, query head) of a row tile: nt column tiles of 4 rows, as pairs of
-// high and low part, or of 8 rows.
-__host__ __device__ constexpr int step_rows(bool pair, int nt) { return (pair ? 4 : 8) * nt; }
-// Keys of a unit, and warps of a block (one a multiprocessor), by the registers
-// that a lane's sums (dp / 4 * nt of them), queries and scores take.
-__host__ __device__ constexpr int step_unit(int dp, bool pair, int nt) { return pair && dp * nt <= 128 ? 64 : 32; }
-__host__ __device__ constexpr int step_warps(int dp, bool pair, int nt) { return dp * nt > 128 ? 8 : 12; }
-__host__ __device__ constexpr int step_unit_bytes(int dp, bool pair, int nt) { return kv4_block(step_unit(dp, pair, nt), dp); }
+// Rows (token, query head) of a row tile: 4, as pairs of high and low part, or 8.
+__host__ __device__ constexpr int step_rows(bool pair) { return pair ? 4 : 8; }
+// Keys of a unit.  (64 where a lane's registers hold them: 256 steps on 1000 keys in
+// f32, 32 heads of 128, 8 key heads 114 us against 87; one on 16000 15.6 against 16.3.)
+constexpr int kUnit = 32;
+// Warps of a block (one a multiprocessor), by the registers that a lane's sums
+// (dp / 4) and queries take.
+__host__ __device__ constexpr int step_warps(int dp) { return dp > 128 ? 8 : 12; }
+__host__ __device__ constexpr int step_unit_bytes(int dp) { return kv4_block(kUnit, dp); }
 // Units a warp's ring holds: what the 227 KB a block may have leave beside its tables (2072 bytes, 548 a warp, 8 a unit).
-__host__ __device__ constexpr int step_stages(int dp, bool pair, int nt) {
-    const int w = step_warps(dp, pair, nt);
-    const int n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp, pair, nt) + 8));
+__host__ __device__ constexpr int step_stages(int dp) {
+    const int w = step_warps(dp);
+    const int n = (232448 - 2072 - w * 548) / (w * (step_unit_bytes(dp) + 8));
     return n > 8 ? 8 : n;
 }
 // Byte offsets of the workspace's parts.
@@ -202,12 +204,12 @@ __device__ __forceinline__ void step_store(const StepK &p, const float (&acc)[E]
     if (lane == 0 && p.a.lse) p.a.lse[(int64_t)tok * p.a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int DP, bool PAIR, int NT, int SB>
-__global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_kernel(const StepK p) {
-    constexpr int kWarps = step_warps(DP, PAIR, NT), kStages = step_stages(DP, PAIR, NT);
-    constexpr int U = step_unit(DP, PAIR, NT), kBytes = step_unit_bytes(DP, PAIR, NT), NB = U / 16;
+template <int DP, bool PAIR, int SB>
+__global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const StepK p) {
+    constexpr int kWarps = step_warps(DP), kStages = step_stages(DP);
+    constexpr int U = kUnit, kBytes = step_unit_bytes(DP), NB = U / 16;
     constexpr int kItemCost = 64 / U;  // what an item costs beside its units (its queries, its output), in units
-    constexpr int R = step_rows(PAIR, NT), RT = R / NT, NH = PAIR ? 1 : 2;  // rows: of a tile, a column tile, a lane's
+    constexpr int R = step_rows(PAIR), NH = PAIR ? 1 : 2;  // rows: of a tile, a lane's
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;         // groups, groups a plane, planes
     constexpr int kSub = kv4_block(SB, DP);                               // a sub-block of SB rows in shared memory
     constexpr int kCodes = SB * DP / 2, kSteps = SB * DP / 16, kPlane = SB * 16 * W;
@@ -452,78 +454,75 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const bool to_end = units == item_left;
 
         // the queries as B fragments: column g of tile n is a row (half precision) or a row's high or low part (f32)
-        uint32_t B[NT][NG][2][2];
-        float cinit[NT][NG][PAIR ? 1 : 2], cs[NT][NH];
+        uint32_t B[NG][2][2];
+        float cinit[NG][PAIR ? 1 : 2], cs[NH];
+        const int rho = s_rt * R + (PAIR ? g >> 1 : g), j = rho / p.grp;
+        const bool live = j < s_T;
+        const int64_t at = (int64_t)(s_q0 + j) * p.a.q_stride + (int64_t)(s_kvh * p.grp + rho - j * p.grp) * p.a.c.d;
+        auto load = [&](int G, float (&x)[8]) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int rho = s_rt * R + n * RT + (PAIR ? g >> 1 : g), j = rho / p.grp;
-            const bool live = j < s_T;
-            const int64_t at = (int64_t)(s_q0 + j) * p.a.q_stride + (int64_t)(s_kvh * p.grp + rho - j * p.grp) * p.a.c.d;
-            auto load = [&](int G, float (&x)[8]) {
+            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            const int el = G * 32 + t * 8;
+            if (!live || el >= p.a.c.d) return;
+            if (PAIR && p.a.type == QB_T_F32) {
+                load8<QB_T_F32>(static_cast<const float *>(p.a.q) + at + el, x);
+            } else {
+                const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at + el;
+                if (p.a.type == QB_T_F16) load8<QB_T_F16>(q, x); else load8<QB_T_BF16>(q, x);
+            }
+        };
+        float xs[NG][8], top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-                const int el = G * 32 + t * 8;
-                if (!live || el >= p.a.c.d) return;
-                if (PAIR && p.a.type == QB_T_F32) {
-                    load8<QB_T_F32>(static_cast<const float *>(p.a.q) + at + el, x);
-                } else {
-                    const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at + el;
-                    if (p.a.type == QB_T_F16) load8<QB_T_F16>(q, x); else load8<QB_T_BF16>(q, x);
+        for (int G = 0; G < NG; ++G) load(G, xs[G]);
+#pragma unroll
+        for (int G = 0; G < NG; ++G)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(xs[G][i]));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // the row's largest magnitude into [2^14, 2^15)
+        const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 14;
+        const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        // undone in the scores, with the codes' 2^-24 where they stand as subnormals
+        const float back = p.a.scale * 1.4426950408889634f * exp2f((float)(e - 14 + (PAIR ? 0 : 24)));
+#pragma unroll
+        for (int h = 0; h < NH; ++h) cs[h] = __shfl_sync(0xFFFFFFFFu, back, PAIR ? 8 * t : 8 * t + 4 * h);
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+            float (&x)[8] = xs[G];
+            float sum = 0.0f;
+            uint32_t h2[4];
+            // a pair's high part is cut to f16's 11 bits, its low part what is left
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = x[i] * f;
+                const float hi = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
+                x[i] = !PAIR ? y : (g & 1) ? y - hi : hi;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h2[i] = pack_f16(x[i], x[i + 4]);
+            if constexpr (!PAIR) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = unpack_f16(h2[i]);
+                    sum += u.x + u.y;
                 }
-            };
-            float xs[NG][8], top = 0.0f;
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                sum *= -8.0f / 16777216.0f;
 #pragma unroll
-            for (int G = 0; G < NG; ++G) load(G, xs[G]);
+                for (int h = 0; h < 2; ++h) cinit[G][h] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * h);
+                // as subnormals, every second code stands as 16 c * 2^-24
 #pragma unroll
-            for (int G = 0; G < NG; ++G)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(xs[G][i]));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // the row's largest magnitude into [2^14, 2^15)
-            const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 14;
-            const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            // undone in the scores, with the codes' 2^-24 where they stand as subnormals
-            const float back = p.a.scale * 1.4426950408889634f * exp2f((float)(e - 14 + (PAIR ? 0 : 24)));
-#pragma unroll
-            for (int h = 0; h < NH; ++h) cs[n][h] = __shfl_sync(0xFFFFFFFFu, back, PAIR ? 8 * t : 8 * t + 4 * h);
-#pragma unroll
-            for (int G = 0; G < NG; ++G) {
-                float (&x)[8] = xs[G];
-                float sum = 0.0f;
-                uint32_t h2[4];
-                // a pair's high part is cut to f16's 11 bits, its low part what is left
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = x[i] * f;
-                    const float hi = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
-                    x[i] = !PAIR ? y : (g & 1) ? y - hi : hi;
+                for (int i = 1; i < 4; i += 2) {
+                    __half2 &u = *reinterpret_cast<__half2 *>(&h2[i]);
+                    u = __hmul2(u, __float2half2_rn(0.0625f));
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h2[i] = pack_f16(x[i], x[i + 4]);
-                if constexpr (!PAIR) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 u = unpack_f16(h2[i]);
-                        sum += u.x + u.y;
-                    }
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                    sum *= -8.0f / 16777216.0f;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) cinit[n][G][h] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * h);
-                    // as subnormals, every second code stands as 16 c * 2^-24
-#pragma unroll
-                    for (int i = 1; i < 4; i += 2) {
-                        __half2 &u = *reinterpret_cast<__half2 *>(&h2[i]);
-                        u = __hmul2(u, __float2half2_rn(0.0625f));
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    B[n][G][m][0] = h2[2 * m];
-                    B[n][G][m][1] = h2[2 * m + 1];
-                }
+            for (int m = 0; m < 2; ++m) {
+                B[G][m][0] = h2[2 * m];
+                B[G][m][1] = h2[2 * m + 1];
             }
         }
         // units whose keys every row sees need no mask
@@ -532,25 +531,22 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const int first_hi = p.a.window ? max(0, pos_hi - p.a.window + 1) : 0;
         const int first_lo = p.a.window ? max(0, pos_lo - p.a.window + 1) : 0;
 
-        float O[NT][NG][2][4];
-        float m[NT][NH], l[NT][NH];
+        float O[NG][2][4];
+        float m[NH], l[NH];
         int eb = 1;  // biased exponent (binary16's) of the largest step so far
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int G = 0; G < NG; ++G)
 #pragma unroll
-            for (int G = 0; G < NG; ++G)
+            for (int i = 0; i < 8; ++i) O[G][i / 4][i % 4] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) O[n][G][i / 4][i % 4] = 0.0f;
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                m[n][h] = -INFINITY;
-                l[n][h] = 0.0f;
-            }
+        for (int h = 0; h < NH; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.0f;
         }
 
         auto unit = [&](const uint8_t *ub, int k0, auto masked) {
             // ---- scores: key krow + 16 b + 8 i, this lane's rows
-            float z[NT][NB][2][NH];
+            float z[NB][2][NH];
             uint32_t vs[NB][2][NG / 2];  // the values' steps of the same keys
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -562,9 +558,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                     lds<NG / 2>(kb + kCodes + (r0 + 8 * i + krow) * NG * 2, st[i]);
                     lds<NG / 2>(kb + 2 * kCodes + kSteps + (r0 + 8 * i + krow) * NG * 2, vs[b][i]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int h = 0; h < NH; ++h) z[n][b][i][h] = 0.0f;
+                    for (int h = 0; h < NH; ++h) z[b][i][h] = 0.0f;
                 }
 #pragma unroll
                 for (int pl = 0; pl < NP; ++pl) {
@@ -574,7 +568,7 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 #pragma unroll
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
-                        float acc[NT][4];
+                        float acc[4];
 #pragma unroll
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t x0 = mm ? w0[gi] >> 8 : w0[gi], x1 = mm ? w1[gi] >> 8 : w1[gi];
@@ -590,30 +584,25 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                                 a2 = x0 & 0x00F000F0u;
                                 a3 = x1 & 0x00F000F0u;
                             }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                if (mm == 0) {
-                                    const float c0 = PAIR ? 0.0f : cinit[n][G][0], c1 = PAIR ? 0.0f : cinit[n][G][PAIR ? 0 : 1];
-                                    mma_f16(acc[n], a0, a1, a2, a3, B[n][G][0][0], B[n][G][0][1], c0, c1, c0, c1);
-                                } else {
-                                    mma_f16(acc[n], a0, a1, a2, a3, B[n][G][1][0], B[n][G][1][1]);
-                                }
+                            if (mm == 0) {
+                                const float c0 = PAIR ? 0.0f : cinit[G][0], c1 = PAIR ? 0.0f : cinit[G][PAIR ? 0 : 1];
+                                mma_f16(acc, a0, a1, a2, a3, B[G][0][0], B[G][0][1], c0, c1, c0, c1);
+                            } else {
+                                mma_f16(acc, a0, a1, a2, a3, B[G][1][0], B[G][1][1]);
                             }
                         }
                         const float2 d0 = unpack_f16(st[0][G / 2]), d1 = unpack_f16(st[1][G / 2]);
                         const float s0 = (G & 1) ? d0.y : d0.x, s1 = (G & 1) ? d1.y : d1.x;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int h = PAIR ? 0 : c;
-                                z[n][b][0][h] = fmaf(s0, acc[n][c], z[n][b][0][h]);
-                                z[n][b][1][h] = fmaf(s1, acc[n][2 + c], z[n][b][1][h]);
-                            }
+                        for (int c = 0; c < 2; ++c) {
+                            const int h = PAIR ? 0 : c;
+                            z[b][0][h] = fmaf(s0, acc[c], z[b][0][h]);
+                            z[b][1][h] = fmaf(s1, acc[2 + c], z[b][1][h]);
+                        }
                     }
                 }
             }
-            uint32_t seen[NT][NH];  // bit 2 b + i: the row sees that key
+            uint32_t seen[NH];  // bit 2 b + i: the row sees that key
             if constexpr (masked) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
@@ -624,19 +613,17 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                             for (int h = 0; h < NG / 2; ++h) vs[b][i][h] = 0;
                         }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int h = 0; h < NH; ++h) {
+                    const int j = (s_rt * R + (PAIR ? t : 2 * t + h)) / p.grp;
+                    const int pos = j < s_T ? s_len - s_T + j : -1;
+                    const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
+                    seen[h] = 0;
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        const int j = (s_rt * R + n * RT + (PAIR ? t : 2 * t + h)) / p.grp;
-                        const int pos = j < s_T ? s_len - s_T + j : -1;
-                        const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
-                        seen[n][h] = 0;
-#pragma unroll
-                        for (int k = 0; k < 2 * NB; ++k) {
-                            const int key = k0 + 8 * k + krow;
-                            if (key >= first && key <= pos) seen[n][h] |= 1u << k;
-                        }
+                    for (int k = 0; k < 2 * NB; ++k) {
+                        const int key = k0 + 8 * k + krow;
+                        if (key >= first && key <= pos) seen[h] |= 1u << k;
                     }
+                }
             }
             // ---- the running maximum and the steps' largest exponent; both rarely move
             __half2 top2 = __float2half2_rn(0.0f);
@@ -659,61 +646,54 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
                     }
             }
             bool moved = (int)(tb >> 10) > eb;
-            float top[NT][NH];
+            float top[NH];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int h = 0; h < NH; ++h) {
+                top[h] = m[h];
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    top[n][h] = m[n][h];
-#pragma unroll
-                    for (int k = 0; k < 2 * NB; ++k) {
-                        float y = z[n][k >> 1][k & 1][h] * cs[n][h];
-                        if constexpr (masked) {
-                            if (!(seen[n][h] >> k & 1)) y = -INFINITY;
-                        }
-                        z[n][k >> 1][k & 1][h] = y;
-                        top[n][h] = fmaxf(top[n][h], y);
+                for (int k = 0; k < 2 * NB; ++k) {
+                    float y = z[k >> 1][k & 1][h] * cs[h];
+                    if constexpr (masked) {
+                        if (!(seen[h] >> k & 1)) y = -INFINITY;
                     }
-                    moved |= top[n][h] > m[n][h];
+                    z[k >> 1][k & 1][h] = y;
+                    top[h] = fmaxf(top[h], y);
                 }
+                moved |= top[h] > m[h];
+            }
             if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) tb = max(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, o));
                 const int eb_new = max(eb, (int)(tb >> 10));
                 const float fe = __uint_as_float((uint32_t)(127 + eb - eb_new) << 23);
                 eb = eb_new;
+                float f[NH];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float f[NH];
+                for (int h = 0; h < NH; ++h) {
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-#pragma unroll
-                        for (int o = 4; o <= 16; o <<= 1)
-                            top[n][h] = fmaxf(top[n][h], __shfl_xor_sync(0xFFFFFFFFu, top[n][h], o));
-                        f[h] = top[n][h] == m[n][h] ? 1.0f : ex2(m[n][h] - top[n][h]);
-                        l[n][h] *= f[h];
-                        f[h] *= fe;
-                        m[n][h] = top[n][h];
-                    }
-#pragma unroll
-                    for (int G = 0; G < NG; ++G)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) O[n][G][i / 4][i % 4] *= f[PAIR ? 0 : i & 1];
+                    for (int o = 4; o <= 16; o <<= 1)
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], o));
+                    f[h] = top[h] == m[h] ? 1.0f : ex2(m[h] - top[h]);
+                    l[h] *= f[h];
+                    f[h] *= fe;
+                    m[h] = top[h];
                 }
+#pragma unroll
+                for (int G = 0; G < NG; ++G)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) O[G][i / 4][i % 4] *= f[PAIR ? 0 : i & 1];
             }
             const float pe = __uint_as_float((uint32_t)(127 + 28 - eb) << 23);  // |step| * pe < 2^14
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int h = 0; h < NH; ++h) {
+                const float mm = m[h] == -INFINITY ? 0.0f : m[h];
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const float mm = m[n][h] == -INFINITY ? 0.0f : m[n][h];
-#pragma unroll
-                    for (int k = 0; k < 2 * NB; ++k) {
-                        const float e = ex2(z[n][k >> 1][k & 1][h] - mm);
-                        l[n][h] += e;
-                        z[n][k >> 1][k & 1][h] = e * pe;
-                    }
+                for (int k = 0; k < 2 * NB; ++k) {
+                    const float e = ex2(z[k >> 1][k & 1][h] - mm);
+                    l[h] += e;
+                    z[k >> 1][k & 1][h] = e * pe;
                 }
+            }
 
             // ---- the values' codes times probabilities times steps
 #pragma unroll
@@ -729,33 +709,30 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
 #pragma unroll
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
-                        uint32_t x[NT][2];
+                        uint32_t x[2];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float2 d2 = unpack_f16(vs[b][i][G / 2]);
-                                const float d = (G & 1) ? d2.y : d2.x;
-                                float x0 = z[n][b][i][0] * d, x1 = PAIR ? 0.0f : z[n][b][i][NH - 1] * d;
-                                if constexpr (masked) {  // a key that the row does not see may hold a step that is not finite
-                                    if (!(seen[n][0] >> (2 * b + i) & 1)) x0 = 0.0f;
-                                    if (!(seen[n][NH - 1] >> (2 * b + i) & 1)) x1 = 0.0f;
-                                }
-                                if constexpr (PAIR) {
-                                    const float hi = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);  // f16's 11 bits
-                                    x1 = x0 - hi;
-                                    x0 = hi;
-                                }
-                                x[n][i] = transpose8(pack_f16(x0, x1));
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 d2 = unpack_f16(vs[b][i][G / 2]);
+                            const float d = (G & 1) ? d2.y : d2.x;
+                            float x0 = z[b][i][0] * d, x1 = PAIR ? 0.0f : z[b][i][NH - 1] * d;
+                            if constexpr (masked) {  // a key that the row does not see may hold a step that is not finite
+                                if (!(seen[0] >> (2 * b + i) & 1)) x0 = 0.0f;
+                                if (!(seen[NH - 1] >> (2 * b + i) & 1)) x1 = 0.0f;
                             }
+                            if constexpr (PAIR) {
+                                const float hi = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);  // f16's 11 bits
+                                x1 = x0 - hi;
+                                x0 = hi;
+                            }
+                            x[i] = transpose8(pack_f16(x0, x1));
+                        }
                         const uint32_t y0 = __byte_perm(c00[gi / 2], c01[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
                         const uint32_t y1 = __byte_perm(c10[gi / 2], c11[gi / 2], (gi & 1) ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t v0 = mm ? y0 >> 8 : y0, v1 = mm ? y1 >> 8 : y1;
                             const uint32_t a0 = centre_lo(ck, v0), a1 = centre_hi(ck, v0), a2 = centre_lo(ck, v1), a3 = centre_hi(ck, v1);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(O[n][G][mm], a0, a1, a2, a3, x[n][0], x[n][1]);
+                            mma_f16(O[G][mm], a0, a1, a2, a3, x[0], x[1]);
                         }
                     }
                 }
@@ -789,53 +766,51 @@ __global__ void __launch_bounds__(step_warps(DP, PAIR, NT) * 32, 1) kv4_step_ker
         const bool whole = from_start && to_end;
         const float fo = __uint_as_float((uint32_t)(127 - 28 + eb) << 23);  // undoes pe
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int h = 0; h < NH; ++h) {
+            float sum = l[h];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                float sum = l[n][h];
+            for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float f = !whole ? fo : sum == 0.0f ? 0.0f : fo / sum;
+            const int row = (PAIR ? t : 2 * t + h), rho = s_rt * R + row, j = rho / p.grp;
+            if (j >= s_T) continue;
+            const int64_t tok = s_q0 + j;
+            const int head = s_kvh * p.grp + rho - j * p.grp;
+            const int64_t rec = (int64_t)((blockIdx.x * kWarps + warp) * 2 + (from_start ? 1 : 0)) * R + row;
 #pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                const float f = !whole ? fo : sum == 0.0f ? 0.0f : fo / sum;
-                const int row = n * RT + (PAIR ? t : 2 * t + h), rho = s_rt * R + row, j = rho / p.grp;
-                if (j >= s_T) continue;
-                const int64_t tok = s_q0 + j;
-                const int head = s_kvh * p.grp + rho - j * p.grp;
-                const int64_t rec = (int64_t)((blockIdx.x * kWarps + warp) * 2 + (from_start ? 1 : 0)) * R + row;
+            for (int G = 0; G < NG; ++G) {
+                float x[4];
 #pragma unroll
-                for (int G = 0; G < NG; ++G) {
-                    float x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float (&o)[4] = O[n][G][i / 2];
-                        const int c = (i & 1) * 2;
-                        x[i] = (PAIR ? o[c] + o[c + 1] : o[c + h]) * f;
-                    }
-                    const int el = G * 32 + g * 4;
-                    if (!whole) {
-                        *reinterpret_cast<float4 *>(p.part + rec * DP + el) = make_float4(x[0], x[1], x[2], x[3]);
-                    } else if (el < p.a.c.d) {
-                        const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d + el;
-                        if (PAIR && p.a.type == QB_T_F32) {
-                            *reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
-                        } else {
-                            uint2 u;
-                            if (p.a.type == QB_T_F16) {
-                                u = make_uint2(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
-                            } else {
-                                const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-                                u = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-                            }
-                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = u;
-                        }
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float (&o)[4] = O[G][i / 2];
+                    const int c = (i & 1) * 2;
+                    x[i] = (PAIR ? o[c] + o[c + 1] : o[c + h]) * f;
                 }
-                if (g == 0) {
-                    if (!whole)
-                        p.stat[rec] = make_float2(m[n][h], sum);
-                    else if (p.a.lse)
-                        p.a.lse[tok * p.a.nh + head] = (m[n][h] + log2f(sum)) * 0.6931471805599453f;
+                const int el = G * 32 + g * 4;
+                if (!whole) {
+                    *reinterpret_cast<float4 *>(p.part + rec * DP + el) = make_float4(x[0], x[1], x[2], x[3]);
+                } else if (el < p.a.c.d) {
+                    const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d + el;
+                    if (PAIR && p.a.type == QB_T_F32) {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+                    } else {
+                        uint2 u;
+                        if (p.a.type == QB_T_F16) {
+                            u = make_uint2(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
+                        } else {
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+                            u = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                        }
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = u;
+                    }
                 }
             }
+            if (g == 0) {
+                if (!whole)
+                    p.stat[rec] = make_float2(m[h], sum);
+                else if (p.a.lse)
+                    p.a.lse[tok * p.a.nh + head] = (m[h] + log2f(sum)) * 0.6931471805599453f;
+            }
+        }
         if (!whole && lane == 0) {
             piece[warp][from_start ? 1 : 0] = make_int4(s_q0, s_T, s_kvh, s_rt);
             if (!from_start) piece_ends[warp] = to_end;
@@ -1003,14 +978,19 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p, int blo
 
 // ---------------------------------------------------------------- launch
 
-// an item of at most this many keys is not split (and no join is launched)
+// Where the table rows hold no more keys than this, items are not split and no join
+// is launched (one sequence of 100 keys: 9.4 us, 12.7 with the join).
 constexpr int kNoSplitKeys = 256;
+// A block has at least this many keys' places: on short sequences more blocks cost more in
+// the join than they save, fewer leave more to each (64, 128, 256, two tokens on 200 keys in
+// bf16: 11.5, 12.1, 12.9 us; one on 600: 11.7, 11.3, 11.5).
+constexpr int kMinShareKeys = 128;
 
-template <int DP, bool PAIR, int NT, int SB>
+template <int DP, bool PAIR, int SB>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
-    constexpr int kWarps = step_warps(DP, PAIR, NT), R = step_rows(PAIR, NT);
-    constexpr int smem = kWarps * step_stages(DP, PAIR, NT) * step_unit_bytes(DP, PAIR, NT);
-    p.min_share = 256 / step_unit(DP, PAIR, NT);
+    constexpr int kWarps = step_warps(DP), R = step_rows(PAIR);
+    constexpr int smem = kWarps * step_stages(DP) * step_unit_bytes(DP);
+    p.min_share = kMinShareKeys / kUnit;
     const StepWs w = step_ws(grid, kWarps, R, DP);
     p.part = reinterpret_cast<float *>(p.a.ws + w.part);
     p.stat = reinterpret_cast<float2 *>(p.a.ws + w.stat);
@@ -1018,20 +998,11 @@ static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     p.cstat = reinterpret_cast<float2 *>(p.a.ws + w.cstat);
     p.last = reinterpret_cast<int *>(p.a.ws + w.last);
     p.meta = reinterpret_cast<int4 *>(p.a.ws + w.meta);
-    auto *f = kv4_step_kernel<DP, PAIR, NT, SB>;
+    auto *f = kv4_step_kernel<DP, PAIR, SB>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p)) return rc;
     if (p.nosplit) return QB_OK;
-    return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p,
-                      grid);
-}
-
-template <int DP, bool PAIR, int NT>
-static int launch_step_m(StepK &p, int grid, cudaStream_t stream) {
-    constexpr int U = step_unit(DP, PAIR, NT);
-    return p.a.c.page == 16                ? launch_step_k<DP, PAIR, NT, 16>(p, grid, stream)
-           : p.a.c.page == 32 || U == 32   ? launch_step_k<DP, PAIR, NT, 32>(p, grid, stream)
-                                           : launch_step_k<DP, PAIR, NT, U>(p, grid, stream);
+    return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p, grid);
 }
 
 template <int DP>
@@ -1041,12 +1012,16 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.grp = a.nh / a.c.nkv;
     const int grid = attn_grid();
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
-    // rows a sequence and key head, on average: pairs where they fit one column
-    // tile (and for f32 always), two column tiles where one does not hold them
-    const int64_t rows = a.ntok * p.grp, n = a.s.nseq;
-    if (rows <= 4 * n) return launch_step_m<DP, true, 1>(p, grid, stream);
-    if (a.type == QB_T_F32) return launch_step_m<DP, true, 2>(p, grid, stream);
-    return rows <= 8 * n ? launch_step_m<DP, false, 1>(p, grid, stream) : launch_step_m<DP, false, 2>(p, grid, stream);
+    // f32 takes pairs for its accuracy; half precision takes them where a sequence and
+    // key head have 4 rows or fewer on average, which a tile of 8 would only pad (256
+    // steps on 1000 keys: 88 us, 91 as eights), else eights (two tokens a step: 96 us).
+    // A tile of two such columns, which decodes a key once for both, has 8 warps a
+    // multiprocessor instead of 12: four tokens a step 182 us against 130 in bf16, 184
+    // against 180 in f32.
+    const bool pair = a.type == QB_T_F32 || a.ntok * p.grp <= 4 * (int64_t)a.s.nseq;
+    if (a.c.page == 16)
+        return pair ? launch_step_k<DP, true, 16>(p, grid, stream) : launch_step_k<DP, false, 16>(p, grid, stream);
+    return pair ? launch_step_k<DP, true, 32>(p, grid, stream) : launch_step_k<DP, false, 32>(p, grid, stream);
 }
 
 }  // namespace qb
