@@ -21,13 +21,13 @@ int64_t kv4_attn_ws(int dp) {
 // kernel's 8, which read and decode the keys anew.  Step against prompt kernel, us,
 // heads of 128, 32 on 8 key heads, in bf16:
 //     rows                        64          96          128         192
-//     1 sequence of 2000 keys     18 / 33     20 / 35     22 / 36     27 / 38
-//     1 of 8000                   30 / 32     38 / 33     45 / 34     61 / 36
-//     8 of 2000                   37 / 58     51 / 59     58 / 60     90 / 61
-//     8 of 8000                   99 / 96     149 / 99    176 / 101   290 / 106
-//     64 of 300                   55 / 127    77 / 115    96 / 114    122 / 114
-//     64 of 2000                  191 / 324   277 / 327   339 / 326   509 / 311
-constexpr int kPromptFrom = 128;
+//     1 sequence of 2000 keys     18 / 36     20 / 36     22 / 37     27 / 36
+//     1 of 8000                   30 / 33     38 / 33     45 / 33     61 / 33
+//     8 of 2000                   37 / 51     51 / 51     58 / 51     90 / 52
+//     8 of 8000                   99 / 87     149 / 88    176 / 88    290 / 89
+//     64 of 300                   55 / 86     77 / 83     96 / 83     122 / 88
+//     64 of 2000                  191 / 238   277 / 238   339 / 239   509 / 242
+constexpr int kPromptFrom = 96;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)

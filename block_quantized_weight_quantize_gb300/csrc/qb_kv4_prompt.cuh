@@ -11,12 +11,12 @@
 //
 // A rounded key moves a score by 2^-12 of its terms, which averages out over many
 // keys but not over few: lse is off by 1e-5 to 2e-5 of itself at 100 keys, 3e-6 at
-// 500.  Where a row of an item sees fewer than kPromptFine keys, what the rounding
-// leaves is decoded too (one multiply-add, exact) and multiplied by Q into the same
-// scores: 1e-7 then.  It costs 5 to 10% (2048 tokens by themselves, 32 heads of
-// 128: 98 -> 108 us; 512 on 4096 keys 68 -> 82); the output keeps the error of
-// values and probabilities in f16, 3.4e-4 of an f16 output, 2.1e-4 of it the output's own
-// rounding.
+// 500, 1.2e-6 at 2200, 5e-7 at 8192.  Where a row of an item sees fewer than kPromptFine
+// keys, what the rounding leaves is decoded too (one multiply-add, exact) and multiplied
+// by Q into the same scores: 1e-7 then.  It costs 5 to 30% (a prompt of 2048 tokens by
+// itself, 32 heads of 128: 90 -> 98 us; 64 sequences of 64 tokens on 2000 keys: 188 ->
+// 248).  The output keeps the error of values and probabilities in f16: 3.4e-4 to 4.2e-4
+// of an f16 output, 2.1e-4 of it the output's own rounding.
 //
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
 // head + head) of one sequence and key head, over the tiles of 128 keys that they
@@ -24,7 +24,8 @@
 // block takes the same count of consecutive ones.  An item that blocks share
 // leaves its rows' sums in the workspace, joined by kv4_prompt_join_kernel.
 // (Whole items to a block: 258 us for 2048 tokens on 8192 keys, 32 heads of 128,
-// 256 items on 152 multiprocessors; shared ones 254 us with their join.  With few
+// 256 items on 152 multiprocessors; shared ones 254 us with their join: 0.95 PFLOP/s
+// where a plain product of matrices reaches 1.9.  With few
 // items it is what fills the card.)
 // Roles of a block's 16 warps (152 registers a thread in warps 0-7, 104 in the
 // others: 2 * 152 + 2 * 104 = the 4 * 128 of the launch):
@@ -44,6 +45,7 @@
 // outputs of that group are NaN.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "qb_kv4.cuh"
@@ -78,7 +80,7 @@ struct PromptItem {
     int fine;            // keys as two f16
 };
 
-constexpr int kPromptFine = 4096;  // keys; see above
+constexpr int kPromptFine = 2048;  // keys; see above
 constexpr int kPromptCost = 1;  // what an item costs beside its tiles, in tiles
 
 template <int DP>
@@ -89,7 +91,7 @@ struct PromptSmem {
     alignas(128) uint8_t v[2][kTileBytes];
     uint16_t flags[4][kPromptTile];  // of a tile's keys: 1 K, 2 V decoded 2^-4 smaller; from bit 8 the groups that are not finite
     uint32_t any[4][4];              // whether a decoder warp's keys have one
-    uint64_t q_full[kPromptQ], s_full[kPromptQ], p_ready[kPromptQ], o_done[kPromptQ];
+    uint64_t q_full[kPromptQ], q_free[kPromptQ], s_full[kPromptQ], p_ready[kPromptQ], o_done[kPromptQ];
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
     uint32_t tmem;
     long long chunk_sum[8192 / 32 + 1];
@@ -272,18 +274,25 @@ __device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, in
     return max(1, pos_hi < 0 ? 0 : pos_hi / kPromptTile + 1 - t0);
 }
 
-// The places of a chunk of 32 sequences, a lane's own, by the whole warp.
+// The places of a chunk of 32 sequences, a lane's own, by the whole warp: a lane
+// counts its own sequence's row pairs, or the warp one sequence after the other where
+// that takes fewer steps (32 sequences of a row pair: 19 us one after the other, counted
+// twice).
 __device__ __forceinline__ long long prompt_places(const PromptK &p, int c, int lane, bool report, SeqInfo &q) {
     q = seq_info(p.a, c * 32 + lane, report);
+    uint32_t left = __ballot_sync(0xFFFFFFFFu, q.T > 0);
+    const int pairs = prompt_pairs(p, q.T), most = (int)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)pairs);
     long long mine = 0;
-    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, q.T > 0); left; left &= left - 1) {
+    int t0;
+    if (most <= 4 * __popc(left)) {
+        for (int rp = 0; rp < pairs; ++rp) mine += prompt_tiles(p, q.len, q.T, rp, t0) + kPromptCost;
+        return mine * p.a.c.nkv;
+    }
+    for (; left; left &= left - 1) {
         const int l = __ffs(left) - 1;
         const int len = __shfl_sync(0xFFFFFFFFu, q.len, l), T = __shfl_sync(0xFFFFFFFFu, q.T, l);
         long long n = 0;
-        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) {
-            int t0;
-            n += prompt_tiles(p, len, T, rp, t0) + kPromptCost;
-        }
+        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) n += prompt_tiles(p, len, T, rp, t0) + kPromptCost;
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
         if (lane == l) mine = n * p.a.c.nkv;
@@ -423,6 +432,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPromptQ; ++i) {
             mbar_init(&sm.q_full[i], kPromptTile);
+            mbar_init(&sm.q_free[i], 4);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_ready[i], kPromptTile);
             mbar_init(&sm.o_done[i], 1);
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         const int q = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tb + lanes + 128u * q, tO = tb + lanes + 256u + (uint32_t)DP * q;
-        uint32_t tiles = 0;  // of this row tile so far
+        uint32_t tiles = 0, items = 0;  // of this row tile so far
         int goes_on = -1;
         bool ok = true;
         while (ok && prompt_next(p, lane, it)) {
@@ -471,52 +481,73 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
             const int64_t tok = it.q0 + j;
             const int head = it.kvh * p.grp + rho - j * p.grp;
+            const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d;  // of the row's output
             float cs = 0.0f;
             {
-                // the row's queries as f16, its largest magnitude scaled into [2^14, 2^15)
-                const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + tok * p.a.q_stride + (int64_t)head * p.a.c.d;
-                uint4 raw[DP / 8];  // the whole row's loads under way together
-#pragma unroll
-                for (int o = 0; o < DP / 8; ++o) {
-                    raw[o] = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && o * 8 < p.a.c.d) raw[o] = *reinterpret_cast<const uint4 *>(src + o * 8);
-                }
+                // The queries as f16, a row's largest magnitude scaled into [2^8, 2^9).  Four
+                // lanes load a row (64 bytes together), a warp its 32 rows in four goes, all
+                // loads under way together.  (A row a thread: 32 cache lines a load, 2.5 us an item.)
+                constexpr int NO = DP / 32;  // eights of a row that a lane has
+                uint4 raw[4][NO];
                 const bool f16 = p.a.type == QB_T_F16;
-                auto load = [&](int o, float (&x)[8]) {
-                    if (f16) unpack8<QB_T_F16>(raw[o], x); else unpack8<QB_T_BF16>(raw[o], x);
-                };
-                float top = 0.0f;
 #pragma unroll
-                for (int o = 0; o < DP / 8; ++o) {
-                    float x[8];
-                    load(o, x);
+                for (int k = 0; k < 4; ++k) {
+                    const int rho2 = it.rp * kPromptRows + q * kPromptTile + (r & 96) + 8 * k + (lane >> 2), j2 = rho2 / p.grp;
+                    const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (it.q0 + (int64_t)j2) * p.a.q_stride +
+                                          (int64_t)(it.kvh * p.grp + rho2 - j2 * p.grp) * p.a.c.d;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+                    for (int o = 0; o < NO; ++o) {
+                        const int el = (4 * o + (lane & 3)) * 8;
+                        raw[k][o] = make_uint4(0u, 0u, 0u, 0u);
+                        if (j2 < it.T && el < p.a.c.d) raw[k][o] = *reinterpret_cast<const uint4 *>(src + el);
+                    }
                 }
-                const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 8;
-                const float f = copysignf(__uint_as_float((uint32_t)(127 + 8 - e) << 23), p.a.scale);
+                auto load = [&](const uint4 &u, float (&x)[8]) {
+                    if (f16) unpack8<QB_T_F16>(u, x); else unpack8<QB_T_BF16>(u, x);
+                };
+                // the item before: every warp has read its outputs from where the queries go
+                if (items && !(ok = prompt_wait(&sm.q_free[q], (items - 1) & 1, p.a.fault))) break;
+                ++items;
+                int e = 0;  // of this thread's row
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int o = 0; o < NO; ++o) {
+                        float x[8];
+                        load(raw[k][o], x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const int e2 = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 8;
+                    const float f = copysignf(__uint_as_float((uint32_t)(127 + 8 - e2) << 23), p.a.scale);
+                    const int own = __shfl_sync(0xFFFFFFFFu, e2, 4 * (lane & 7));
+                    if (lane >> 3 == k) e = own;
+                    uint8_t *dst = sm.q[q] + ((r & 96) + 8 * k + (lane >> 2)) * 16;
+#pragma unroll
+                    for (int o = 0; o < NO; ++o) {
+                        float x[8];
+                        load(raw[k][o], x);
+                        uint4 u;
+                        u.x = prompt_half2(__floats2half2_rn(x[0] * f, x[4] * f));
+                        u.y = prompt_half2(__floats2half2_rn(x[1] * f, x[5] * f));
+                        u.z = prompt_half2(__floats2half2_rn(x[2] * f, x[6] * f));
+                        u.w = prompt_half2(__floats2half2_rn(x[3] * f, x[7] * f));
+                        *reinterpret_cast<uint4 *>(dst + (4 * o + (lane & 3)) * kOctStride) = u;
+                    }
+                }
                 // not zero, so that a score that is masked stays -inf
                 cs = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f * exp2f((float)(e - 8)), 1e-37f);
-                uint8_t *dst = sm.q[q] + r * 16;
-#pragma unroll
-                for (int o = 0; o < DP / 8; ++o) {
-                    float x[8];
-                    load(o, x);
-                    uint4 u;
-                    u.x = prompt_half2(__floats2half2_rn(x[0] * f, x[4] * f));
-                    u.y = prompt_half2(__floats2half2_rn(x[1] * f, x[5] * f));
-                    u.z = prompt_half2(__floats2half2_rn(x[2] * f, x[6] * f));
-                    u.w = prompt_half2(__floats2half2_rn(x[3] * f, x[7] * f));
-                    *reinterpret_cast<uint4 *>(dst + o * kOctStride) = u;
-                }
                 fence_async_shared();
                 mbar_arrive(&sm.q_full[q]);
             }
             // tiles whose keys all of this row tile's rows see need no mask
             const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
             const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
-            const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : -1;
-            const int first_hi = p.a.window ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
+            const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : INT_MAX;  // no row: whatever comes out
+            const int first_hi = p.a.window && j_lo < it.T ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
             PromptRow row = {cs, -INFINITY, 0.0f, 0, 0};
             uint32_t bad = 0;
             const int n_tiles = it.n, t_first = it.t0;
@@ -550,7 +581,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const bool whole = it.from_start && it.n == it.rest;
             const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
             const int64_t rec = (int64_t)(blockIdx.x * 2 + (it.from_start ? 1 : 0)) * kPromptRows + q * kPromptTile + r;
-            uint16_t *out = static_cast<uint16_t *>(p.a.out) + tok * p.a.out_stride + (int64_t)head * p.a.c.d;
+            // The rows go through shared memory, where the queries were, so that lanes write a
+            // row's bytes together: whole rows in the output's type, a piece's sums in f32 and
+            // two goes of 16 dims a group.  Pieces of 16 bytes of a row lie in the order of
+            // their number ^ (row % 8).  (A row a thread: 4 and 7 us an item.)
+            constexpr int C = DP / 8;  // such pieces, lanes that write a row
+            uint8_t *const rows = sm.q[q] + (r & 96) * DP * 2;  // this warp's 32
+            const int64_t mine = live ? at : -1;
+            auto piece = [&](int row2, int c) { return reinterpret_cast<uint4 *>(rows + row2 * DP * 2 + (c ^ (row2 & 7)) * 16); };
             // 32 columns are chunks 2kk, 2kk + 1 (W = 4; all four of W = 2's eight dims): eight dims of every group
 #pragma unroll
             for (int kk = 0; kk < DP / 32; ++kk) {
@@ -559,31 +597,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 tc_ld32(tO + 32 * kk, o);
                 // column (c * (W / 2) + u) * 8 + 2 j + h is dim (2 u + h) * 32 + 4 c + j
                 constexpr int CPL = 8 / W;  // chunks in 32 columns
-                if (live) {
 #pragma unroll
-                    for (int G = 0; G < W; ++G) {
-                        float x[4 * CPL];
+                for (int G = 0; G < W; ++G) {
+                    float x[4 * CPL];
 #pragma unroll
-                        for (int c = 0; c < CPL; ++c)
+                    for (int c = 0; c < CPL; ++c)
 #pragma unroll
-                            for (int j2 = 0; j2 < 4; ++j2) {
-                                const float y = __uint_as_float(o[(c * (W / 2) + (G >> 1)) * 8 + 2 * j2 + (G & 1)]) * inv;
-                                x[c * 4 + j2] = (bad >> G & 1) ? __uint_as_float(kEngineNaN) : y;
-                            }
-                        const int el = G * 32 + kk * 4 * CPL;
+                        for (int j2 = 0; j2 < 4; ++j2) {
+                            const float y = __uint_as_float(o[(c * (W / 2) + (G >> 1)) * 8 + 2 * j2 + (G & 1)]) * inv;
+                            x[c * 4 + j2] = (bad >> G & 1) ? __uint_as_float(kEngineNaN) : y;
+                        }
+                    const int el = kk * 4 * CPL;  // of the group's 32
 #pragma unroll
-                        for (int h = 0; h < 4 * CPL; h += 8) {
-                            const float (&y)[8] = *reinterpret_cast<const float (*)[8]>(&x[h]);
-                            if (!whole) {
-                                store8<QB_T_F32>(p.part + rec * DP + el + h, y);
-                                continue;
-                            }
-                            if (el + h >= p.a.c.d) continue;
-                            if (p.a.type == QB_T_F16) store8<QB_T_F16>(out + el + h, y); else store8<QB_T_BF16>(out + el + h, y);
+                    for (int h = 0; h < 4 * CPL; h += 8) {
+                        const float (&y)[8] = *reinterpret_cast<const float (*)[8]>(&x[h]);
+                        if (!whole) {
+                            *reinterpret_cast<float4 *>(piece(lane, G * 4 + (el + h) % 16 / 4)) = make_float4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<float4 *>(piece(lane, G * 4 + (el + h) % 16 / 4 + 1)) = make_float4(y[4], y[5], y[6], y[7]);
+                        } else if (p.a.type == QB_T_F16) {
+                            store8<QB_T_F16>(piece(lane, G * 4 + (el + h) / 8), y);
+                        } else {
+                            store8<QB_T_BF16>(piece(lane, G * 4 + (el + h) / 8), y);
                         }
                     }
                 }
+                if (!whole && (kk + 1) * 4 * CPL % 16 == 0) {
+                    __syncwarp();
+                    float *const to = p.part + (rec - lane) * DP + (kk + 1) * 4 * CPL - 16;
+#pragma unroll 4
+                    for (int k = 0; k < C; ++k) {
+                        const int row2 = k * (32 / C) + lane / C, c = lane % C;
+                        *reinterpret_cast<uint4 *>(to + row2 * DP + c / 4 * 32 + c % 4 * 4) = *piece(row2, c);
+                    }
+                }
             }
+            __syncwarp();
+            if (whole) {
+#pragma unroll 4
+                for (int k = 0; k < C; ++k) {
+                    const int row2 = k * (32 / C) + lane / C, c = lane % C;
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, row2);
+                    if (to >= 0 && c * 8 < p.a.c.d)
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.out) + to + c * 8) = *piece(row2, c);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&sm.q_free[q]);
             if (live && !whole) p.stat[rec] = make_float2(m, l);
             if (live && whole && p.a.lse) p.a.lse[tok * p.a.nh + head] = (m + log2f(l)) * 0.6931471805599453f;
             if (threadIdx.x == 0 && it.from_start && !whole) {
