@@ -69,6 +69,14 @@ def _stream(stream, t) -> int:
     return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
+def _workspace(nbytes: int, like, stream):
+    """A workspace for one call on `stream` (None: the current one) of the device of `like`."""
+    w = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:  # its memory is given out again only when that stream has passed the call
+        w.record_stream(stream)
+    return w
+
+
 def _bytes(n: int, where: str) -> int:
     if n < 0:
         raise QbError(int(n), where)
@@ -199,7 +207,7 @@ def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: i
         if lse.numel() != q.shape[0] * nh:
             raise ValueError("lse: [ntok, nh] expected")
     if workspace is None:
-        workspace = torch.empty(kv4_attn_workspace_bytes(cache, q), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(kv4_attn_workspace_bytes(cache, q), q, stream)
     _check(_c.kv4_attn(cache.ref, seqs.ref, _TYPE[q.dtype], qp, qs, q.shape[0], nh, scale, window, op, os_, lp,
                        _dev(workspace, what="workspace"), workspace.numel() * workspace.element_size(),
                        _stream(stream, q)), "kv4_attn")
@@ -220,9 +228,9 @@ def kv_pages_workspace_bytes(pages: KvPages) -> int:
     return _bytes(_c.kv_pages_workspace_bytes(pages.ref), "kv_pages_workspace_bytes")
 
 
-def _page_ws(pages, workspace):
+def _page_ws(pages, workspace, stream):
     if workspace is None:
-        workspace = torch.empty(kv_pages_workspace_bytes(pages), dtype=torch.uint8, device=pages.refs.device)
+        workspace = _workspace(kv_pages_workspace_bytes(pages), pages.refs, stream)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -249,7 +257,7 @@ def kv_pages_fork(pages: KvPages, data, parents, children, status, workspace=Non
     if children.numel() != n or status.numel() < n:
         raise ValueError("children, status: one entry a parent expected")
     dp, layers, pb = _pool(data, pages.c.npages)
-    ws, wb = _page_ws(pages, workspace)
+    ws, wb = _page_ws(pages, workspace, stream)
     _check(_c.kv_pages_fork(pages.ref, dp, layers, pb, _dev(parents, i32, "parents"), _dev(children, i32, "children"),
                             n, _dev(status, i32, "status"), _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
            "kv_pages_fork")
@@ -264,7 +272,7 @@ def kv_pages_free(pages: KvPages, rows, stream=None) -> None:
 def kv_pages_compact(pages: KvPages, data, workspace=None, stream=None) -> None:
     """Moves the held pages to the pool's beginning, in every layer of data."""
     dp, layers, pb = _pool(data, pages.c.npages)
-    ws, wb = _page_ws(pages, workspace)
+    ws, wb = _page_ws(pages, workspace, stream)
     _check(_c.kv_pages_compact(pages.ref, dp, layers, pb, _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
            "kv_pages_compact")
 
