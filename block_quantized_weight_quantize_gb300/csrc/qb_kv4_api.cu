@@ -96,7 +96,7 @@ int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const vo
         return QB_E_ARG;
     if (!seqs->rows && seqs->nseq > seqs->nrows) return QB_E_ARG;
     if (nh < 1 || nh > 4096 || nh % cache->nkv != 0 || ntok < 0 || ntok > (int64_t(1) << 24) ||
-        ntok * nh >= (int64_t(1) << 31))
+        ntok * nh > (int64_t(1) << 30))
         return QB_E_ARG;
     if (!seqs->q_start && ntok != seqs->nseq) return QB_E_ARG;
     const int64_t width = (int64_t)nh * cache->d;

@@ -494,7 +494,7 @@ QB_API int64_t kv4_attn_workspace_bytes(const qb_kv4 *cache, int nh);
  * bits), otherwise as one f16; a probability (of the largest, 1) below 2^-38
  * may vanish beside the largest step among the values.  Queries of magnitude
  * past 2^110 are out of range.  q, out 16-byte aligned, strides multiples of 16
- * bytes; nh % nkv == 0; ntok <= 2^24, ntok * nh < 2^31.
+ * bytes; nh % nkv == 0; ntok <= 2^24, ntok * nh <= 2^30.
  * workspace: at least kv4_attn_workspace_bytes() bytes, 16-byte aligned, not
  * shared with a call that may run at the same time.  A length past its table row is cut to it; a row
  * or page number outside its range reads as no keys / page 0 and is reported
