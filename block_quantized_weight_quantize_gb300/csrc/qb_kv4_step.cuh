@@ -11,13 +11,12 @@
 //
 // Operands.  The codes are the A side (16 keys, or 16 of the value's elements, by
 // 16), the rows the 8 columns of the B side, since a step has few rows: 4 rows as
-// pairs (high part, low part) in f32 or where there are no more, else 8 rows; of more rows
-// there are more tiles, each with the keys anew.  Codes become f16
-// without a conversion: a code in the low bits of an f16 is the subnormal
-// c * 2^-24, exact, and 1024 + c is one OR away.  Half-precision keys take the
-// first where there are 8 rows, with -8 * sum of the queries as the sums'
-// initial value; elsewhere a
-// packed addition takes 1032 off (the sum of q or p times 8 taken off at the end
+// pairs (high part, low part), or 8 rows, in f32 with a product more for their low
+// parts; of more rows there are more tiles, each with the keys anew.  Codes become
+// f16 without a conversion: a code in the low bits of an f16 is the subnormal
+// c * 2^-24, exact, and 1024 + c is one OR away.  Half-precision tiles of 8 take the
+// first for keys, with -8 * sum of the queries as the sums' initial value; elsewhere
+// a packed addition takes 1032 off (the sum of q or p times 8 taken off at the end
 // costs f32 its last three bits: an error of 1.4e-6 against 2.1e-7).  Queries are
 // scaled by a power of two a row to f16's top; in f32 they enter as two f16 (22
 // bits).  The probabilities times steps likewise, scaled by a power of two that
@@ -210,12 +209,13 @@ __device__ __forceinline__ void step_store(const StepK &p, const float (&acc)[E]
     if (lane == 0 && p.a.lse) p.a.lse[(int64_t)tok * p.a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int DP, bool PAIR, int SB>
+template <int DP, bool PAIR, bool LOW, int SB>
 __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const StepK p) {
     constexpr int kWarps = step_warps(DP), kStages = step_stages(DP);
     constexpr int U = kUnit, kBytes = step_unit_bytes(DP), NB = U / 16;
     constexpr int kItemCost = 64 / U;  // what an item costs beside its units (its queries, its output), in units
     constexpr int R = step_rows(PAIR), NH = PAIR ? 1 : 2;  // rows: of a tile, a lane's
+    constexpr bool CENTRE = PAIR || LOW;
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4, NP = NG / W;         // groups, groups a plane, planes
     constexpr int kSub = kv4_block(SB, DP);                               // a sub-block of SB rows in shared memory
     constexpr int kCodes = SB * DP / 2, kSteps = SB * DP / 16, kPlane = SB * 16 * W;
@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
 
         // the queries as B fragments: column g of tile n is a row (half precision) or a row's high or low part (f32)
         uint32_t B[NG][2][2];
-        float cinit[NG][PAIR ? 1 : 2], cs[NH];
+        uint32_t BL[LOW ? NG : 1][2][2];  // the low parts
+        float cinit[CENTRE ? 1 : NG][2], cs[NH];
         const int rho = s_rt * R + (PAIR ? g >> 1 : g), j = rho / p.grp;
         const bool live = j < s_T;
         const int64_t at = (int64_t)(s_q0 + j) * p.a.q_stride + (int64_t)(s_kvh * p.grp + rho - j * p.grp) * p.a.c.d;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             for (int i = 0; i < 8; ++i) x[i] = 0.0f;
             const int el = G * 32 + t * 8;
             if (!live || el >= p.a.c.d) return;
-            if (PAIR && p.a.type == QB_T_F32) {
+            if (LOW || (PAIR && p.a.type == QB_T_F32)) {
                 load8<QB_T_F32>(static_cast<const float *>(p.a.q) + at + el, x);
             } else {
                 const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at + el;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 14;
         const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
         // undone in the scores, with the codes' 2^-24 where they stand as subnormals
-        const float back = p.a.scale * 1.4426950408889634f * exp2f((float)(e - 14 + (PAIR ? 0 : 24)));
+        const float back = p.a.scale * 1.4426950408889634f * exp2f((float)(e - 14 + (CENTRE ? 0 : 24)));
 #pragma unroll
         for (int h = 0; h < NH; ++h) cs[h] = __shfl_sync(0xFFFFFFFFu, back, PAIR ? 8 * t : 8 * t + 4 * h);
 #pragma unroll
@@ -499,15 +500,21 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             float sum = 0.0f;
             uint32_t h2[4];
             // a pair's high part is cut to f16's 11 bits, its low part what is left
+            float low[LOW ? 8 : 1];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float y = x[i] * f;
                 const float hi = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
-                x[i] = !PAIR ? y : (g & 1) ? y - hi : hi;
+                x[i] = !CENTRE ? y : (PAIR && (g & 1)) ? y - hi : hi;
+                if constexpr (LOW) low[i] = y - hi;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) h2[i] = pack_f16(x[i], x[i + 4]);
-            if constexpr (!PAIR) {
+            if constexpr (LOW) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) BL[G][i >> 1][i & 1] = pack_f16(low[i], low[i + 4]);
+            }
+            if constexpr (!CENTRE) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 u = unpack_f16(h2[i]);
@@ -579,7 +586,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t x0 = mm ? w0[gi] >> 8 : w0[gi], x1 = mm ? w1[gi] >> 8 : w1[gi];
                             uint32_t a0, a1, a2, a3;
-                            if constexpr (PAIR) {
+                            if constexpr (CENTRE) {
                                 a0 = centre_lo(ck, x0);
                                 a1 = centre_lo(ck, x1);
                                 a2 = centre_hi(ck, x0);
@@ -591,11 +598,12 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                                 a3 = x1 & 0x00F000F0u;
                             }
                             if (mm == 0) {
-                                const float c0 = PAIR ? 0.0f : cinit[G][0], c1 = PAIR ? 0.0f : cinit[G][PAIR ? 0 : 1];
+                                const float c0 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][0], c1 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][1];
                                 mma_f16(acc, a0, a1, a2, a3, B[G][0][0], B[G][0][1], c0, c1, c0, c1);
                             } else {
                                 mma_f16(acc, a0, a1, a2, a3, B[G][1][0], B[G][1][1]);
                             }
+                            if constexpr (LOW) mma_f16(acc, a0, a1, a2, a3, BL[G][mm][0], BL[G][mm][1]);
                         }
                         const float2 d0 = unpack_f16(st[0][G / 2]), d1 = unpack_f16(st[1][G / 2]);
                         const float s0 = (G & 1) ? d0.y : d0.x, s1 = (G & 1) ? d1.y : d1.x;
@@ -716,6 +724,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
                         uint32_t x[2];
+                        [[maybe_unused]] uint32_t xl[2];  // the low parts
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float2 d2 = unpack_f16(vs[b][i][G / 2]);
@@ -725,10 +734,15 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                                 if (!(seen[0] >> (2 * b + i) & 1)) x0 = 0.0f;
                                 if (!(seen[NH - 1] >> (2 * b + i) & 1)) x1 = 0.0f;
                             }
+                            const float hi = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);  // f16's 11 bits
                             if constexpr (PAIR) {
-                                const float hi = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);  // f16's 11 bits
                                 x1 = x0 - hi;
                                 x0 = hi;
+                            } else if constexpr (LOW) {
+                                const float hi1 = __uint_as_float(__float_as_uint(x1) & 0xFFFFE000u);
+                                xl[i] = transpose8(pack_f16(x0 - hi, x1 - hi1));
+                                x0 = hi;
+                                x1 = hi1;
                             }
                             x[i] = transpose8(pack_f16(x0, x1));
                         }
@@ -739,6 +753,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                             const uint32_t v0 = mm ? y0 >> 8 : y0, v1 = mm ? y1 >> 8 : y1;
                             const uint32_t a0 = centre_lo(ck, v0), a1 = centre_hi(ck, v0), a2 = centre_lo(ck, v1), a3 = centre_hi(ck, v1);
                             mma_f16(O[G][mm], a0, a1, a2, a3, x[0], x[1]);
+                            if constexpr (LOW) mma_f16(O[G][mm], a0, a1, a2, a3, xl[0], xl[1]);
                         }
                     }
                 }
@@ -796,7 +811,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                     *reinterpret_cast<float4 *>(p.part + rec * DP + el) = make_float4(x[0], x[1], x[2], x[3]);
                 } else if (el < p.a.c.d) {
                     const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d + el;
-                    if (PAIR && p.a.type == QB_T_F32) {
+                    if (LOW || (PAIR && p.a.type == QB_T_F32)) {
                         *reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
                     } else {
                         uint2 u;
@@ -992,7 +1007,7 @@ constexpr int kNoSplitKeys = 256;
 // bf16: 11.5, 12.1, 12.9 us; one on 600: 11.7, 11.3, 11.5).
 constexpr int kMinShareKeys = 128;
 
-template <int DP, bool PAIR, int SB>
+template <int DP, bool PAIR, bool LOW, int SB>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     constexpr int kWarps = step_warps(DP), R = step_rows(PAIR);
     constexpr int smem = kWarps * step_stages(DP) * step_unit_bytes(DP);
@@ -1004,7 +1019,7 @@ static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     p.cstat = reinterpret_cast<float2 *>(p.a.ws + w.cstat);
     p.last = reinterpret_cast<int *>(p.a.ws + w.last);
     p.meta = reinterpret_cast<int4 *>(p.a.ws + w.meta);
-    auto *f = kv4_step_kernel<DP, PAIR, SB>;
+    auto *f = kv4_step_kernel<DP, PAIR, LOW, SB>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p)) return rc;
     if (p.nosplit) return QB_OK;
@@ -1018,16 +1033,20 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.grp = a.nh / a.c.nkv;
     const int grid = attn_grid();
     p.nosplit = (int64_t)a.s.maxp * a.c.page <= kNoSplitKeys;
-    // f32 takes pairs for its accuracy; half precision takes them where a sequence and
-    // key head have 4 rows or fewer on average, which a tile of 8 would only pad (256
-    // steps on 1000 keys: 88 us, 91 as eights), else eights (two tokens a step: 96 us).
-    // A tile of two such columns, which decodes a key once for both, has 8 warps a
-    // multiprocessor instead of 12: four tokens a step 182 us against 130 in bf16, 184
-    // against 180 in f32.
-    const bool pair = a.type == QB_T_F32 || a.ntok * p.grp <= 4 * (int64_t)a.s.nseq;
+    // f32 enters as high and low parts for its accuracy: side by side in tiles of 4 rows, or in
+    // tiles of 8 with a product more for the low parts, which decode a key for twice the rows.
+    // By the rows a sequence and key head, on average (us in tiles of 4, of 8): 256 sequences of
+    // 1000 keys, 8 rows 119, 117, 16 rows 180, 161, 64 rows 693, 505; one of 600 keys, 8 rows
+    // 11.0, 12.7, 64 rows 13.9, 14.8.  Half precision takes tiles of 4 where a tile of 8 would only
+    // be padded (4 rows: 88, 91), and eights from there on.  (Two such column tiles, which decode
+    // a key once for both, leave 8 warps a multiprocessor instead of 12: 16 rows 182 us
+    // against 130 in bf16, 184 against 180 in f32.)
+    const bool low = a.type == QB_T_F32, few = a.ntok * p.grp <= (low ? 8 : 4) * (int64_t)a.s.nseq;
     if (a.c.page == 16)
-        return pair ? launch_step_k<DP, true, 16>(p, grid, stream) : launch_step_k<DP, false, 16>(p, grid, stream);
-    return pair ? launch_step_k<DP, true, 32>(p, grid, stream) : launch_step_k<DP, false, 32>(p, grid, stream);
+        return few ? launch_step_k<DP, true, false, 16>(p, grid, stream)
+               : low ? launch_step_k<DP, false, true, 16>(p, grid, stream) : launch_step_k<DP, false, false, 16>(p, grid, stream);
+    return few ? launch_step_k<DP, true, false, 32>(p, grid, stream)
+           : low ? launch_step_k<DP, false, true, 32>(p, grid, stream) : launch_step_k<DP, false, false, 32>(p, grid, stream);
 }
 
 }  // namespace qb
