@@ -582,29 +582,31 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                     for (int gi = 0; gi < W; ++gi) {
                         const int G = pl * W + gi;
                         float acc[4];
+                        uint32_t a[2][4];
 #pragma unroll
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t x0 = mm ? w0[gi] >> 8 : w0[gi], x1 = mm ? w1[gi] >> 8 : w1[gi];
-                            uint32_t a0, a1, a2, a3;
                             if constexpr (CENTRE) {
-                                a0 = centre_lo(ck, x0);
-                                a1 = centre_lo(ck, x1);
-                                a2 = centre_hi(ck, x0);
-                                a3 = centre_hi(ck, x1);
+                                a[mm][0] = centre_lo(ck, x0);
+                                a[mm][1] = centre_lo(ck, x1);
+                                a[mm][2] = centre_hi(ck, x0);
+                                a[mm][3] = centre_hi(ck, x1);
                             } else {
-                                a0 = x0 & 0x000F000Fu;
-                                a1 = x1 & 0x000F000Fu;
-                                a2 = x0 & 0x00F000F0u;
-                                a3 = x1 & 0x00F000F0u;
+                                a[mm][0] = x0 & 0x000F000Fu;
+                                a[mm][1] = x1 & 0x000F000Fu;
+                                a[mm][2] = x0 & 0x00F000F0u;
+                                a[mm][3] = x1 & 0x00F000F0u;
                             }
-                            if (mm == 0) {
-                                const float c0 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][0], c1 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][1];
-                                mma_f16(acc, a0, a1, a2, a3, B[G][0][0], B[G][0][1], c0, c1, c0, c1);
-                            } else {
-                                mma_f16(acc, a0, a1, a2, a3, B[G][1][0], B[G][1][1]);
-                            }
-                            if constexpr (LOW) mma_f16(acc, a0, a1, a2, a3, BL[G][mm][0], BL[G][mm][1]);
                         }
+                        if constexpr (LOW) {  // the small products first: the tensor cores' sums lose bits at each step
+                            mma_f16(acc, a[0][0], a[0][1], a[0][2], a[0][3], BL[G][0][0], BL[G][0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                            mma_f16(acc, a[1][0], a[1][1], a[1][2], a[1][3], BL[G][1][0], BL[G][1][1]);
+                            mma_f16(acc, a[0][0], a[0][1], a[0][2], a[0][3], B[G][0][0], B[G][0][1]);
+                        } else {
+                            const float c0 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][0], c1 = CENTRE ? 0.0f : cinit[CENTRE ? 0 : G][1];
+                            mma_f16(acc, a[0][0], a[0][1], a[0][2], a[0][3], B[G][0][0], B[G][0][1], c0, c1, c0, c1);
+                        }
+                        mma_f16(acc, a[1][0], a[1][1], a[1][2], a[1][3], B[G][1][0], B[G][1][1]);
                         const float2 d0 = unpack_f16(st[0][G / 2]), d1 = unpack_f16(st[1][G / 2]);
                         const float s0 = (G & 1) ? d0.y : d0.x, s1 = (G & 1) ? d1.y : d1.x;
 #pragma unroll
@@ -752,8 +754,13 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                         for (int mm = 0; mm < 2; ++mm) {
                             const uint32_t v0 = mm ? y0 >> 8 : y0, v1 = mm ? y1 >> 8 : y1;
                             const uint32_t a0 = centre_lo(ck, v0), a1 = centre_hi(ck, v0), a2 = centre_lo(ck, v1), a3 = centre_hi(ck, v1);
+                            if constexpr (LOW) {  // added here, rounded: 2.4e-7 off 64 bits, 8.7e-7 as products into O, 4% faster
+                                float y[4];
+                                mma_f16(y, a0, a1, a2, a3, xl[0], xl[1], 0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) O[G][mm][i] += y[i];
+                            }
                             mma_f16(O[G][mm], a0, a1, a2, a3, x[0], x[1]);
-                            if constexpr (LOW) mma_f16(O[G][mm], a0, a1, a2, a3, xl[0], xl[1]);
                         }
                     }
                 }
@@ -1036,8 +1043,8 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     // f32 enters as high and low parts for its accuracy: side by side in tiles of 4 rows, or in
     // tiles of 8 with a product more for the low parts, which decode a key for twice the rows.
     // By the rows a sequence and key head, on average (us in tiles of 4, of 8): 256 sequences of
-    // 1000 keys, 8 rows 119, 117, 16 rows 180, 161, 64 rows 693, 505; one of 600 keys, 8 rows
-    // 11.0, 12.7, 64 rows 13.9, 14.8.  Half precision takes tiles of 4 where a tile of 8 would only
+    // 1000 keys, 8 rows 119, 123, 16 rows 180, 169, 64 rows 693, 533; one of 600 keys, 8 rows
+    // 11.1, 12.9, 64 rows 13.9, 15.2.  Half precision takes tiles of 4 where a tile of 8 would only
     // be padded (4 rows: 88, 91), and eights from there on.  (Two such column tiles, which decode
     // a key once for both, leave 8 warps a multiprocessor instead of 12: 16 rows 182 us
     // against 130 in bf16, 184 against 180 in f32.)
