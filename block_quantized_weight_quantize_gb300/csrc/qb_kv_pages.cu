@@ -379,7 +379,8 @@ struct CopyK {
 constexpr int kCopyThreads = 256, kCopyVecs = 4;  // 16 KB a block and turn
 
 __global__ void __launch_bounds__(kCopyThreads) kv_pages_copy_kernel(const CopyK p) {
-    pdl_launch_dependents();
+    // no early launch_dependents: the pages may be those of the int8 cache, whose
+    // score kernel reads key rows before its own pdl_wait
     pdl_wait();
     const int n = p.count ? p.count[0] : p.n;
     const int64_t vecs = p.page_bytes / 16;

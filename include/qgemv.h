@@ -36,8 +36,10 @@
  * stream finishes, and waits for it before it reads activations or writes
  * outputs.  So weights and the key cache must be complete before that
  * previous kernel signals its dependents: true for any kernel that does not
- * trigger them early, and for kv_cache_rows, which lets its successor start
- * only when it has finished.
+ * trigger them early, and for kv_cache_rows and the page copies (kv_pages_copy,
+ * kv_pages_fork, kv_pages_compact), which let their successor start only when
+ * they have finished.  The other calls' outputs (kv4_read's rows among them) are
+ * not weights or key caches of the call right after them.
  *
  * Errors: 0 on success, else a negative QB_E_* code (argument checks happen
  * on the host before any launch; nothing is launched on error).

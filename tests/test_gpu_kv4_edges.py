@@ -1,0 +1,61 @@
+"""The paged 4-bit cache at its edges on the GPU."""
+import numpy as np
+import pytest
+
+import block_quantized_weight_quantize_gb300 as qb
+from test_gpu_kv4 import _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    qb.lib()
+    yield
+    torch.cuda.synchronize()
+    assert qb.q_device_status() == qb.QB_OK
+
+
+@pytest.mark.parametrize("call", ["copy", "fork", "compact"])
+def test_scores_right_after_page_copies(call):
+    """Pages of the int8 key cache are copied and scored at once: the scores are those of the copied rows."""
+    import torch
+    nkv, nh, d, page, half = 4, 8, 128, 16, 1024
+    npages = 2 * half
+    lcap = npages * page
+    rng = np.random.default_rng(61)
+    qc = torch.from_numpy(rng.integers(-127, 128, (nh, d), dtype=np.int8)).cuda()
+    qs = torch.full((nh, 1), 128, dtype=torch.int32, device="cuda")           # 128 * 2^0
+    ks = torch.full((nkv, lcap), 0x3C00, dtype=torch.int16, device="cuda")    # 1.0
+    for turn in range(4):
+        kc = torch.from_numpy(rng.integers(-127, 128, (nkv, lcap, d), dtype=np.int8)).cuda()
+        want_kc = kc.clone().view(nkv, npages, page * d)
+        want_kc[:, :half] = want_kc[:, half:]                                  # page half + i to page i
+        want, got = (torch.zeros((nh, lcap), device="cuda") for _ in range(2))
+        qb.kv_scores(qb.PERBLOCK, qc, qs, d, want_kc.view(nkv, lcap, d), ks, lcap, 0.125, want)
+        data = kc.view(nkv, npages, page * d)
+        refs = np.zeros(npages, np.int32)
+        refs[half:] = 1
+        free = np.concatenate([np.arange(half)[::-1], np.full(half, -1)])      # page 0 the next to go
+        status = torch.zeros(half, dtype=torch.int32, device="cuda")
+        if call == "compact":                                                  # one sequence holds the upper half
+            tables, lens = np.arange(half, npages)[None], [half * page]
+        else:                                                                  # each page a sequence of its own, partly filled
+            tables = np.full((npages, 1), -1)
+            tables[:half, 0] = np.arange(half, npages)
+            lens = [page - 1] * half + [0] * half
+        pages = qb.KvPages(page, _i32([half]), _i32(free), _i32(refs), _i32(lens), _i32(tables))
+        work = torch.empty(qb.kv_pages_workspace_bytes(pages), dtype=torch.uint8, device="cuda")
+        lo, hi = _i32(np.arange(half)), _i32(np.arange(half, npages))
+        torch.cuda.synchronize()
+        if call == "copy":
+            qb.kv_pages_copy(data, npages, hi, lo)
+        elif call == "fork":
+            qb.kv_pages_fork(pages, data, lo, hi, status, work)
+        else:
+            qb.kv_pages_compact(pages, data, work)
+        qb.kv_scores(qb.PERBLOCK, qc, qs, d, kc, ks, lcap, 0.125, got)
+        assert torch.equal(got, want) and int(status.min()) == 0
+        assert torch.equal(kc, want_kc.view(nkv, lcap, d))
