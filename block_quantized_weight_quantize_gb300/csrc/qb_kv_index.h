@@ -1,0 +1,22 @@
+// qb_kv_index.h -- index arithmetic of the paged caches that has to hold at the
+// ends of its ranges.  Plain C++, so that a host compiler takes it as well.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define QB_HD __host__ __device__ __forceinline__
+#else
+#define QB_HD inline
+#endif
+
+namespace qb {
+
+// Slots that a request of `count` tokens may write, its first one being entry
+// `first` of `nslots`.
+QB_HD int64_t kv_slots_room(int64_t count, int64_t first, int64_t nslots) {
+    const int64_t left = nslots > first ? nslots - first : 0;
+    return count < left ? count : left;
+}
+
+}  // namespace qb

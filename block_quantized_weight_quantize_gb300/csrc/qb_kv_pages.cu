@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "qb_kv4.cuh"
+#include "qb_kv_index.h"
 
 namespace qb {
 
@@ -164,14 +165,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_extend_kernel(const Pag
                 }
             }
             __syncwarp();
-            for (int t = lane; t < c; t += 32) {
-                const int pos = o + t;
-                const int pg = rr >= 0 ? tab[pos >> pshift] : -1;
-                if (t0 + t < nslots)
-                    slots[t0 + t] = pg < 0 ? -1 : (pg << pshift) + (pos & (p.page - 1));
-                else
-                    atomicOr(p.fault, kFaultIndex);
+            // a refused request's count may be any: only the entries that `slots` has
+            const int64_t room = kv_slots_room(c, t0, nslots);
+            for (int64_t t = lane; t < room; t += 32) {
+                int slot = -1;
+                if (rr >= 0) {
+                    const int pos = o + (int)t, pg = tab[pos >> pshift];
+                    if (pg >= 0) slot = (pg << pshift) + (pos & (p.page - 1));
+                }
+                slots[t0 + t] = slot;
             }
+            if (lane == 0 && room < c) atomicOr(p.fault, kFaultIndex);
         }
         __syncthreads();
     }

@@ -59,3 +59,34 @@ def test_scores_right_after_page_copies(call):
         qb.kv_scores(qb.PERBLOCK, qc, qs, d, kc, ks, lcap, 0.125, got)
         assert torch.equal(got, want) and int(status.min()) == 0
         assert torch.equal(kc, want_kc.view(nkv, lcap, d))
+
+
+def test_slots_of_requests_of_any_count():
+    """Refused requests of up to 2^31 - 1 tokens, and an array of slots that ends in the middle: nothing outside is written."""
+    import torch
+    page, npages, nrows, maxp = 16, 40, 8, 4
+    d = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, npages, npages, nrows, (nrows, maxp))]
+    pages = qb.KvPages(page, *d)
+    for counts, nslots, want_status in (([3, 2 ** 31 - 1, 5], 50, [0, -8, 0]), ([2 ** 31 - 1, 2 ** 31 - 32, 2 ** 31 - 20], 7, [-8] * 3),
+                                        ([20, 1 << 30, 4], 22, [0, -8, 0]), ([64, 2 ** 31 - 31, 64], 0, [0, -8, 0])):
+        qb.kv_pages_reset(pages)
+        wide = torch.full((nslots + 4096,), -7, dtype=torch.int32, device="cuda")
+        slots = wide[2048:2048 + nslots] if nslots else wide[2048:2048]
+        status = torch.full((3,), 5, dtype=torch.int32, device="cuda")
+        rows = [1, 2, 3]
+        if nslots:
+            qb.kv_pages_extend(pages, _i32(rows), _i32(counts), slots, status)
+        else:  # the entry itself: an array of no entries
+            from block_quantized_weight_quantize_gb300 import kv4
+            r, c = _i32(rows), _i32(counts)
+            assert kv4._c.kv_pages_extend(pages.ref, r.data_ptr(), c.data_ptr(), 3, wide.data_ptr() + 8192, 0, status.data_ptr(),
+                                          torch.cuda.current_stream().cuda_stream) == qb.QB_OK
+        assert status.tolist() == want_status
+        want, page_at = [], 0
+        for n, st in zip(counts, want_status):
+            want += [page * page_at + t if st == 0 else -1 for t in range(min(n, 64))] if st == 0 else [-1] * min(n, nslots)
+            page_at += -(-n // page) if st == 0 else 0
+        assert slots.tolist() == want[:nslots]
+        assert (wide[:2048] == -7).all() and (wide[2048 + nslots:] == -7).all()
+        assert d[3].tolist()[1:4] == [n if st == 0 else 0 for n, st in zip(counts, want_status)]
+        assert qb.q_device_status() == qb.QB_E_INDEX

@@ -1,11 +1,40 @@
 """The paged 4-bit cache at its edges, on a host without a GPU: what calls without work, orders of kernels and index
 arithmetic have to keep to."""
+import ctypes
 import pathlib
 import re
+import shutil
+import subprocess
 
 import pytest
 
 CSRC = pathlib.Path(__file__).resolve().parent.parent / "block_quantized_weight_quantize_gb300" / "csrc"
+TOP = 2 ** 31
+
+
+@pytest.fixture(scope="module")
+def index(tmp_path_factory):
+    """The functions of qb_kv_index.h as a host library, every signed overflow an abort."""
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    d = tmp_path_factory.mktemp("index")
+    (d / "i.cpp").write_text("""#include "qb_kv_index.h"
+extern "C" long long room(long long c, long long first, long long n) { return qb::kv_slots_room(c, first, n); }
+""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", str(CSRC), str(d / "i.cpp"),
+                    "-o", str(d / "i.so")], check=True)
+    lib = ctypes.CDLL(str(d / "i.so"))
+    lib.room.argtypes, lib.room.restype = [ctypes.c_longlong] * 3, ctypes.c_longlong
+    return lib
+
+
+@pytest.mark.parametrize("count", [0, 1, 31, 32, 100, TOP - 33, TOP - 32, TOP - 31, TOP - 1])
+@pytest.mark.parametrize("first", [0, 1, 49, 50, 51, TOP - 1, (TOP - 1) * (1 << 20)])
+def test_slots_of_a_request_stay_in_their_array(index, count, first):
+    """Whatever a request's count and place: the entries first .. first + room - 1 are in the array, and all of the request's that are."""
+    for nslots in (0, 1, 50, TOP - 1, TOP * 8):
+        room = index.room(count, first, nslots)
+        assert room == len(range(first, min(first + count, nslots)))
 
 
 @pytest.mark.parametrize("file,kernel", [("qb_kv.cu", "kv_cache_rows_kernel"), ("qb_kv_pages.cu", "kv_pages_copy_kernel")])
