@@ -6,8 +6,13 @@
 // products bound it, so keys and values are decoded once a tile to f16
 // ((code - 8) * step, rounded once) and the tensor cores do the rest:
 //     S = Q K^T (f32), P = 2^(S cs - m) (f16), O += P V (f32),
-// m a running maximum that moves only when it has to rise by more than 8 (the
-// factor 2^8 fits f16), when O is rescaled in tensor memory; sums in f32.
+// m 11 below a running maximum, which moves only when P would pass f16's top, when
+// O is rescaled in tensor memory; sums in f32.  The largest probability then lies at
+// 2^11 to 2^15.9 (2^11 itself where m has last moved, so that it is not rounded), and
+// f16's last place, 2^-24, is 2^-35 of it or less: what is below 2^-36 vanishes.
+// (13 instead of 11: m moves more often, 330 us for 2048 tokens on 8192 keys, 32
+// heads of 128, against 258; m at the maximum and 8 let pass: 256 us, but what is
+// below 2^-25 vanishes.)
 //
 // A rounded key moves a score by 2^-12 of its terms, which averages out over many
 // keys but not over few: lse is off by 1e-5 to 2e-5 of itself at 100 keys, 3e-6 at
@@ -40,7 +45,8 @@
 // that unpacking gives, and is undone in Q's rows and the output's columns.
 //
 // Values out of the ordinary: a key whose steps reach 2^12 is decoded 2^-4
-// smaller, and its scores or probabilities multiplied by 16; a group whose step
+// smaller, and its scores or probabilities multiplied by 16 (a row that sees such a
+// value keeps 2^4 more room under f16's top); a group whose step
 // is not finite is decoded as zeros and marks the rows that see it, whose
 // outputs of that group are NaN.
 #pragma once
@@ -63,7 +69,7 @@ struct PromptK {
     int grp;
     int min_share;  // tiles a block
     float *part;    // [grid][2][kPromptRows][DP]: a block's pieces (0: of an item begun before it)
-    float2 *stat;   // [grid][2][kPromptRows] running maximum, sum
+    float2 *stat;   // [grid][2][kPromptRows] m of the probabilities, sum
     int *last;      // [grid] the last block that holds a piece of the item that starts here and goes on; -1: none
     int4 *meta;     // [grid] that item's first token, tokens, key head, row pair
 };
@@ -133,20 +139,25 @@ __device__ __forceinline__ bool prompt_wait(uint64_t *bar, uint32_t parity, int 
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// The groups that are not finite among the keys lo..hi of a step.
-__device__ __forceinline__ uint32_t prompt_bad(const uint16_t *flags, int lo, int hi) {
-    uint32_t bad = 0;
-    for (int i = max(lo, 0); i <= min(hi, kPromptTile - 1); ++i) bad |= flags[i] >> 8;
-    return bad;
+// The flags among the keys lo..hi of a step, together.
+__device__ __forceinline__ uint32_t prompt_flags(const uint16_t *flags, int lo, int hi) {
+    uint32_t all = 0;
+    for (int i = max(lo, 0); i <= min(hi, kPromptTile - 1); ++i) all |= flags[i];
+    return all;
 }
+
+// The probability of the maximum that m was taken from is 2^kPromptTop, and m rises
+// when one would pass 2^kPromptMost (f16 ends at 2^16).
+constexpr float kPromptTop = 11.0f, kPromptMost = 15.9f;
 
 // What a row's softmax carries from tile to tile.
 struct PromptRow {
-    float cs, m, l;   // factor of the scores, running maximum, sum
+    float cs, m, l;   // factor of the scores, m of the probabilities, sum
+    float up;         // 4 where the row sees a key of the step whose probability is 16 times larger
     int lo, hi;       // columns lo..hi of the step are seen
 };
 
-// The maximum rises to mn in lanes where that is more than m: O (DP columns, if
+// m rises to mn in lanes where that is more: O (DP columns, if
 // any products were added), the `done` columns of this step's probabilities and the sum shrink.
 template <int DP>
 __device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
@@ -220,14 +231,14 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
             t0 = fmaxf(t0, __uint_as_float(x[i]));
             t1 = fmaxf(t1, __uint_as_float(x[i + 1]));
         }
-        const float z = fmaxf(t0, t1) * row.cs;
-        if (__any_sync(0xFFFFFFFFu, z > row.m + 8.0f)) {
+        const float z = fmaxf(t0, t1) * row.cs + (ODD ? row.up : 0.0f);
+        if (__any_sync(0xFFFFFFFFu, z > row.m + kPromptMost)) {
             // no score stays in a register meanwhile: they are read again
             tc_ld_wait(next);
             const float2 part = unpair_f32(sum);
             row.l += part.x + part.y;
             sum = 0;
-            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, z > row.m + 8.0f ? z : row.m, have_o, o_done, parity, fault) && ok;
+            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, z > row.m + kPromptMost ? z - kPromptTop : row.m, have_o, o_done, parity, fault) && ok;
             tc_ld32_begin(tS + 32 * c, x);
             tc_ld_wait(x);
             if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), next);
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
             const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : INT_MAX;  // no row: whatever comes out
             const int first_hi = p.a.window && j_lo < it.T ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
-            PromptRow row = {cs, -INFINITY, 0.0f, 0, 0};
+            PromptRow row = {cs, -INFINITY, 0.0f, 0.0f, 0, 0};
             uint32_t bad = 0;
             const int n_tiles = it.n, t_first = it.t0;
             for (int i = 0; i < n_tiles; ++i, ++tiles) {
@@ -562,7 +573,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 row.hi = pos - k0;
                 row.lo = first - k0;
                 if (odd) {
-                    bad |= prompt_bad(flags, row.lo, row.hi);
+                    const uint32_t fl = prompt_flags(flags, row.lo, row.hi);
+                    bad |= fl >> 8;
+                    row.up = fl & 2u ? 4.0f : 0.0f;
                     ok = prompt_step<DP, true, true>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else if (masked) {
                     ok = prompt_step<DP, true, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 
 import block_quantized_weight_quantize_gb300 as qb
-from test_gpu_kv4 import _i32
+import kv4_ref as ref
+from test_gpu_kv4 import OUT, SUM, Batch, _fill, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,63 @@ def test_slots_of_requests_of_any_count():
         assert (wide[:2048] == -7).all() and (wide[2048 + nslots:] == -7).all()
         assert d[3].tolist()[1:4] == [n if st == 0 else 0 for n, st in zip(counts, want_status)]
         assert qb.q_device_status() == qb.QB_E_INDEX
+
+
+# A row's probabilities next to a key far above the others.  Tolerance, from the stored values: a score is off by at most
+# its magnitudes' sum Z times 2^-19 (f32 sums; queries are exact in f16, keys as two f16) or times 2^-11 more where keys are
+# rounded to f16 (a row that sees 2048 keys or more), a probability by twice that relatively, probabilities and values are f16 (2^-11 each, or
+# one product of 2^-11 in the step kernel), the output is rounded once, and each probability may lose `low` of the largest (as the header states).
+# An f16 output has an absolute 2^-25 besides (its least place).
+
+def _check_probabilities(b, name, scale, low, dims=slice(None)):
+    out, lse = b.run(scale)
+    want, wlse, zabs, mag = b.want(scale)
+    off = zabs * (SUM + (2.0 ** -11 if b.lens[0] - b.news[0] + 1 >= 2048 else 0.0))
+    tol = (2 * off + 2.0 ** -10 + SUM)[..., None] * mag + OUT[name] * np.abs(want) + 2.0 ** -25 * (name == "f16")
+    tol += len(b.v) * np.abs(b.v).max() * low
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - want)[..., dims] <= tol[..., dims]), np.max((np.abs(got - want) / tol)[..., dims])
+    assert np.all(np.abs(lse.double().cpu().numpy() - wlse) <= off + SUM * (1 + np.abs(wlse)))
+
+
+def _beside_one_key(name, d, n, T, gap, place, seed=71):
+    """Queries u + noise; key `place` is gap nats above the others for every row, its value zero, the others' 30 +- 10."""
+    b = Batch(seed, [n], [T], 2, 1, d, 32, name)
+    rng = np.random.default_rng(seed)
+    u = np.where(np.arange(d) % 2, 1.0, -1.0)
+    import torch
+    b.q = torch.from_numpy((u + 0.05 * rng.standard_normal((T, 2, d))).astype(np.float32)).cuda().to(b.q.dtype)
+    k = rng.standard_normal((n, 1, d)) * 0.05
+    v = 30.0 + 10.0 * rng.standard_normal((n, 1, d))
+    k[place, 0] = u * gap * d ** -0.5
+    v[place] = 0.0
+    _fill(b, k, v)
+    return b
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 18.0, 21.0])
+@pytest.mark.parametrize("d,n,T,place", [(64, 1900, 100, 3), (128, 900, 100, 780), (128, 2300, 120, 0), (64, 300, 20, 3)])
+def test_small_probabilities_beside_a_large_one(name, gap, d, n, T, place):
+    """Probabilities of 2^-14 to 2^-30 of the largest make up the output, through both kernels."""
+    _check_probabilities(_beside_one_key(name, d, n, T, gap, place), name, d ** -0.5, 2.0 ** (-36 if T >= 100 else -38))
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("at", [5, 130, 640])
+def test_small_probabilities_beside_a_large_value(name, at):
+    """The same with a value of steps past 2^12 in one group of a key without weight in the sum: the other groups' outputs."""
+    d = 128
+    b = _beside_one_key(name, d, 700, 100, 12.0, 3)
+    v = b.v.copy()
+    v[at, 0, 32:64] = np.resize([3e5, -3e5], 32)
+    k = b.k.copy()
+    u = np.where(np.arange(d) % 2, 1.0, -1.0)
+    k[at, 0] = -u * 40.0 * d ** -0.5
+    _fill(b, k, v)
+    big = b.v[:, :, 32:64].copy()
+    b.v[at, 0, 32:64] = 0.0     # the sum of magnitudes in the bound is that of the other groups
+    try:
+        _check_probabilities(b, name, d ** -0.5, 2.0 ** -32, np.r_[0:32, 64:128])
+    finally:
+        b.v[:, :, 32:64] = big
