@@ -11,7 +11,7 @@
 // 2^11 to 2^15.9 (2^11 itself where m has last moved, so that it is not rounded), and
 // f16's last place, 2^-24, is 2^-35 of it or less: what is below 2^-36 vanishes.
 // (13 instead of 11: m moves more often, 330 us for 2048 tokens on 8192 keys, 32
-// heads of 128, against 258; m at the maximum and 8 let pass: 256 us, but what is
+// heads of 128, against 257; m at the maximum and 8 let pass: 256 us, but what is
 // below 2^-25 vanishes.)
 //
 // A rounded key moves a score by 2^-12 of its terms, which averages out over many
@@ -158,12 +158,14 @@ struct PromptRow {
 };
 
 // m rises to mn in lanes where that is more: O (DP columns, if
-// any products were added), the `done` columns of this step's probabilities and the sum shrink.
+// any products were added), the `done` columns of this step's probabilities and the sums l
+// and `sum` shrink; nothing of the other lanes changes, whose rows keep their bits.
 template <int DP>
-__device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, float mn,
-                                                   bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
+__device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, uint64_t &sum,
+                                                   float mn, bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
     const float al = mn == m ? 1.0f : prompt_ex2(m - mn);
     l *= al;
+    sum = mul_f32x2(sum, pair_f32(al, al));
     m = mn;
     if (have_o) {
         if (!prompt_wait(o_done, parity, fault)) return false;
@@ -235,10 +237,7 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
         if (__any_sync(0xFFFFFFFFu, z > row.m + kPromptMost)) {
             // no score stays in a register meanwhile: they are read again
             tc_ld_wait(next);
-            const float2 part = unpair_f32(sum);
-            row.l += part.x + part.y;
-            sum = 0;
-            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, z > row.m + kPromptMost ? z - kPromptTop : row.m, have_o, o_done, parity, fault) && ok;
+            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, sum, z > row.m + kPromptMost ? z - kPromptTop : row.m, have_o, o_done, parity, fault) && ok;
             tc_ld32_begin(tS + 32 * c, x);
             tc_ld_wait(x);
             if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), next);

@@ -19,9 +19,10 @@
 // a packed addition takes 1032 off (the sum of q or p times 8 taken off at the end
 // costs f32 its last three bits: an error of 1.4e-6 against 2.1e-7).  Queries are
 // scaled by a power of two a row to f16's top; in f32 they enter as two f16 (22
-// bits).  The probabilities times steps likewise, scaled by a power of two that
-// follows the largest step seen (as the running maximum does), and pass from the
-// scores' layout to the B side by an 8 x 8 transpose in registers.
+// bits).  The probabilities times steps likewise, scaled by a power of two a row that
+// follows the largest step that the row sees (as the running maximum does; one for all
+// rows of a tile would let a row's bits depend on values that it does not see), and
+// pass from the scores' layout to the B side by an 8 x 8 transpose in registers.
 //
 // Layout.  A lane of the A fragment (row g, slots of t) needs 8 elements of key g
 // in one word: the cache's key rows are ordered so that one wide load holds a
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
 
         float O[NG][2][4];
         float m[NH], l[NH];
-        int eb = 1;  // biased exponent (binary16's) of the largest step so far
+        int eb[NH];  // biased exponent (binary16's) of the largest step that the row has seen
 #pragma unroll
         for (int G = 0; G < NG; ++G)
 #pragma unroll
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         for (int h = 0; h < NH; ++h) {
             m[h] = -INFINITY;
             l[h] = 0.0f;
+            eb[h] = 1;
         }
 
         auto unit = [&](const uint8_t *ub, int k0, auto masked) {
@@ -621,14 +623,6 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             uint32_t seen[NH];  // bit 2 b + i: the row sees that key
             if constexpr (masked) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (k0 + 16 * b + 8 * i + krow >= s_len) {  // a place that holds no key may hold anything
-#pragma unroll
-                            for (int h = 0; h < NG / 2; ++h) vs[b][i][h] = 0;
-                        }
-#pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     const int j = (s_rt * R + (PAIR ? t : 2 * t + h)) / p.grp;
                     const int pos = j < s_T ? s_len - s_T + j : -1;
@@ -642,26 +636,39 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                 }
             }
             // ---- the running maximum and the steps' largest exponent; both rarely move
-            __half2 top2 = __float2half2_rn(0.0f);
-#pragma unroll
-            for (int k = 0; k < 2 * NB; ++k)
-#pragma unroll
-                for (int h = 0; h < NG / 2; ++h)
-                    top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&vs[k >> 1][k & 1][h])));
-            top2 = __hmax2(top2, __lowhigh2highlow(top2));
-            uint32_t tb = *reinterpret_cast<const uint32_t *>(&top2) & 0xFFFFu;
-            if (tb >= 0x7C00u) {  // a step that is not finite says nothing about the others
-                tb = 0;
+            // the keys that a row does not see, and places that hold no key, may hold any step
+            auto largest_step = [&](int h) {
+                __half2 top2 = __float2half2_rn(0.0f);
+                auto steps = [&](int k, int i) {
+                    if constexpr (masked) return seen[h] >> k & 1 ? vs[k >> 1][k & 1][i] : 0u;
+                    else return vs[k >> 1][k & 1][i];
+                };
 #pragma unroll
                 for (int k = 0; k < 2 * NB; ++k)
 #pragma unroll
-                    for (int h = 0; h < NG / 2; ++h) {
-                        const uint32_t lo = vs[k >> 1][k & 1][h] & 0x7FFFu, hi = vs[k >> 1][k & 1][h] >> 16 & 0x7FFFu;
-                        if (lo < 0x7C00u) tb = max(tb, lo);
-                        if (hi < 0x7C00u) tb = max(tb, hi);
+                    for (int i = 0; i < NG / 2; ++i) {
+                        const uint32_t u = steps(k, i);
+                        top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2 *>(&u)));
                     }
-            }
-            bool moved = (int)(tb >> 10) > eb;
+                top2 = __hmax2(top2, __lowhigh2highlow(top2));
+                uint32_t tb = *reinterpret_cast<const uint32_t *>(&top2) & 0xFFFFu;
+                if (tb >= 0x7C00u) {  // a step that is not finite says nothing about the others
+                    tb = 0;
+#pragma unroll
+                    for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                        for (int i = 0; i < NG / 2; ++i) {
+                            const uint32_t u = steps(k, i), lo = u & 0x7FFFu, hi = u >> 16 & 0x7FFFu;
+                            if (lo < 0x7C00u) tb = max(tb, lo);
+                            if (hi < 0x7C00u) tb = max(tb, hi);
+                        }
+                }
+                return tb;
+            };
+            uint32_t tb[NH];
+            tb[0] = largest_step(0);
+            if constexpr (NH == 2) tb[1] = masked ? largest_step(1) : tb[0];
+            bool moved = false;
             float top[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
@@ -675,20 +682,20 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                     z[k >> 1][k & 1][h] = y;
                     top[h] = fmaxf(top[h], y);
                 }
-                moved |= top[h] > m[h];
+                moved |= top[h] > m[h] || (int)(tb[h] >> 10) > eb[h];
             }
             if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) tb = max(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, o));
-                const int eb_new = max(eb, (int)(tb >> 10));
-                const float fe = __uint_as_float((uint32_t)(127 + eb - eb_new) << 23);
-                eb = eb_new;
                 float f[NH];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
 #pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1)
+                    for (int o = 4; o <= 16; o <<= 1) {
                         top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], o));
+                        tb[h] = max(tb[h], __shfl_xor_sync(0xFFFFFFFFu, tb[h], o));
+                    }
+                    const int eb_new = max(eb[h], (int)(tb[h] >> 10));
+                    const float fe = __uint_as_float((uint32_t)(127 + eb[h] - eb_new) << 23);
+                    eb[h] = eb_new;
                     f[h] = top[h] == m[h] ? 1.0f : ex2(m[h] - top[h]);
                     l[h] *= f[h];
                     f[h] *= fe;
@@ -699,9 +706,9 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
 #pragma unroll
                     for (int i = 0; i < 8; ++i) O[G][i / 4][i % 4] *= f[PAIR ? 0 : i & 1];
             }
-            const float pe = __uint_as_float((uint32_t)(127 + 28 - eb) << 23);  // |step| * pe < 2^14
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
+                const float pe = __uint_as_float((uint32_t)(127 + 28 - eb[h]) << 23);  // |step| * pe < 2^14
                 const float mm = m[h] == -INFINITY ? 0.0f : m[h];
 #pragma unroll
                 for (int k = 0; k < 2 * NB; ++k) {
@@ -792,12 +799,12 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
 
         // ---- the item's rows: out, or this piece's sums
         const bool whole = from_start && to_end;
-        const float fo = __uint_as_float((uint32_t)(127 - 28 + eb) << 23);  // undoes pe
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             float sum = l[h];
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float fo = __uint_as_float((uint32_t)(127 - 28 + eb[h]) << 23);  // undoes pe
             const float f = !whole ? fo : sum == 0.0f ? 0.0f : fo / sum;
             const int row = (PAIR ? t : 2 * t + h), rho = s_rt * R + row, j = rho / p.grp;
             if (j >= s_T) continue;

@@ -494,9 +494,10 @@ QB_API int64_t kv4_attn_workspace_bytes(const qb_kv4 *cache, int nh);
  * tokens; lse f32 [ntok][nh] or NULL.  Sums and softmax statistics are f32; with
  * QB_T_F32 queries and probabilities enter the products as pairs of f16 (22
  * bits), otherwise as one f16.  A probability (of the largest, 1) below 2^-38
- * may vanish beside the largest step among the values; in half-precision calls
- * of many tokens one below 2^-36, or below 2^-32 where the token sees a value
- * step of 2^12 or more.  Queries of magnitude past 2^110 are out of range.  q, out 16-byte aligned, strides multiples of 16
+ * may vanish beside the largest step among the values that the token sees; in
+ * half-precision calls of many tokens one below 2^-36, or below 2^-32 where the
+ * token sees a value step of 2^12 or more.  A key or value that a token does not
+ * see changes no bit of its output.  Queries of magnitude past 2^110 are out of range.  q, out 16-byte aligned, strides multiples of 16
  * bytes; nh % nkv == 0; ntok <= 2^24, ntok * nh <= 2^30.
  * workspace: at least kv4_attn_workspace_bytes() bytes, 16-byte aligned, not
  * shared with a call that may run at the same time.  A length past its table row is cut to it; a row

@@ -151,3 +151,27 @@ def test_small_probabilities_beside_a_large_value(name, at):
         _check_probabilities(b, name, d ** -0.5, 2.0 ** -32, np.r_[0:32, 64:128])
     finally:
         b.v[:, :, 32:64] = big
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("nh,nkv,d,page,T,window", [(1, 1, 64, 16, 3, 0), (4, 2, 128, 64, 5, 0), (8, 1, 256, 32, 3, 0), (4, 1, 128, 16, 1, 50), (12, 2, 64, 64, 1, 50),
+                                                    (3, 1, 256, 16, 1, 50), (4, 2, 64, 16, 150, 0), (4, 1, 128, 32, 70, 45)])
+def test_finite_keys_and_values_that_a_token_does_not_see(name, nh, nkv, d, page, T, window):
+    """A key and a value near the top of the format's range in one place: tokens that do not see it keep their bits."""
+    import torch
+    n = 190
+    b = Batch(81, [n], [T], nh, nkv, d, page, name)
+    _fill(b, b.k, b.v * 0.01)
+    scale = 0.05
+    clean, clean_lse = b.run(scale, window)
+    place = n - 1 - window if T == 1 else n - T // 2 - 1   # just left of the window; seen by the later tokens
+    k, v = b.k.copy(), b.v.copy()
+    v[place] = np.resize([4e5, -3e5, 2.0], d)
+    k[place] *= 1e4
+    _fill(b, k, v)
+    out, lse = b.run(scale, window)
+    pos = n - T + np.arange(T)
+    seen = (pos >= place) & ((pos < place + window) | (window == 0))
+    not_seen = torch.from_numpy(~seen).cuda()
+    assert (~seen).any() and seen.any() == (T > 1)
+    assert torch.equal(out[not_seen], clean[not_seen]) and torch.equal(lse[not_seen], clean_lse[not_seen])
