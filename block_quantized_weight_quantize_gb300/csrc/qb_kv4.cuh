@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "qb_common.cuh"
+#include "qb_kv_index.h"
 #include "qb_launch.h"
 
 namespace qb {

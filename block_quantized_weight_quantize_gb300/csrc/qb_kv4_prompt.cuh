@@ -280,7 +280,7 @@ __device__ __forceinline__ int prompt_pairs(const PromptK &p, int T) { return (T
 __device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, int rp, int &t0) {
     const int j_lo = rp * kPromptRows / p.grp, j_hi = min(T - 1, (rp * kPromptRows + kPromptRows - 1) / p.grp);
     const int pos_lo = len - T + j_lo, pos_hi = len - T + j_hi;
-    t0 = (p.a.window ? max(0, pos_lo - p.a.window + 1) : 0) / kPromptTile;
+    t0 = kv_first_seen(pos_lo, p.a.window) / kPromptTile;
     return max(1, pos_hi < 0 ? 0 : pos_hi / kPromptTile + 1 - t0);
 }
 
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
             const bool live = j < it.T;
             const int pos = live ? it.len - it.T + j : -1;
-            const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
+            const int first = kv_first_seen(pos, p.a.window);
             const int64_t tok = it.q0 + j;
             const int head = it.kvh * p.grp + rho - j * p.grp;
             const int64_t at = tok * p.a.out_stride + (int64_t)head * p.a.c.d;  // of the row's output
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
             const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
             const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : INT_MAX;  // no row: whatever comes out
-            const int first_hi = p.a.window && j_lo < it.T ? max(0, it.len - it.T + j_hi - p.a.window + 1) : 0;
+            const int first_hi = j_lo < it.T ? kv_first_seen(it.len - it.T + j_hi, p.a.window) : 0;
             PromptRow row = {cs, -INFINITY, 0.0f, 0.0f, 0, 0};
             uint32_t bad = 0;
             const int n_tiles = it.n, t_first = it.t0;

@@ -149,7 +149,7 @@ __device__ __forceinline__ void lds(const uint8_t *p, uint32_t (&w)[N]) {
 // units of U keys of one item of the sequence: from the unit of its first seen key to its end (one at least)
 template <int U>
 __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0, int &nu) {
-    const int first = window ? max(0, q.len - q.T - window + 1) : 0;
+    const int first = kv_first_seen(q.len - q.T, window);
     u0 = first / U;
     nu = max(1, (q.len + U - 1) / U - u0);
 }
@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         // units whose keys every row sees need no mask
         const int pos_lo = s_len - s_T + (s_rt * R) / p.grp;
         const int pos_hi = s_len - s_T + min(s_T - 1, (s_rt * R + R - 1) / p.grp);
-        const int first_hi = p.a.window ? max(0, pos_hi - p.a.window + 1) : 0;
-        const int first_lo = p.a.window ? max(0, pos_lo - p.a.window + 1) : 0;
+        const int first_hi = kv_first_seen(pos_hi, p.a.window);
+        const int first_lo = kv_first_seen(pos_lo, p.a.window);
 
         float O[NG][2][4];
         float m[NH], l[NH];
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                 for (int h = 0; h < NH; ++h) {
                     const int j = (s_rt * R + (PAIR ? t : 2 * t + h)) / p.grp;
                     const int pos = j < s_T ? s_len - s_T + j : -1;
-                    const int first = p.a.window ? max(0, pos - p.a.window + 1) : 0;
+                    const int first = kv_first_seen(pos, p.a.window);
                     seen[h] = 0;
 #pragma unroll
                     for (int k = 0; k < 2 * NB; ++k) {

@@ -19,4 +19,8 @@ QB_HD int64_t kv_slots_room(int64_t count, int64_t first, int64_t nslots) {
     return count < left ? count : left;
 }
 
+// The first key that a token at place `pos` sees (negative: a token before the
+// first key) with the last `window` ones in sight, 0: all.
+QB_HD int kv_first_seen(int pos, int window) { return window == 0 || pos < window ? 0 : pos - window + 1; }
+
 }  // namespace qb

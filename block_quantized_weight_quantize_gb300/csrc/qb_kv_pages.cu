@@ -14,7 +14,6 @@
 #include <cstdint>
 
 #include "qb_kv4.cuh"
-#include "qb_kv_index.h"
 
 namespace qb {
 

@@ -175,3 +175,16 @@ def test_finite_keys_and_values_that_a_token_does_not_see(name, nh, nkv, d, page
     not_seen = torch.from_numpy(~seen).cuda()
     assert (~seen).any() and seen.any() == (T > 1)
     assert torch.equal(out[not_seen], clean[not_seen]) and torch.equal(lse[not_seen], clean_lse[not_seen])
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lens,news", [([3, 1, 40], [8, 5, 2]), ([3, 300, 0], [200, 150, 100])])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30])
+def test_a_window_as_wide_as_any(name, lens, news, window):
+    """A window past every length, beside tokens before the first key, is no window (few tokens and many)."""
+    import torch
+    b = Batch(91, lens, news, 2, 1, 64, 16, name)
+    want, wlse = b.run(0.125)
+    out, lse = b.run(0.125, window)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    b.check(window=window)

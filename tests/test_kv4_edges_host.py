@@ -20,6 +20,7 @@ def index(tmp_path_factory):
     d = tmp_path_factory.mktemp("index")
     (d / "i.cpp").write_text("""#include "qb_kv_index.h"
 extern "C" long long room(long long c, long long first, long long n) { return qb::kv_slots_room(c, first, n); }
+extern "C" int first_seen(int pos, int window) { return qb::kv_first_seen(pos, window); }
 """)
     subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", str(CSRC), str(d / "i.cpp"),
                     "-o", str(d / "i.so")], check=True)
@@ -44,3 +45,10 @@ def test_writers_of_a_key_cache_let_no_kernel_start_early(file, kernel):
     text = (CSRC / file).read_text()
     body = re.search(r"__global__[^;{]*\b%s\(.*?\n}\n" % kernel, text, re.S).group(0)
     assert "pdl_wait();" in body and "pdl_launch_dependents();" not in body
+
+
+@pytest.mark.parametrize("window", [0, 1, 2, 50, TOP - 18, TOP - 17, TOP - 1])
+def test_first_key_seen(index, window):
+    """Places from 2^24 tokens before the first key up to the last key of the longest table row."""
+    for pos in (-(1 << 24), -5, -1, 0, 1, 48, 49, 50, 51, TOP - 19, TOP - 18, TOP - 17):
+        assert index.first_seen(pos, window) == (max(0, pos - window + 1) if window else 0)
