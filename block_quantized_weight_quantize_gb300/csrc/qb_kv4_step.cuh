@@ -151,7 +151,7 @@ template <int U>
 __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0, int &nu) {
     const int first = kv_first_seen(q.len - q.T, window);
     u0 = first / U;
-    nu = max(1, (q.len + U - 1) / U - u0);
+    nu = max(1, kv_parts(q.len, U) - u0);
 }
 
 // A place in the call's work: sequence, key head, row tile, unit of the key axis.
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
-            if (k0 > pos_hi || k0 + U <= first_lo)
+            if (k0 > pos_hi || k0 <= first_lo - U)
                 ;  // no row sees it: the sequence's other row tiles do
             else if (k0 + U - 1 > pos_lo || k0 < first_hi)
                 unit(ub, k0, std::true_type());

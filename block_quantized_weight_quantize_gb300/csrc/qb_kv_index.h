@@ -23,4 +23,7 @@ QB_HD int64_t kv_slots_room(int64_t count, int64_t first, int64_t nslots) {
 // first key) with the last `window` ones in sight, 0: all.
 QB_HD int kv_first_seen(int pos, int window) { return window == 0 || pos < window ? 0 : pos - window + 1; }
 
+// Parts of `size` keys that hold `len` (up to 2^31 - 1).
+QB_HD int kv_parts(int len, int size) { return len / size + (len % size != 0); }
+
 }  // namespace qb

@@ -188,3 +188,60 @@ def test_a_window_as_wide_as_any(name, lens, news, window):
     out, lse = b.run(0.125, window)
     assert torch.equal(out, want) and torch.equal(lse, wlse)
     b.check(window=window)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5])
+def test_the_longest_sequence(name, T):
+    """2^31 - 16 keys of one sequence, all in one page but the last 16.  Scores are 0 and values eighths from -7 to 8, so that the sums are
+    exact in f32 while a warp's keys, times eight, are fewer than 2^24; the warps' and blocks' sums are joined in f32, at most
+    12 + 152 roundings of 2^-24.  Then the last page's keys are 30 nats above the others: they make up the output but for
+    2^31 / (16 e^30) = 1.3e-5 of values of at most 1.  Then a window over the last 40 keys."""
+    import torch
+    page, d, n = 16, 64, 2 ** 31 - 16
+    pool = torch.zeros((2, qb.kv4_block_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    cache = qb.Kv4(pool, page, 1, d)
+    rng = np.random.default_rng(93)
+    v = rng.integers(-7, 8, (32, 1, d)) / 8
+    v[:, :, ::32] = 1.0      # a group's extreme: the step is -1/8
+    vt = torch.from_numpy(v.astype(np.float32)).cuda()
+
+    def fill(k):
+        kt = torch.from_numpy(np.broadcast_to(k, (32, 1, d)).astype(np.float32)).cuda().contiguous()
+        qb.kv4_append(cache, kt, vt, _i32(np.arange(32)))
+        back = torch.empty_like(vt)
+        qb.kv4_read(cache, _i32(np.arange(32)), torch.empty_like(kt), back)
+        assert torch.equal(back, vt)
+
+    tables = torch.zeros((1, n // page), dtype=torch.int32, device="cuda")
+    tables[0, -1] = 1
+    seqs = qb.KvSeqs(tables, _i32([n]), q_start=_i32([0, T]))
+    q = torch.ones((T, 1, d), dtype={"f32": torch.float32, "bf16": torch.bfloat16}[name], device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((T, 1), device="cuda")
+    rounding = 164 * 2.0 ** -24 + OUT[name]
+    fill(0.0)
+    qb.kv4_attn(cache, q, seqs, 1.0, out, lse=lse)
+    got = out.double().cpu().numpy()[:, 0]
+    for j in range(T):
+        keys = n - T + 1 + j
+        want = (v[:16, 0].sum(0) * (n // page - 1) + v[16:32 - T + 1 + j, 0].sum(0)) / keys
+        assert np.all(np.abs(got[j] - want) <= rounding)
+        assert abs(float(lse[j]) - np.log(keys)) <= SUM * (1 + np.log(keys))
+    k = np.zeros((32, 1, d))
+    k[16:] = 30.0 / d
+    fill(k)
+    if T == 1:
+        kb = torch.empty_like(vt)
+        qb.kv4_read(cache, _i32(np.arange(32)), kb, torch.empty_like(vt))
+        gap = float(kb[16].double().sum())
+        qb.kv4_attn(cache, q, seqs, 1.0, out, lse=lse)
+        assert np.all(np.abs(out.double().cpu().numpy()[0, 0] - v[16:, 0].mean(0)) <= 2 * (n - 16) / (16 * np.exp(gap)) + rounding + 2 * gap * SUM)
+        assert abs(float(lse[0]) - (gap + np.log(16))) <= (n - 16) / (16 * np.exp(gap)) + SUM * (2 + gap) * 2
+    fill(0.0)
+    qb.kv4_attn(cache, q, seqs, 1.0, out, lse=lse, window=40)
+    got = out.double().cpu().numpy()[:, 0]
+    for j in range(T):
+        places = np.arange(n - T + j - 39, n - T + j + 1, dtype=np.int64)
+        rows = np.where(places >= n - 16, 16 + places % 16, places % 16)
+        assert np.all(np.abs(got[j] - v[rows, 0].mean(0)) <= rounding)
+        assert abs(float(lse[j]) - np.log(40)) <= SUM * 5

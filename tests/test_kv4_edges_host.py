@@ -20,6 +20,7 @@ def index(tmp_path_factory):
     d = tmp_path_factory.mktemp("index")
     (d / "i.cpp").write_text("""#include "qb_kv_index.h"
 extern "C" long long room(long long c, long long first, long long n) { return qb::kv_slots_room(c, first, n); }
+extern "C" int parts(int len, int size) { return qb::kv_parts(len, size); }
 extern "C" int first_seen(int pos, int window) { return qb::kv_first_seen(pos, window); }
 """)
     subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", str(CSRC), str(d / "i.cpp"),
@@ -52,3 +53,8 @@ def test_first_key_seen(index, window):
     """Places from 2^24 tokens before the first key up to the last key of the longest table row."""
     for pos in (-(1 << 24), -5, -1, 0, 1, 48, 49, 50, 51, TOP - 19, TOP - 18, TOP - 17):
         assert index.first_seen(pos, window) == (max(0, pos - window + 1) if window else 0)
+
+
+def test_parts_of_a_length(index):
+    for n in (0, 1, 31, 32, 33, 64, TOP - 64, TOP - 33, TOP - 32, TOP - 31, TOP - 16, TOP - 1):
+        assert index.parts(n, 32) == -(-n // 32)
