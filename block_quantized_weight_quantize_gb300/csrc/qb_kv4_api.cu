@@ -29,8 +29,9 @@ bool type_ok(qb_type t) { return t == QB_T_F32 || t == QB_T_F16 || t == QB_T_BF1
 
 int check_rows(const qb_kv4 *c, qb_type type, const void *k, int64_t ks, const void *v, int64_t vs,
                const int32_t *slots, int64_t n) {
-    if (check_cache(c) || !type_ok(type) || !slots || off(slots, 4) || n < 0 || n >= (int64_t(1) << 31))
-        return QB_E_ARG;
+    if (check_cache(c) || !type_ok(type) || n < 0 || n >= (int64_t(1) << 31)) return QB_E_ARG;
+    if (n == 0) return QB_OK;  // empty arrays may have no address
+    if (!slots || off(slots, 4)) return QB_E_ARG;
     const int64_t width = (int64_t)c->nkv * c->d;
     const int es = type_bytes(type);
     if (rows_bad(k, ks, width, es) || rows_bad(v, vs, width, es)) return QB_E_ARG;
@@ -91,7 +92,7 @@ int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const vo
     if (!seqs->tables || !seqs->lens || off(seqs->tables, 4) || off(seqs->lens, 4) || off(seqs->rows, 4) ||
         off(seqs->q_start, 4))
         return QB_E_ARG;
-    if (seqs->nseq < 1 || seqs->nseq > 8192 || seqs->nrows < 1 || seqs->maxp < 1 ||
+    if (seqs->nseq < 0 || seqs->nseq > 8192 || (seqs->nseq == 0 && ntok != 0) || seqs->nrows < 1 || seqs->maxp < 1 ||
         (int64_t)seqs->maxp * cache->page >= (int64_t(1) << 31))
         return QB_E_ARG;
     if (!seqs->rows && seqs->nseq > seqs->nrows) return QB_E_ARG;
@@ -99,13 +100,13 @@ int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const vo
         ntok * nh > (int64_t(1) << 30))
         return QB_E_ARG;
     if (!seqs->q_start && ntok != seqs->nseq) return QB_E_ARG;
+    if (ntok == 0) return QB_OK;
     const int64_t width = (int64_t)nh * cache->d;
     const int es = type_bytes(type);
     if (rows_bad(q, q_stride, width, es) || rows_bad(out, out_stride, width, es) || off(lse, 4)) return QB_E_ARG;
     const int64_t need = kv4_attn_workspace_bytes(cache, nh);
     if (need < 0) return (int)need;
     if (!workspace || off(workspace, 16) || (int64_t)workspace_bytes < need) return QB_E_ARG;
-    if (ntok == 0) return QB_OK;
     Kv4AttnArgs a = {};
     a.c = kv4_view(*cache);
     a.s = *seqs;
@@ -138,10 +139,11 @@ int kv_pages_reset(const qb_kv_pages *pages, void *stream) {
 int kv_pages_extend(const qb_kv_pages *pages, const int32_t *rows, const int32_t *counts, int n, int32_t *slots,
                     int64_t nslots, int32_t *status, void *stream) {
     if (const int rc = check_pages(pages)) return rc;
-    if (!rows || !counts || !slots || !status || n < 0 || n > pages->nrows || nslots < 0 || off(rows, 4) ||
-        off(counts, 4) || off(slots, 4) || off(status, 4))
-        return QB_E_ARG;
+    if (n < 0 || n > pages->nrows || nslots < 0) return QB_E_ARG;
     if (n == 0) return QB_OK;
+    if (!rows || !counts || (!slots && nslots > 0) || !status || off(rows, 4) || off(counts, 4) || off(slots, 4) ||
+        off(status, 4))
+        return QB_E_ARG;
     return launch_kv_pages_extend(*pages, rows, counts, n, slots, nslots, status, static_cast<cudaStream_t>(stream));
 }
 
@@ -149,20 +151,20 @@ int kv_pages_fork(const qb_kv_pages *pages, void *data, int nlayers, int64_t pag
                   const int32_t *children, int n, int32_t *status, void *workspace, size_t workspace_bytes,
                   void *stream) {
     if (const int rc = check_pages(pages)) return rc;
-    if (data_bad(data, nlayers, page_bytes) || !parents || !children || !status || n < 0 || n > pages->nrows ||
-        off(parents, 4) || off(children, 4) || off(status, 4))
-        return QB_E_ARG;
+    if (data_bad(data, nlayers, page_bytes) || n < 0 || n > pages->nrows) return QB_E_ARG;
+    if (n == 0) return QB_OK;
+    if (!parents || !children || !status || off(parents, 4) || off(children, 4) || off(status, 4)) return QB_E_ARG;
     if (!workspace || off(workspace, 16) || (int64_t)workspace_bytes < kv_pages_ws(pages->npages, pages->nrows))
         return QB_E_ARG;
-    if (n == 0) return QB_OK;
     return launch_kv_pages_fork(*pages, data, nlayers, page_bytes, parents, children, n, status, workspace,
                                 static_cast<cudaStream_t>(stream));
 }
 
 int kv_pages_free(const qb_kv_pages *pages, const int32_t *rows, int n, void *stream) {
     if (const int rc = check_pages(pages)) return rc;
-    if (!rows || off(rows, 4) || n < 0 || n > pages->nrows) return QB_E_ARG;
+    if (n < 0 || n > pages->nrows) return QB_E_ARG;
     if (n == 0) return QB_OK;
+    if (!rows || off(rows, 4)) return QB_E_ARG;
     return launch_kv_pages_free(*pages, rows, n, static_cast<cudaStream_t>(stream));
 }
 
@@ -177,10 +179,9 @@ int kv_pages_compact(const qb_kv_pages *pages, void *data, int nlayers, int64_t 
 
 int kv_pages_copy(void *data, int nlayers, int64_t npages, int64_t page_bytes, const int32_t *src, const int32_t *dst,
                   int n, void *stream) {
-    if (data_bad(data, nlayers, page_bytes) || npages < 1 || npages > (1 << 20) || !src || !dst || off(src, 4) ||
-        off(dst, 4) || n < 0 || n > npages)
-        return QB_E_ARG;
+    if (data_bad(data, nlayers, page_bytes) || npages < 1 || npages > (1 << 20) || n < 0 || n > npages) return QB_E_ARG;
     if (n == 0) return QB_OK;
+    if (!src || !dst || off(src, 4) || off(dst, 4)) return QB_E_ARG;
     return launch_kv_pages_copy(data, nlayers, npages, page_bytes, src, dst, n, static_cast<cudaStream_t>(stream));
 }
 

@@ -429,7 +429,10 @@ QB_API int q_matvec_host(int scaling, qb_fmt fmt, const void *W, int64_t rows, i
  *     keys:    N = (((p*page + r)*4 + e/8)*w + g)*8 + e%8
  *     values:  N = (((p*page + r)*8 + (e/4 ^ 4*(r>>1 & 1)))*w + g)*4 + e%4
  * so that a thread of a tensor-core fragment finds its share of a row in one
- * wide load, and the shares of neighbouring rows in different banks. */
+ * wide load, and the shares of neighbouring rows in different banks.
+ *
+ * Here and in the page calls below, a call of no rows, tokens, sequences or
+ * pairs (n or ntok 0) does nothing, and its per-row arrays may be NULL. */
 
 /* Element types of the rows, queries and outputs of the calls below. */
 typedef enum { QB_T_F32 = 0, QB_T_F16 = 1, QB_T_BF16 = 2 } qb_type;
@@ -468,7 +471,7 @@ QB_API int kv4_read(const qb_kv4 *cache, qb_type type, const int32_t *slots, int
  * key i of it is row i % page of page tables[..][i / page].  Its new tokens
  * are q_start[s] .. q_start[s+1]-1 of the call's (q_start NULL: the one token
  * s), the last ones of its lens[R] tokens, already in the cache.
- * 1 <= nseq <= 8192. */
+ * 0 <= nseq <= 8192, 0 with no tokens only. */
 typedef struct {
     const int32_t *tables;
     const int32_t *lens;
@@ -543,7 +546,7 @@ QB_API int kv_pages_reset(const qb_kv_pages *pages, void *stream);
  * `slots`, request after request.  A request that the pages left by those
  * before it (refused ones counted as served) or its table row cannot hold is refused whole:
  * its slots are -1.  status[i]: QB_OK, QB_E_PAGES or QB_E_ARG.  slots has room
- * for `nslots` entries; those past it are dropped and reported. */
+ * for `nslots` entries (NULL: none); those past it are dropped and reported. */
 QB_API int kv_pages_extend(const qb_kv_pages *pages, const int32_t *rows, const int32_t *counts, int n,
                            int32_t *slots, int64_t nslots, int32_t *status, void *stream);
 

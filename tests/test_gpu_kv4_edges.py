@@ -245,3 +245,29 @@ def test_the_longest_sequence(name, T):
         rows = np.where(places >= n - 16, 16 + places % 16, places % 16)
         assert np.all(np.abs(got[j] - v[rows, 0].mean(0)) <= rounding)
         assert abs(float(lse[j]) - np.log(40)) <= SUM * 5
+
+
+def test_calls_without_rows():
+    """Every call through the binding with empty tensors: nothing changes, nothing is refused."""
+    import torch
+    b = Batch(95, [20, 0], [0, 0], 4, 2, 64, 16, "f32")
+    page, npages, nrows, maxp = 16, b.pool.shape[0], 3, 4
+    state = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, npages, npages, nrows, (nrows, maxp))]
+    pages = qb.KvPages(page, *state)
+    qb.kv_pages_reset(pages)
+    before = [x.clone() for x in (*state, b.pool)]
+    no, rows, q = _i32([]), torch.empty((0, 2, 64), device="cuda"), torch.empty((0, 4, 64), device="cuda")
+    qb.kv4_append(b.cache, rows, rows, no)
+    qb.kv4_read(b.cache, no, rows, rows)
+    tables, lens = _i32(b.tables), _i32(b.lens)
+    for seqs in (qb.KvSeqs(tables, lens, q_start=_i32([0, 0, 0])), qb.KvSeqs(tables, lens, rows=no), qb.KvSeqs(tables, lens, rows=no, q_start=_i32([0]))):
+        qb.kv4_attn(b.cache, q, seqs, 0.125, torch.empty_like(q), lse=torch.empty((0, 4), device="cuda"))
+    qb.kv_pages_extend(pages, no, no, no, no)
+    status = _i32([5, 5])
+    qb.kv_pages_extend(pages, _i32([0, 2]), _i32([0, 0]), no, status)
+    assert status.tolist() == [0, 0]
+    qb.kv_pages_fork(pages, b.pool, no, no, no)
+    qb.kv_pages_free(pages, no)
+    qb.kv_pages_copy(b.pool, npages, no, no)
+    assert all(torch.equal(x, y) for x, y in zip((*state, b.pool), before))
+    assert qb.q_device_status() == qb.QB_OK

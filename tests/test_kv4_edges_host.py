@@ -8,6 +8,10 @@ import subprocess
 
 import pytest
 
+import block_quantized_weight_quantize_gb300 as qb
+from block_quantized_weight_quantize_gb300 import kv4
+from test_kv4_host import A, _cache, _pages, _seqs
+
 CSRC = pathlib.Path(__file__).resolve().parent.parent / "block_quantized_weight_quantize_gb300" / "csrc"
 TOP = 2 ** 31
 
@@ -58,3 +62,29 @@ def test_first_key_seen(index, window):
 def test_parts_of_a_length(index):
     for n in (0, 1, 31, 32, 33, 64, TOP - 64, TOP - 33, TOP - 32, TOP - 31, TOP - 16, TOP - 1):
         assert index.parts(n, 32) == -(-n // 32)
+
+
+def test_calls_without_rows_take_arrays_without_an_address():
+    """An empty tensor's address is NULL.  Nothing else about the call may be wrong."""
+    c, p, s, f = _cache(), _pages(), _seqs(q_start=A), kv4._c
+    ca, pa, sa = (ctypes.addressof(x) for x in (c, p, s))
+    assert f.kv4_append(ca, 0, None, 128, None, 128, None, 0, None) == qb.QB_OK
+    assert f.kv4_read(ca, 0, None, 0, None, 128, None, 128, None) == qb.QB_OK
+    assert f.kv4_attn(ca, sa, 0, None, 256, 0, 4, 1.0, 0, None, 256, None, None, 0, None) == qb.QB_OK
+    none = _seqs(nseq=0)
+    na = ctypes.addressof(none)
+    assert f.kv4_attn(ca, na, 0, None, 256, 0, 4, 1.0, 0, None, 256, None, None, 0, None) == qb.QB_OK
+    assert f.kv_pages_extend(pa, None, None, 0, None, 0, None, None) == qb.QB_OK
+    assert f.kv_pages_fork(pa, A, 1, 64, None, None, 0, None, None, 0, None) == qb.QB_OK
+    assert f.kv_pages_free(pa, None, 0, None) == qb.QB_OK
+    assert f.kv_pages_copy(A, 1, 8, 64, None, None, 0, None) == qb.QB_OK
+    # tokens without a sequence, and what is wrong without rows too
+    none.q_start = A
+    assert f.kv4_attn(ca, na, 0, A, 256, 3, 4, 1.0, 0, A, 256, None, A, 1 << 30, None) == qb.QB_E_ARG
+    assert f.kv4_append(ca, 7, None, 128, None, 128, None, 0, None) == qb.QB_E_ARG
+    assert f.kv4_attn(ca, sa, 0, None, 256, 0, 3, 1.0, 0, None, 256, None, None, 0, None) == qb.QB_E_ARG
+    assert f.kv_pages_fork(pa, None, 1, 64, None, None, 0, None, None, 0, None) == qb.QB_E_ARG
+    # slots without an address only where there are none
+    assert f.kv_pages_extend(pa, A, A, 1, None, 5, A, None) == qb.QB_E_ARG
+    bad = _cache(page=24)
+    assert f.kv4_append(ctypes.addressof(bad), 0, None, 128, None, 128, None, 0, None) == qb.QB_E_ARG
