@@ -70,11 +70,13 @@ def _stream(stream, t) -> int:
 
 
 def _workspace(nbytes: int, like, stream):
-    """A workspace for one call on `stream` (None: the current one) of the device of `like`."""
-    w = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:  # its memory is given out again only when that stream has passed the call
-        w.record_stream(stream)
-    return w
+    """A workspace for one call on `stream` (None: the current one) of the device of `like`.  It is that stream's memory from the
+    start: a block that the current stream has given back may still be in use by what is queued there, and one of this
+    stream's is given out again only to calls that follow on it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
 def _bytes(n: int, where: str) -> int:

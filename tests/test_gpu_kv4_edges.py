@@ -271,3 +271,51 @@ def test_calls_without_rows():
     qb.kv_pages_copy(b.pool, npages, no, no)
     assert all(torch.equal(x, y) for x, y in zip((*state, b.pool), before))
     assert qb.q_device_status() == qb.QB_OK
+
+
+@pytest.mark.parametrize("what", ["attn", "fork", "compact"])
+def test_a_workspace_for_another_stream_is_not_memory_still_in_use_here(what, monkeypatch):
+    """A block given back on the current stream, whose queued work still writes it, is not the workspace of a call on another stream."""
+    import torch
+    from block_quantized_weight_quantize_gb300 import kv4
+    b = Batch(97, [40, 0], [1, 0], 4, 2, 64, 16, "f32")
+    npages = b.pool.shape[0]
+    state = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, npages, npages, 2, (2, 4))]
+    pages = qb.KvPages(16, *state)
+    qb.kv_pages_reset(pages)
+    seqs = qb.KvSeqs(_i32(b.tables), _i32(b.lens), q_start=_i32(b.q_start))
+    out, status, zero, one = torch.empty_like(b.q), _i32([5]), _i32([0]), _i32([1])
+    side = torch.cuda.Stream()
+    size = qb.kv4_attn_workspace_bytes(b.cache, b.q) if what == "attn" else qb.kv_pages_workspace_bytes(pages)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    block = torch.empty(size, dtype=torch.uint8, device="cuda")
+    where = block.data_ptr()
+    torch.cuda._sleep(50_000_000)
+    block.fill_(1)
+    del block
+    made, empty = [], torch.empty
+
+    def note(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    with monkeypatch.context() as mp:
+        mp.setattr(kv4.torch, "empty", note)
+        if what == "attn":
+            kv4.kv4_attn(b.cache, b.q, seqs, 0.125, out, stream=side)
+        elif what == "fork":
+            kv4.kv_pages_fork(pages, b.pool, zero, one, status, stream=side)
+        else:
+            kv4.kv_pages_compact(pages, b.pool, stream=side)
+    assert len(made) == 1 and made[0].numel() == size and made[0].data_ptr() != where
+    # and it is that stream's: given back, it goes to the next call there and to none here
+    mine = made.pop().data_ptr()
+    assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != mine
+    with torch.cuda.stream(side):
+        again = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == mine
+    torch.cuda.synchronize()
+    if what == "attn":
+        want, _ = b.run(0.125)
+        assert torch.equal(out, want)
