@@ -5,7 +5,8 @@ A cache, its sequences and its pages are small handles made once; each call
 marshals pointers and raises on a non-zero status.  Tensors keep the layouts
 of the header: caches uint8 [npages, nkv * kv4_block_bytes(page, d)], rows
 [n, nkv, d] and queries [ntok, nh, d] of float32, float16 or bfloat16 (the last
-two axes contiguous), int32 for everything that counts pages or tokens.
+two axes contiguous), int32 for everything that counts pages or tokens.  The
+tensors of a call lie on one device, the current one, where the library launches.
 """
 from __future__ import annotations
 
@@ -61,12 +62,14 @@ class _Calls:
 
 
 _c = _Calls()
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _stream(stream, t) -> int:
-    """Handle of `stream`, or of the current stream of t's device."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+def _stream(stream, dev: int) -> int:
+    """Handle of `stream`, or of the current one, for a call whose tensors lie on device `dev`."""
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _workspace(nbytes: int, like, stream):
@@ -85,10 +88,20 @@ def _bytes(n: int, where: str) -> int:
     return int(n)
 
 
-def _dev(t, dtype=None, what="tensor"):
-    """Device address of a contiguous CUDA tensor of `dtype`."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: device memory expected, got a CPU tensor")
+def _on(t, what: str, dev=None) -> int:
+    """The device that t lies on: `dev`, where that is given."""
+    d = t.get_device()
+    if d != dev:
+        if d < 0:
+            raise ValueError(f"{what}: device memory expected, got a CPU tensor")
+        if dev is not None:
+            raise ValueError(f"{what}: on cuda:{d}, where the call's other tensors are on cuda:{dev}")
+    return d
+
+
+def _dev(t, dtype, what: str, dev: int):
+    """Address of a contiguous tensor of `dtype` on device `dev`."""
+    _on(t, what, dev)
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
     if not t.is_contiguous():
@@ -96,10 +109,9 @@ def _dev(t, dtype=None, what="tensor"):
     return t.data_ptr()
 
 
-def _rows(t, heads: int, d: int, what: str):
-    """Address and token stride of [n, heads, d] rows whose last two axes are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: device memory expected, got a CPU tensor")
+def _rows(t, heads: int, d: int, what: str, dev: int):
+    """Address and token stride of [n, heads, d] rows on device `dev` whose last two axes are contiguous."""
+    _on(t, what, dev)
     n, h, e = t.shape if t.dim() == 3 else (0, 0, 0)
     if h != heads or e != d:
         raise ValueError(f"{what}: [n, {heads}, {d}] expected, got {tuple(t.shape)}")
@@ -117,14 +129,15 @@ def kv4_block_bytes(page: int, d: int) -> int:
 class Kv4:
     """One layer's cache: data uint8 [npages, nkv * kv4_block_bytes(page, d)] (16-byte aligned device memory)."""
 
-    __slots__ = ("data", "page", "nkv", "d", "c", "ref")
+    __slots__ = ("data", "page", "nkv", "d", "dev", "c", "ref")
 
     def __init__(self, data, page: int, nkv: int, d: int):
         per = nkv * kv4_block_bytes(page, d)
         if data.dtype is not torch.uint8 or data.numel() % per:
             raise ValueError(f"data: uint8 pages of {per} bytes expected")
         self.data, self.page, self.nkv, self.d = data, page, nkv, d
-        self.c = _CKv4(_dev(data, what="data"), data.numel() // per, page, nkv, d)
+        self.dev = _on(data, "data")
+        self.c = _CKv4(_dev(data, None, "data", self.dev), data.numel() // per, page, nkv, d)
         self.ref = ctypes.addressof(self.c)
 
 
@@ -132,7 +145,7 @@ class KvSeqs:
     """The sequences of a call: tables int32 [nrows, maxp], lens int32 [nrows]; rows int32 [nseq] chooses and orders them
     (None: all, in order), q_start int32 [nseq + 1] bounds each one's new tokens (None: one token each)."""
 
-    __slots__ = ("tables", "lens", "rows", "q_start", "c", "ref")
+    __slots__ = ("tables", "lens", "rows", "q_start", "dev", "c", "ref")
 
     def __init__(self, tables, lens, rows=None, q_start=None):
         i32 = torch.int32
@@ -143,9 +156,10 @@ class KvSeqs:
         if q_start is not None and q_start.numel() != nseq + 1:
             raise ValueError("q_start: nseq + 1 entries expected")
         self.tables, self.lens, self.rows, self.q_start = tables, lens, rows, q_start
-        self.c = _CSeqs(_dev(tables, i32, "tables"), _dev(lens, i32, "lens"),
-                        None if rows is None else _dev(rows, i32, "rows"),
-                        None if q_start is None else _dev(q_start, i32, "q_start"), nrows, maxp, nseq)
+        self.dev = dev = _on(tables, "tables")
+        self.c = _CSeqs(_dev(tables, i32, "tables", dev), _dev(lens, i32, "lens", dev),
+                        None if rows is None else _dev(rows, i32, "rows", dev),
+                        None if q_start is None else _dev(q_start, i32, "q_start", dev), nrows, maxp, nseq)
         self.ref = ctypes.addressof(self.c)
 
 
@@ -153,7 +167,7 @@ class KvPages:
     """The state of a pool's pages, all int32 device tensors: nfree [1], free [npages], refs [npages], lens [nrows],
     tables [nrows, maxp]."""
 
-    __slots__ = ("page", "nfree", "free", "refs", "lens", "tables", "c", "ref")
+    __slots__ = ("page", "nfree", "free", "refs", "lens", "tables", "dev", "c", "ref")
 
     def __init__(self, page: int, nfree, free, refs, lens, tables):
         i32 = torch.int32
@@ -162,8 +176,9 @@ class KvPages:
         if free.numel() != npages or lens.numel() != nrows or nfree.numel() != 1:
             raise ValueError("nfree [1], free and refs [npages], lens [nrows], tables [nrows, maxp] expected")
         self.page, self.nfree, self.free, self.refs, self.lens, self.tables = page, nfree, free, refs, lens, tables
-        self.c = _CPages(_dev(nfree, i32, "nfree"), _dev(free, i32, "free"), _dev(refs, i32, "refs"),
-                         _dev(lens, i32, "lens"), _dev(tables, i32, "tables"), page, npages, nrows, maxp)
+        self.dev = dev = _on(refs, "refs")
+        self.c = _CPages(_dev(nfree, i32, "nfree", dev), _dev(free, i32, "free", dev), _dev(refs, i32, "refs", dev),
+                         _dev(lens, i32, "lens", dev), _dev(tables, i32, "tables", dev), page, npages, nrows, maxp)
         self.ref = ctypes.addressof(self.c)
 
 
@@ -171,22 +186,24 @@ class KvPages:
 
 def kv4_append(cache: Kv4, k, v, slots, stream=None) -> None:
     """Writes the rows k, v [n, nkv, d] into the cache at slots int32 [n] (page * cache.page + place; below zero: passed over)."""
-    kp, ks = _rows(k, cache.nkv, cache.d, "k")
-    vp, vs = _rows(v, cache.nkv, cache.d, "v")
+    dev = cache.dev
+    kp, ks = _rows(k, cache.nkv, cache.d, "k", dev)
+    vp, vs = _rows(v, cache.nkv, cache.d, "v", dev)
     if k.dtype is not v.dtype or k.dtype not in _TYPE or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
         raise ValueError("k, v: float32, float16 or bfloat16 rows of one type, one slot each, expected")
-    _check(_c.kv4_append(cache.ref, _TYPE[k.dtype], kp, ks, vp, vs, _dev(slots, torch.int32, "slots"), k.shape[0],
-                         _stream(stream, k)), "kv4_append")
+    _check(_c.kv4_append(cache.ref, _TYPE[k.dtype], kp, ks, vp, vs, _dev(slots, torch.int32, "slots", dev), k.shape[0],
+                         _stream(stream, dev)), "kv4_append")
 
 
 def kv4_read(cache: Kv4, slots, k, v, stream=None) -> None:
     """Reads the rows at slots int32 [n] back into k, v [n, nkv, d] (any of the three types)."""
-    kp, ks = _rows(k, cache.nkv, cache.d, "k")
-    vp, vs = _rows(v, cache.nkv, cache.d, "v")
+    dev = cache.dev
+    kp, ks = _rows(k, cache.nkv, cache.d, "k", dev)
+    vp, vs = _rows(v, cache.nkv, cache.d, "v", dev)
     if k.dtype is not v.dtype or k.dtype not in _TYPE or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
         raise ValueError("k, v: float32, float16 or bfloat16 rows of one type, one slot each, expected")
-    _check(_c.kv4_read(cache.ref, _TYPE[k.dtype], _dev(slots, torch.int32, "slots"), k.shape[0], kp, ks, vp, vs,
-                       _stream(stream, k)), "kv4_read")
+    _check(_c.kv4_read(cache.ref, _TYPE[k.dtype], _dev(slots, torch.int32, "slots", dev), k.shape[0], kp, ks, vp, vs,
+                       _stream(stream, dev)), "kv4_read")
 
 
 def kv4_attn_workspace_bytes(cache: Kv4, q, seqs: KvSeqs = None) -> int:
@@ -198,31 +215,33 @@ def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: i
              stream=None) -> None:
     """Causal attention of the new tokens q [ntok, nh, d] over the cache: out like q, lse f32 [ntok, nh] (optional);
     window > 0: only the last `window` keys.  workspace: uint8, kv4_attn_workspace_bytes long (allocated here when None)."""
-    nh = q.shape[1]
-    qp, qs = _rows(q, nh, cache.d, "q")
-    op, os_ = _rows(out, nh, cache.d, "out")
+    nh, dev = q.shape[1], cache.dev
+    if seqs.dev != dev:
+        raise ValueError(f"seqs: on cuda:{seqs.dev}, where the cache is on cuda:{dev}")
+    qp, qs = _rows(q, nh, cache.d, "q", dev)
+    op, os_ = _rows(out, nh, cache.d, "out", dev)
     if q.dtype is not out.dtype or q.dtype not in _TYPE or q.shape[0] != out.shape[0]:
         raise ValueError("q, out: one shape and one of float32, float16, bfloat16 expected")
     lp = None
     if lse is not None:
-        lp = _dev(lse, torch.float32, "lse")
+        lp = _dev(lse, torch.float32, "lse", dev)
         if lse.numel() != q.shape[0] * nh:
             raise ValueError("lse: [ntok, nh] expected")
     if workspace is None:
         workspace = _workspace(kv4_attn_workspace_bytes(cache, q), q, stream)
     _check(_c.kv4_attn(cache.ref, seqs.ref, _TYPE[q.dtype], qp, qs, q.shape[0], nh, scale, window, op, os_, lp,
-                       _dev(workspace, what="workspace"), workspace.numel() * workspace.element_size(),
-                       _stream(stream, q)), "kv4_attn")
+                       _dev(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
+                       _stream(stream, dev)), "kv4_attn")
 
 
 # ------------------------------------------------------------------ pages
 
-def _pool(data, npages: int):
+def _pool(data, npages: int, dev: int):
     """Address, layers and page bytes of a pool [layers, npages, ...] (or [npages, ...]: one layer) of any type."""
     layers = data.shape[0] if data.dim() > 2 else 1
     if (data.shape[1] if data.dim() > 2 else data.shape[0]) != npages:
         raise ValueError(f"data: [layers, {npages}, page] expected, got {tuple(data.shape)}")
-    return _dev(data, what="data"), layers, data.numel() * data.element_size() // (layers * npages)
+    return _dev(data, None, "data", dev), layers, data.numel() * data.element_size() // (layers * npages)
 
 
 def kv_pages_workspace_bytes(pages: KvPages) -> int:
@@ -238,7 +257,7 @@ def _page_ws(pages, workspace, stream):
 
 def kv_pages_reset(pages: KvPages, stream=None) -> None:
     """Every page free, every sequence empty."""
-    _check(_c.kv_pages_reset(pages.ref, _stream(stream, pages.refs)), "kv_pages_reset")
+    _check(_c.kv_pages_reset(pages.ref, _stream(stream, pages.dev)), "kv_pages_reset")
 
 
 def kv_pages_extend(pages: KvPages, rows, counts, slots, status, stream=None) -> None:
@@ -247,9 +266,9 @@ def kv_pages_extend(pages: KvPages, rows, counts, slots, status, stream=None) ->
     i32, n = torch.int32, rows.numel()
     if counts.numel() != n or status.numel() < n:
         raise ValueError("counts, status: one entry a row expected")
-    _check(_c.kv_pages_extend(pages.ref, _dev(rows, i32, "rows"), _dev(counts, i32, "counts"), n,
-                              _dev(slots, i32, "slots"), slots.numel(), _dev(status, i32, "status"),
-                              _stream(stream, pages.refs)), "kv_pages_extend")
+    _check(_c.kv_pages_extend(pages.ref, _dev(rows, i32, "rows", pages.dev), _dev(counts, i32, "counts", pages.dev), n,
+                              _dev(slots, i32, "slots", pages.dev), slots.numel(), _dev(status, i32, "status", pages.dev),
+                              _stream(stream, pages.dev)), "kv_pages_extend")
 
 
 def kv_pages_fork(pages: KvPages, data, parents, children, status, workspace=None, stream=None) -> None:
@@ -258,24 +277,24 @@ def kv_pages_fork(pages: KvPages, data, parents, children, status, workspace=Non
     i32, n = torch.int32, parents.numel()
     if children.numel() != n or status.numel() < n:
         raise ValueError("children, status: one entry a parent expected")
-    dp, layers, pb = _pool(data, pages.c.npages)
+    dp, layers, pb = _pool(data, pages.c.npages, pages.dev)
     ws, wb = _page_ws(pages, workspace, stream)
-    _check(_c.kv_pages_fork(pages.ref, dp, layers, pb, _dev(parents, i32, "parents"), _dev(children, i32, "children"),
-                            n, _dev(status, i32, "status"), _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
+    _check(_c.kv_pages_fork(pages.ref, dp, layers, pb, _dev(parents, i32, "parents", pages.dev), _dev(children, i32, "children", pages.dev),
+                            n, _dev(status, i32, "status", pages.dev), _dev(ws, None, "workspace", pages.dev), wb, _stream(stream, pages.dev)),
            "kv_pages_fork")
 
 
 def kv_pages_free(pages: KvPages, rows, stream=None) -> None:
     """Sequences rows (int32) become empty; pages nobody holds go back to the stack."""
-    _check(_c.kv_pages_free(pages.ref, _dev(rows, torch.int32, "rows"), rows.numel(), _stream(stream, pages.refs)),
+    _check(_c.kv_pages_free(pages.ref, _dev(rows, torch.int32, "rows", pages.dev), rows.numel(), _stream(stream, pages.dev)),
            "kv_pages_free")
 
 
 def kv_pages_compact(pages: KvPages, data, workspace=None, stream=None) -> None:
     """Moves the held pages to the pool's beginning, in every layer of data."""
-    dp, layers, pb = _pool(data, pages.c.npages)
+    dp, layers, pb = _pool(data, pages.c.npages, pages.dev)
     ws, wb = _page_ws(pages, workspace, stream)
-    _check(_c.kv_pages_compact(pages.ref, dp, layers, pb, _dev(ws, what="workspace"), wb, _stream(stream, pages.refs)),
+    _check(_c.kv_pages_compact(pages.ref, dp, layers, pb, _dev(ws, None, "workspace", pages.dev), wb, _stream(stream, pages.dev)),
            "kv_pages_compact")
 
 
@@ -284,6 +303,7 @@ def kv_pages_copy(data, npages: int, src, dst, stream=None) -> None:
     n = src.numel()
     if dst.numel() != n:
         raise ValueError("src, dst: as many destinations as sources expected")
-    dp, layers, pb = _pool(data, npages)
-    _check(_c.kv_pages_copy(dp, layers, npages, pb, _dev(src, torch.int32, "src"), _dev(dst, torch.int32, "dst"), n,
-                            _stream(stream, src)), "kv_pages_copy")
+    dev = _on(data, "data")
+    dp, layers, pb = _pool(data, npages, dev)
+    _check(_c.kv_pages_copy(dp, layers, npages, pb, _dev(src, torch.int32, "src", dev),
+                            _dev(dst, torch.int32, "dst", dev), n, _stream(stream, dev)), "kv_pages_copy")

@@ -88,3 +88,93 @@ def test_calls_without_rows_take_arrays_without_an_address():
     assert f.kv_pages_extend(pa, A, A, 1, None, 5, A, None) == qb.QB_E_ARG
     bad = _cache(page=24)
     assert f.kv4_append(ctypes.addressof(bad), 0, None, 128, None, 128, None, 0, None) == qb.QB_E_ARG
+
+
+class _On:
+    """A tensor's outside: on device `at`, at an address that nothing reads."""
+
+    def __init__(self, at, shape, dtype):
+        import torch
+        self.like, self.at, self.dtype, self.shape = torch.empty(shape, dtype=dtype, device="meta"), at, dtype, torch.Size(shape)
+
+    def __getattr__(self, name):
+        return getattr(self.like, name)
+
+    def get_device(self):
+        return self.at
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The entry points that a call reaches, none of them made; device 0 is the current one."""
+    made = []
+
+    class Entries:
+        def __getattr__(self, name):
+            return lambda *a: made.append(name) or qb.QB_OK
+
+    monkeypatch.setattr(kv4, "_c", Entries())
+    monkeypatch.setattr(kv4, "_current_device", lambda: 0)
+    monkeypatch.setattr(kv4, "_raw_stream", lambda dev: 0)
+    return made
+
+
+def _everything(at):
+    """Every call of the binding with tensors where `at(name)` says."""
+    import torch
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+
+    def t(name, shape, dtype=i32):
+        return _On(at(name), shape, dtype)
+
+    bb = 64 * 16 // 2 * 2 + 64 * 16 // 16 * 2
+    c = kv4._CKv4(A, 8, 16, 2, 64)
+    cache = object.__new__(kv4.Kv4)
+    cache.data, cache.page, cache.nkv, cache.d, cache.dev, cache.c, cache.ref = t("data", (8, 2 * bb), u8), 16, 2, 64, at("data"), c, ctypes.addressof(c)
+    rows, q, lse, ws = ((3, 2, 64), (3, 4, 64), (3, 4), (1 << 20,))
+
+    def seqs():
+        return kv4.KvSeqs(t("tables", (3, 4)), t("lens", (3,)), t("rows", (3,)), t("q_start", (4,)))
+
+    def pages():
+        return kv4.KvPages(16, t("nfree", (1,)), t("free", (8,)), t("refs", (8,)), t("lens", (3,)), t("tables", (3, 4)))
+
+    def pool():
+        return t("pool", (2, 8, 64), u8)
+
+    return {
+        "kv4_append": lambda: kv4.kv4_append(cache, t("k", rows, f32), t("v", rows, f32), t("slots", (3,))),
+        "kv4_read": lambda: kv4.kv4_read(cache, t("slots", (3,)), t("k", rows, f32), t("v", rows, f32)),
+        "kv4_attn": lambda: kv4.kv4_attn(cache, t("q", q, f32), seqs(), 1.0, t("out", q, f32), t("lse", lse, f32), workspace=t("ws", ws, u8)),
+        "kv_pages_reset": lambda: kv4.kv_pages_reset(pages()),
+        "kv_pages_extend": lambda: kv4.kv_pages_extend(pages(), t("rows", (3,)), t("counts", (3,)), t("slots", (9,)), t("status", (3,))),
+        "kv_pages_fork": lambda: kv4.kv_pages_fork(pages(), pool(), t("parents", (1,)), t("children", (1,)), t("status", (1,)), t("ws", ws, u8)),
+        "kv_pages_free": lambda: kv4.kv_pages_free(pages(), t("rows", (3,))),
+        "kv_pages_compact": lambda: kv4.kv_pages_compact(pages(), pool(), t("ws", ws, u8)),
+        "kv_pages_copy": lambda: kv4.kv_pages_copy(pool(), 8, t("src", (2,)), t("dst", (2,))),
+    }
+
+
+USES = {"kv4_append": "data k v slots", "kv4_read": "data slots k v", "kv4_attn": "data q tables lens rows q_start out lse ws",
+        "kv_pages_reset": "nfree free refs lens tables", "kv_pages_extend": "refs rows counts slots status", "kv_pages_fork": "refs pool parents children status ws",
+        "kv_pages_free": "refs rows", "kv_pages_compact": "refs pool ws", "kv_pages_copy": "pool src dst"}
+
+
+@pytest.mark.parametrize("call", sorted(USES))
+def test_tensors_lie_on_the_current_device(calls, call):
+    """On device 0, the current one, the call is made; all on device 1, or any one tensor there or in host memory, and nothing is."""
+    _everything(lambda name: 0)[call]()
+    assert calls == [call]
+    calls.clear()
+    with pytest.raises(ValueError, match="current device"):
+        _everything(lambda name: 1)[call]()
+    for one in USES[call].split():
+        with pytest.raises(ValueError, match="cuda:"):
+            _everything(lambda name: int(name == one))[call]()
+        if one != "data":  # a cache refuses host memory itself
+            with pytest.raises(ValueError, match="device memory"):
+                _everything(lambda name: -int(name == one))[call]()
+    assert calls == []
