@@ -15,6 +15,7 @@
 namespace qb {
 
 __device__ int g_fault = 0;
+static __global__ void fault_clear_kernel(int bits) { atomicAnd(&g_fault, ~bits); }
 __device__ int g_unreadable = 0;
 
 // Per-device caches: each entry is written once per device with the same
@@ -264,13 +265,16 @@ int64_t q_weight_bytes(qb_fmt fmt, int64_t rows, int64_t K) {
 
 int q_device_status(void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int h = 0, zero = 0;
+    int h = 0;
     if (cudaMemcpyFromSymbolAsync(&h, g_fault, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return QB_E_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_fault, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return QB_E_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return QB_E_CUDA;
-    return h & kFaultMbarTimeout ? QB_E_DEVICE : h ? QB_E_INDEX : QB_OK;
+    const int bit = fault_reported(h);
+    if (bit) {  // the other bits stay, those too that another stream's kernels have set since
+        fault_clear_kernel<<<1, 1, 0, s>>>(bit);
+        if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) return QB_E_CUDA;
+    }
+    return fault_status(bit);
 }
 
 static int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }

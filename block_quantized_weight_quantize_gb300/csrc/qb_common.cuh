@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "qb_fault.h"
 #include "qgemv.h"
 
 namespace qb {
@@ -23,12 +24,6 @@ __host__ __device__ inline int64_t record_bytes(int f, int64_t K) {
     if (f == kQ4K) return 144 * (K / 256);
     return (210 * (K / 256) + 15) / 16 * 16;
 }
-
-// Bit set in the library's device fault word (a __device__ int in qb_api.cu,
-// passed to kernels by address) when a kernel gives up a bounded wait.
-constexpr int kFaultMbarTimeout = 1;
-// ... and when a 4-bit cache or page kernel meets an index outside its cache.
-constexpr int kFaultIndex = 2;
 
 // ---------------------------------------------------------------- PTX wrappers
 

@@ -241,10 +241,10 @@ QB_API int64_t q_weight_bytes(qb_fmt fmt, int64_t rows, int64_t K);
 QB_API int q_block_values(qb_fmt fmt, const void *W, int64_t rows, int64_t K, const qb_act *act, int ncols,
                    int32_t *C, int32_t *O, float *v, void *stream);
 
-/* Reads and clears the library's device fault word (set when a kernel gives
- * up a bounded wait on its own copies, or when a 4-bit cache or page kernel
- * meets an index outside its cache).  Synchronizes `stream`.  Returns QB_OK,
- * QB_E_DEVICE or QB_E_INDEX. */
+/* Reads the library's device fault word (set when a kernel gives up a bounded
+ * wait on its own copies, or when a 4-bit cache or page kernel meets an index
+ * outside its cache) and clears what it reports, one kind a call: QB_E_DEVICE
+ * first, then QB_E_INDEX, then QB_OK.  Synchronizes `stream`. */
 QB_API int q_device_status(void *stream);
 
 /* Most matrices one grouped call (q_gemv_many, q_gemv_f16_many,

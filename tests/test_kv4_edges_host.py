@@ -18,16 +18,19 @@ TOP = 2 ** 31
 
 @pytest.fixture(scope="module")
 def index(tmp_path_factory):
-    """The functions of qb_kv_index.h as a host library, every signed overflow an abort."""
+    """The functions of qb_kv_index.h and qb_fault.h as a host library, every signed overflow an abort."""
     if not shutil.which("g++"):
         pytest.skip("no g++")
     d = tmp_path_factory.mktemp("index")
-    (d / "i.cpp").write_text("""#include "qb_kv_index.h"
+    (d / "i.cpp").write_text("""#include "qb_fault.h"
+#include "qb_kv_index.h"
+extern "C" int reported(int word) { return qb::fault_reported(word); }
+extern "C" int status(int bit) { return qb::fault_status(bit); }
 extern "C" long long room(long long c, long long first, long long n) { return qb::kv_slots_room(c, first, n); }
 extern "C" int parts(int len, int size) { return qb::kv_parts(len, size); }
 extern "C" int first_seen(int pos, int window) { return qb::kv_first_seen(pos, window); }
 """)
-    subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", str(CSRC), str(d / "i.cpp"),
+    subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", str(CSRC), "-I", str(CSRC.parent.parent / "include"), str(d / "i.cpp"),
                     "-o", str(d / "i.so")], check=True)
     lib = ctypes.CDLL(str(d / "i.so"))
     lib.room.argtypes, lib.room.restype = [ctypes.c_longlong] * 3, ctypes.c_longlong
@@ -178,3 +181,19 @@ def test_tensors_lie_on_the_current_device(calls, call):
             with pytest.raises(ValueError, match="device memory"):
                 _everything(lambda name: -int(name == one))[call]()
     assert calls == []
+
+
+def test_every_kind_of_fault_is_reported(index):
+    """A word with both kinds gives two reports, the given-up wait first; what one call reports is all that it clears."""
+    reports = []
+    word = 3
+    for _ in range(3):
+        bit = index.reported(word)
+        reports.append(index.status(bit))
+        word &= ~bit
+    assert reports == [qb.QB_E_DEVICE, qb.QB_E_INDEX, qb.QB_OK] and word == 0
+    assert index.status(index.reported(2)) == qb.QB_E_INDEX and index.status(index.reported(1)) == qb.QB_E_DEVICE
+    text = (CSRC / "qb_api.cu").read_text()
+    body = text[text.index("int q_device_status("):]
+    body = body[:body.index("\n}\n")]
+    assert "fault_clear_kernel" in body and "cudaMemcpyToSymbol" not in body    # no bit is overwritten
