@@ -98,7 +98,7 @@ struct PromptSmem {
     uint16_t flags[4][kPromptTile];  // of a tile's keys: 1 K, 2 V decoded 2^-4 smaller; from bit 8 the groups that are not finite
     uint32_t any[4][4];              // whether a decoder warp's keys have one
     uint64_t q_full[kPromptQ], q_free[kPromptQ], s_full[kPromptQ], p_ready[kPromptQ], o_done[kPromptQ];
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], drained;
     uint32_t tmem;
     long long chunk_sum[8192 / 32 + 1];
     long long x0, share;             // the block's share: its first place, its places
@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.v_free[i], 1);
         }
+        mbar_init(&sm.drained, 1);
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -882,6 +883,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             if (!ok) break;
             if (it.fine) item(std::true_type());
             else item(std::false_type());
+        }
+        // tensor and shared memory are given back after the last product, also where a wait was given up
+        if (warp == 12) {
+            if (elect_one()) tc_commit(&sm.drained);
+            __syncwarp();
+            prompt_wait(&sm.drained, 0, p.a.fault);
         }
     }
     tc_fence_before();

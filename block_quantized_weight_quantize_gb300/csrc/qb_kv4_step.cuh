@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             if (!__all_sync(0xFFFFFFFFu, landed)) {  // a copy never completed: fault word raised
                 failed = 1;
                 count = -1;
+                cur.u = u;
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
@@ -858,6 +859,18 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             place += kItemCost;
         } else {
             cur.u += units;
+        }
+    }
+
+    // a block does not end while copies issued after one that was given up may still write its memory (waits bounded too)
+    if (count < 0) {
+#pragma unroll 1
+        for (int i = 1; i < kStages; ++i) {
+            if (++cur.u == cur.u_end) step_item<R, U>(p, tab, base, cur);
+            if (cur.u == ahead.u && cur.rt == ahead.rt && cur.kvh == ahead.kvh && cur.s == ahead.s) break;
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            phase ^= slot == 0 ? 1u : 0u;
+            mbar_wait_bounded(full + slot, phase, p.a.fault);
         }
     }
 
