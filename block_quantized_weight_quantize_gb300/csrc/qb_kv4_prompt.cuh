@@ -8,10 +8,10 @@
 //     S = Q K^T (f32), P = 2^(S cs - m) (f16), O += P V (f32),
 // m 11 below a running maximum, which moves only when P would pass f16's top, when
 // O is rescaled in tensor memory; sums in f32.  The largest probability then lies at
-// 2^11 to 2^15.9 (2^11 itself where m has last moved, so that it is not rounded), and
-// f16's last place, 2^-24, is 2^-35 of it or less: what is below 2^-36 vanishes.
-// (13 instead of 11: m moves more often, 330 us for 2048 tokens on 8192 keys, 32
-// heads of 128, against 257; m at the maximum and 8 let pass: 256 us, but what is
+// 2^11 to 2^15.9, and f16's last place, 2^-24, is 2^-35 of it or less: what is below
+// 2^-36 vanishes.  m moves by whole numbers, so that a rescaled P is not rounded
+// anew.  (13 instead of 11: m moves more often, 330 us for 2048 tokens on 8192 keys,
+// 32 heads of 128, against 253; m at the maximum and 8 let pass: 256 us, but what is
 // below 2^-25 vanishes.)
 //
 // A rounded key moves a score by 2^-12 of its terms, which averages out over many
@@ -146,8 +146,9 @@ __device__ __forceinline__ uint32_t prompt_flags(const uint16_t *flags, int lo, 
     return all;
 }
 
-// The probability of the maximum that m was taken from is 2^kPromptTop, and m rises
-// when one would pass 2^kPromptMost (f16 ends at 2^16).
+// The probability of the maximum that m was taken from is 2^kPromptTop or, as m rises by
+// whole numbers, up to twice that, and m rises when one would pass 2^kPromptMost (f16
+// ends at 2^16).
 constexpr float kPromptTop = 11.0f, kPromptMost = 15.9f;
 
 // What a row's softmax carries from tile to tile.
@@ -157,19 +158,22 @@ struct PromptRow {
     int lo, hi;       // columns lo..hi of the step are seen
 };
 
-// m rises to mn in lanes where that is more: O (DP columns, if
-// any products were added), the `done` columns of this step's probabilities and the sums l
-// and `sum` shrink; nothing of the other lanes changes, whose rows keep their bits.
+// m rises to mn in lanes where that is more, by a whole number but from -infinity: O (DP
+// columns, if any products were added), the `done` columns of this step's probabilities and
+// the sums l and `sum` shrink by a power of two, so that no probability is rounded again but
+// below f16's normal numbers; nothing of the other lanes changes, whose rows keep their bits.
+// (Its loops are not unrolled, as it is there six times: 256 -> 253 us.)
 template <int DP>
 __device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int done, float &m, float &l, uint64_t &sum,
                                                    float mn, bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
-    const float al = mn == m ? 1.0f : prompt_ex2(m - mn);
+    const float al = mn == m ? 1.0f : prompt_ex2(rintf(m - mn));
     l *= al;
     sum = mul_f32x2(sum, pair_f32(al, al));
     m = mn;
     if (have_o) {
         if (!prompt_wait(o_done, parity, fault)) return false;
         tc_fence_after();
+#pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             tc_ld32(tO + 32 * c, o);
@@ -180,13 +184,15 @@ __device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int don
     }
     if (done) {
         tc_wait_st();
-        const __half2 a2 = __float2half2_rn(al);
+        // in two factors: f16 holds none below 2^-24
+        const __half2 a2 = __float2half2_rn(fmaxf(al, 0x1p-14f)), b2 = __float2half2_rn(fminf(al * 0x1p14f, 1.0f));
+#pragma unroll 1
         for (int c = 0; c < done; c += 32) {  // 16 or 48 columns: the rest of the last 32 is scores, kept
             uint32_t o[32];
             tc_ld32(tS + c, o);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (c + i < done) o[i] = prompt_half2(__hmul2(*reinterpret_cast<const __half2 *>(&o[i]), a2));
+                if (c + i < done) o[i] = prompt_half2(__hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&o[i]), a2), b2));
             if (done - c >= 32) {
                 tc_st32(tS + c, o);
             } else {
@@ -237,7 +243,9 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
         if (__any_sync(0xFFFFFFFFu, z > row.m + kPromptMost)) {
             // no score stays in a register meanwhile: they are read again
             tc_ld_wait(next);
-            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, sum, z > row.m + kPromptMost ? z - kPromptTop : row.m, have_o, o_done, parity, fault) && ok;
+            const float mn = !(z > row.m + kPromptMost) ? row.m
+                             : row.m == -INFINITY       ? z - kPromptTop : row.m + floorf(z - kPromptTop - row.m);
+            ok = prompt_rescale<DP>(tS, tO, 16 * c, row.m, row.l, sum, mn, have_o, o_done, parity, fault) && ok;
             tc_ld32_begin(tS + 32 * c, x);
             tc_ld_wait(x);
             if (c < 3) tc_ld32_begin(tS + 32 * (c + 1), next);

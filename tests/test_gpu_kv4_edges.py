@@ -127,9 +127,11 @@ def _beside_one_key(name, d, n, T, gap, place, seed=71):
 
 @pytest.mark.parametrize("name", ["f16", "bf16"])
 @pytest.mark.parametrize("gap", [10.0, 18.0, 21.0])
-@pytest.mark.parametrize("d,n,T,place", [(64, 1900, 100, 3), (128, 900, 100, 780), (128, 2300, 120, 0), (64, 300, 20, 3)])
+@pytest.mark.parametrize("d,n,T,place", [(64, 1900, 100, 3), (128, 900, 100, 780), (128, 2300, 120, 0), (64, 300, 20, 3), (64, 900, 100, 110),
+                                             (128, 700, 300, 95)])
 def test_small_probabilities_beside_a_large_one(name, gap, d, n, T, place):
-    """Probabilities of 2^-14 to 2^-30 of the largest make up the output, through both kernels."""
+    """Probabilities of 2^-14 to 2^-30 of the largest make up the output, through both kernels; the large one comes first, or late in a
+    tile of 128 keys."""
     _check_probabilities(_beside_one_key(name, d, n, T, gap, place), name, d ** -0.5, 2.0 ** (-36 if T >= 100 else -38))
 
 
@@ -319,3 +321,25 @@ def test_a_workspace_for_another_stream_is_not_memory_still_in_use_here(what, mo
     if what == "attn":
         want, _ = b.run(0.125)
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("nh,nkv,d,lens,news,rel", [
+    (4, 2, 64, [100, 40, 300], [60, 40, 200], 2.0 ** -10), (4, 1, 128, [900, 33], [50, 33], 2.0 ** -10), (6, 2, 96, [1500], [130], 2.0 ** -10),
+    (8, 1, 128, [300, 17, 1000], [4, 1, 3], 2.0 ** -11), (4, 2, 256, [500], [120], 2.0 ** -11), (3, 3, 64, [700, 20], [2, 5], 2.0 ** -11)])
+@pytest.mark.parametrize("kmul,window", [(1.0, 0), (6.0, 0), (1.0, 37)])
+def test_half_precision_holds_its_accuracy(name, nh, nkv, d, lens, news, rel, kmul, window):
+    """Rows of fewer than 2048 keys: queries and keys enter the scores without a rounding, so that a score is off by at most its
+    magnitudes' sum times 2^-19 (f32 sums), lse by that and 2^-19 of its own parts, and an output by twice that relatively and `rel`:
+    2^-11 for the probability times the step (few tokens), 2^-11 each for probability and value (many)."""
+    b = Batch(d + nh, lens, news, nh, nkv, d, 16, name, kmul=kmul)
+    scale = d ** -0.5
+    out, lse = b.run(scale, window)
+    want, wlse, zabs, mag = b.want(scale, window)
+    off = zabs * SUM
+    tol = (2 * off + rel + SUM)[..., None] * mag + OUT[name] * np.abs(want) + 2.0 ** -25 * (name == "f16")
+    tol += len(b.v) * np.abs(b.v).max() * 2.0 ** -36
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= tol), np.max(err / tol)
+    lerr, ltol = np.abs(lse.double().cpu().numpy() - wlse), off + SUM * (1 + np.abs(wlse))
+    assert np.all(lerr <= ltol), np.max(lerr / ltol)
