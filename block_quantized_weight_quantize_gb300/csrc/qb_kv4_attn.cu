@@ -19,14 +19,16 @@ int64_t kv4_attn_ws(int dp) {
 // Rows (token, query head) a sequence and key head, on average, from which the
 // prompt kernel takes a half-precision call: its items have 256 rows, the step
 // kernel's 8, which read and decode the keys anew.  Step against prompt kernel, us,
-// heads of 128, 32 on 8 key heads, in bf16:
+// heads of 128, 32 on 8 key heads, in bf16, every sequence with as many rows:
 //     rows                        64          96          128         192
-//     1 sequence of 2000 keys     18 / 36     20 / 36     22 / 37     27 / 36
-//     1 of 8000                   30 / 33     38 / 33     45 / 33     61 / 33
-//     8 of 2000                   37 / 51     51 / 51     58 / 51     90 / 52
-//     8 of 8000                   99 / 87     149 / 88    176 / 88    290 / 89
-//     64 of 300                   55 / 86     77 / 83     96 / 83     122 / 88
-//     64 of 2000                  191 / 238   277 / 238   339 / 239   509 / 242
+//     1 sequence of 2000 keys     18 / 36     21 / 35     23 / 36     27 / 36
+//     1 of 8000                   30 / 33     39 / 33     46 / 33     62 / 33
+//     8 of 2000                   50 / 52     66 / 52     83 / 52     117 / 52
+//     8 of 8000                   141 / 86    203 / 87    265 / 88    389 / 89
+//     64 of 300                   72 / 86     124 / 82    132 / 80    197 / 91
+//     64 of 2000                  284 / 241   402 / 242   530 / 248   781 / 250
+// The rule takes the slower kernel where one short sequence fills little of the card
+// (from 96 rows) and where much work has 64 to 95 rows.
 constexpr int kPromptFrom = 96;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {

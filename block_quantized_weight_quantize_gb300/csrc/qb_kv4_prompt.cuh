@@ -2,7 +2,7 @@
 // their chunks) over the paged 4-bit cache, in half precision, on the
 // fifth-generation tensor cores.
 //
-// Mathematics: as in qb_kv4_step.cuh, but with 128 rows and more a key head the
+// Mathematics: as in qb_kv4_step.cuh, but with some 100 rows and more a key head the
 // products bound it, so keys and values are decoded once a tile to f16
 // ((code - 8) * step, rounded once) and the tensor cores do the rest:
 //     S = Q K^T (f32), P = 2^(S cs - m) (f16), O += P V (f32),
@@ -16,22 +16,25 @@
 //
 // A rounded key moves a score by 2^-12 of its terms, which averages out over many
 // keys but not over few: lse is off by 1e-5 to 2e-5 of itself at 100 keys, 3e-6 at
-// 500, 1.2e-6 at 2200, 5e-7 at 8192.  Where a row of an item sees fewer than kPromptFine
+// 500, 7e-7 at 2400, 3e-7 at 8192.  Where a row of an item sees fewer than kPromptFine
 // keys, what the rounding leaves is decoded too (one multiply-add, exact) and multiplied
-// by Q into the same scores: 1e-7 then.  It costs 5 to 30% (a prompt of 2048 tokens by
-// itself, 32 heads of 128: 90 -> 98 us; 64 sequences of 64 tokens on 2000 keys: 188 ->
-// 248).  The output keeps the error of values and probabilities in f16: 3.4e-4 to 4.2e-4
-// of an f16 output, 2.1e-4 of it the output's own rounding.
+// by Q into the same scores: 1e-7 then.  It costs 10 to 46% (a prompt of 2048 tokens by
+// itself, 32 heads of 128: 88 -> 97 us; 64 sequences of 64 tokens on 2000 keys: 193 ->
+// 256; 2048 tokens on 8192 keys, were they to take it, 251 -> 366).  A row that sees
+// more keys but weighs few of them averages nothing out: with scores of magnitudes up to
+// 78, lse is off by up to 4e-3 (8e-4 in the mean square), where it is 2e-5 below kPromptFine.
+// The output keeps the error of values and probabilities in f16: 2.8e-4 to 4.0e-4 of an
+// f16 output, 7e-4 in those rows; 2.1e-4 of it is the output's own rounding.
 //
 // Work: an item is 256 rows (two tiles of 128; row = token * heads of the key
 // head + head) of one sequence and key head, over the tiles of 128 keys that they
 // see.  Tiles are counted along all items, one more for an item's own cost; every
 // block takes the same count of consecutive ones.  An item that blocks share
 // leaves its rows' sums in the workspace, joined by kv4_prompt_join_kernel.
-// (Whole items to a block: 258 us for 2048 tokens on 8192 keys, 32 heads of 128,
-// 256 items on 152 multiprocessors; shared ones 254 us with their join: 0.95 PFLOP/s
-// where a plain product of matrices reaches 1.9.  With few
-// items it is what fills the card.)
+// (Whole items to a block, 2048 tokens on 8192 keys, 32 heads of 128, 256 items on 152
+// multiprocessors: 258 us when shared ones took 254 with their join; 253 now, 0.95
+// PFLOP/s where a plain product of matrices reaches 1.9.  With few items it is what
+// fills the card.)
 // Roles of a block's 16 warps (152 registers a thread in warps 0-7, 104 in the
 // others: 2 * 152 + 2 * 104 = the 4 * 128 of the launch):
 //   0-3, 4-7  softmax of tile 0, 1: a thread a row, 32 scores at a time from

@@ -39,7 +39,7 @@
 // blocks share is joined by kv4_combine_kernel, in the order of the keys.
 //
 // Measured: 64 sequences of up to 8192 keys (297 MB of cache), one token each in f32,
-// 32 heads of 128 on 8 key heads: 77.6 us, 3.9 TB/s.  Instructions bound it (49 million a
+// 32 heads of 128 on 8 key heads: 78.4 us, 3.9 TB/s.  Instructions bound it (49 million a
 // call, 2.2 a cycle and multiprocessor; with the arithmetic taken out the copies alone
 // took 60 us, and the arithmetic alone 69).  One sequence of 131071 keys in bf16 (151 MB):
 // 48 us, 3.2 TB/s, of which some 10 are the start and 8 the joins.
@@ -1063,11 +1063,12 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     // f32 enters as high and low parts for its accuracy: side by side in tiles of 4 rows, or in
     // tiles of 8 with a product more for the low parts, which decode a key for twice the rows.
     // By the rows a sequence and key head, on average (us in tiles of 4, of 8): 256 sequences of
-    // 1000 keys, 8 rows 119, 123, 16 rows 180, 169, 64 rows 693, 533; one of 600 keys, 8 rows
-    // 11.1, 12.9, 64 rows 13.9, 15.2.  Half precision takes tiles of 4 where a tile of 8 would only
-    // be padded (4 rows: 88, 91), and eights from there on.  (Two such column tiles, which decode
-    // a key once for both, leave 8 warps a multiprocessor instead of 12: 16 rows 182 us
-    // against 130 in bf16, 184 against 180 in f32.)
+    // 1000 keys, 4 rows 87, 120, half of them 4 and half 8 119, 125, 8 rows 150, 127, 16 rows 281,
+    // 223, 64 rows 1023, 741; one of 600 keys, 8 rows 11.2, 13.6, 64 rows 13.9, 15.4.  Half precision
+    // takes tiles of 4 where a tile of 8 would only be padded (4 rows: 88, 95), and eights from
+    // there on (8 rows: 152, 102).  (Two such column tiles, which decode a key once for both, leave
+    // 8 warps a multiprocessor instead of 12: up to 16 rows 182 us against 130 in bf16, 184 against
+    // 180 in f32.)
     const bool low = a.type == QB_T_F32, few = a.ntok * p.grp <= (low ? 8 : 4) * (int64_t)a.s.nseq;
     if (a.c.page == 16)
         return few ? launch_step_k<DP, true, false, 16>(p, grid, stream)

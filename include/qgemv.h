@@ -494,18 +494,22 @@ QB_API int64_t kv4_attn_workspace_bytes(const qb_kv4 *cache, int nh);
  *     lse = log sum_i exp(z_i);
  * a token that sees no key gets out 0 and lse -infinity.  q and out
  * [ntok][nh][d] of `type` with q_stride and out_stride elements between
- * tokens; lse f32 [ntok][nh] or NULL.  Sums and softmax statistics are f32; with
- * QB_T_F32 queries and probabilities enter the products as pairs of f16 (22
- * bits), otherwise as one f16.  A probability (of the largest, 1) below 2^-38
- * may vanish beside the largest step among the values that the token sees; in
- * half-precision calls of many tokens one below 2^-36, or below 2^-32 where the
- * token sees a value step of 2^12 or more.  A key or value that a token does not
- * see changes no bit of its output.  Queries of magnitude past 2^110 are out of range.  q, out 16-byte aligned, strides multiples of 16
- * bytes; nh % nkv == 0; ntok <= 2^24, ntok * nh <= 2^30.
+ * tokens; lse f32 [ntok][nh] or NULL.  Sums and softmax statistics are f32;
+ * with QB_T_F32 queries and probabilities enter the products as pairs of f16
+ * (22 bits), otherwise as one f16; in half-precision calls of many tokens (96
+ * rows a sequence and key head on average, d <= 128) values too, and the keys
+ * of tokens that see 2048 keys or more.  A probability (of the largest, 1)
+ * below 2^-38 may vanish beside the largest step among the values that the
+ * token sees; in half-precision calls of many tokens one below 2^-36, or below
+ * 2^-32 where the token sees a value step of 2^12 or more.  A key or value
+ * that a token does not see changes no bit of its output.  Queries of
+ * magnitude past 2^110 are out of range.  q, out 16-byte aligned, strides
+ * multiples of 16 bytes; nh % nkv == 0; ntok <= 2^24, ntok * nh <= 2^30.
  * workspace: at least kv4_attn_workspace_bytes() bytes, 16-byte aligned, not
- * shared with a call that may run at the same time.  A length past its table row is cut to it; a row
- * or page number outside its range reads as no keys / page 0 and is reported
- * by q_device_status; tokens that no sequence holds are not written. */
+ * shared with a call that may run at the same time.  A length past its table
+ * row is cut to it; a row or page number outside its range reads as no keys /
+ * page 0 and is reported by q_device_status; tokens that no sequence holds are
+ * not written. */
 QB_API int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void *q, int64_t q_stride,
                     int64_t ntok, int nh, float scale, int window, void *out, int64_t out_stride, float *lse,
                     void *workspace, size_t workspace_bytes, void *stream);
@@ -517,7 +521,9 @@ QB_API int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, c
  * free_pages[nfree-1]), refs[npages] how many sequences hold a page, and for
  * each sequence its length lens[nrows] and its table row
  * tables[nrows][maxp]: ceil(len/page) page numbers, then -1.  A page held
- * more than once is full.  The pages' bytes are opaque here: any cache laid
+ * more than once is full.  Lengths and table rows are changed by the calls
+ * below alone: a length lowered by hand loses the pages past it, and no call
+ * takes tokens back.  The pages' bytes are opaque here: any cache laid
  * out [layers][npages][page_bytes] can use these calls, page_bytes % 16 == 0.
  * npages <= 2^20.  Every call is asynchronous on stream and gives the same
  * state whatever the order its threads run in.  Sequence numbers
