@@ -1027,11 +1027,12 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const StepK p, int blo
 // ---------------------------------------------------------------- launch
 
 // Where the table rows hold no more keys than this, items are not split and no join
-// is launched (one sequence of 100 keys: 9.4 us, 12.7 with the join).
+// is launched (one sequence of 100 keys: 8.3 us, 10.6 with the join, which
+// a wider table takes whatever the lengths are).
 constexpr int kNoSplitKeys = 256;
 // A block has at least this many keys' places: on short sequences more blocks cost more in
 // the join than they save, fewer leave more to each (64, 128, 256, two tokens on 200 keys in
-// bf16: 11.5, 12.1, 12.9 us; one on 600: 11.7, 11.3, 11.5).
+// bf16: 12.4, 12.7, 13.3 us; one on 600: 11.9, 11.7, 12.0).
 constexpr int kMinShareKeys = 128;
 
 template <int DP, bool PAIR, bool LOW, int SB>
