@@ -37,7 +37,8 @@ EXPORTS = ("quantize_act", "q_gemv", "quantize_act_f16", "q_gemv_f16", "q_check_
            "kv_quantize_heads", "kv_scores", "q_gemv_fp8", "q_matvec_host_workspace_bytes", "q_matvec_host", "q_gemv_w2",
            "kv4_block_bytes", "kv4_append", "kv4_read", "kv4_attn_workspace_bytes", "kv4_attn",
            "kv_pages_workspace_bytes", "kv_pages_reset", "kv_pages_extend", "kv_pages_fork", "kv_pages_free",
-           "kv_pages_compact", "kv_pages_copy")
+           "kv_pages_compact", "kv_pages_copy", "kv4_attn_sinks", "kv4_attn_tree", "kv_tree_masks", "kv_tree_accept", "kv4_keep",
+           "q_logprobs")
 PERBLOCK, SUB32 = 0, 1  # QB_PERBLOCK, QB_SUB32: how an activation (or a query head) is scaled
 
 

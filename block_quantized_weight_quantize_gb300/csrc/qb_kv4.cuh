@@ -160,12 +160,40 @@ struct Kv4AttnArgs {
     int nh;
     float scale;
     int window;
+    int sinks;              // first keys that stay visible; 0 without a window
+    const uint32_t *masks;  // [ntok][words] drafts that a token sees; NULL: all up to itself
+    int words;
     void *out;
     int64_t out_stride;
     float *lse;
     uint8_t *ws;
     int *fault;
 };
+// Whether a call takes the kernels that look keys up one by one (trees, sinks).
+inline bool kv4_attn_ext(const Kv4AttnArgs &a) { return a.masks != nullptr || a.sinks > 0; }
+// What token j (a row's; j < T) of a sequence sees (qb_kv_index.h), and whether it sees one of the keys k0..k0+31.
+__device__ __forceinline__ KvSight kv4_sight(const Kv4AttnArgs &a, int len, int T, int q0, int j) {
+    const int base = len - T;
+    if (a.masks) return kv_tree_sight(a.masks + (int64_t)(q0 + j) * a.words, a.words, T, base, a.window);
+    return KvSight{kv_first_seen(base + j, a.window), base + j, kKvNoKey};
+}
+__device__ __forceinline__ uint32_t kv4_seen(const Kv4AttnArgs &a, const KvSight &s, int len, int T, int q0, int j, int k0) {
+    return kv_seen_word(s, a.sinks, a.masks ? a.masks + (int64_t)(q0 + j) * a.words : nullptr, a.words, len - T, len, k0);
+}
+// The first key that any token from j_lo on sees beside the sinks, at the least; one that each up to j_hi sees from
+// on, at the most; the last key that each from j_lo on sees before any draft or key that some do not.
+__device__ __forceinline__ int kv4_first_lo(const Kv4AttnArgs &a, int len, int T, int j_lo) {
+    return kv_first_seen(len - T + (a.masks ? -1 : j_lo), a.window);
+}
+__device__ __forceinline__ int kv4_first_hi(const Kv4AttnArgs &a, int len, int T, int j_hi) {
+    return kv_first_seen(a.masks ? len - 1 : len - T + j_hi, a.window);
+}
+__device__ __forceinline__ int kv4_pos_lo(const Kv4AttnArgs &a, int len, int T, int j_lo) {
+    return len - T + (a.masks ? -1 : j_lo);
+}
+__device__ __forceinline__ int kv4_pos_hi(const Kv4AttnArgs &a, int len, int T, int j_hi) {
+    return a.masks ? len - 1 : len - T + j_hi;
+}
 // A sequence of the call: its table row, length, new tokens and first new token.
 struct SeqInfo {
     int row, len, T, q0;
@@ -204,6 +232,19 @@ int launch_kv4_step_128(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_step_256(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_prompt_64(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_prompt_128(const Kv4AttnArgs &a, cudaStream_t stream);
+// The same for calls with trees or sinks.
+int launch_kv4_step_ext_64(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_step_ext_128(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_step_ext_256(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_ext_64(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_ext_128(const Kv4AttnArgs &a, cudaStream_t stream);
+
+int launch_kv_tree_masks(const int32_t *parents, int64_t ntok, const int32_t *q_start, int nseq, uint32_t *masks, int words,
+                         int32_t *depth, cudaStream_t stream);
+int launch_kv_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *targets, int64_t ntok,
+                          const int32_t *q_start, int nseq, int32_t *keep, int32_t *nkeep, int32_t *next, cudaStream_t stream);
+int launch_kv4_keep(const qb_kv_pages &p, void *data, int nlayers, int nkv, int d, const int32_t *rows, const int32_t *q_start,
+                    const int32_t *keep, const int32_t *nkeep, int64_t ntok, int n, int32_t *status, cudaStream_t stream);
 
 int64_t kv_pages_ws(int npages, int nrows);
 int launch_kv_pages_reset(const qb_kv_pages &p, cudaStream_t stream);

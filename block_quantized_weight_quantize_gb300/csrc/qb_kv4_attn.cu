@@ -32,6 +32,12 @@ int64_t kv4_attn_ws(int dp) {
 constexpr int kPromptFrom = 96;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
+    if (kv4_attn_ext(a)) {
+        if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)
+            return a.c.dp == 64 ? launch_kv4_prompt_ext_64(a, stream) : launch_kv4_prompt_ext_128(a, stream);
+        return a.c.dp == 64 ? launch_kv4_step_ext_64(a, stream)
+               : a.c.dp == 128 ? launch_kv4_step_ext_128(a, stream) : launch_kv4_step_ext_256(a, stream);
+    }
     if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)
         return a.c.dp == 64 ? launch_kv4_prompt_64(a, stream) : launch_kv4_prompt_128(a, stream);
     return a.c.dp == 64 ? launch_kv4_step_64(a, stream)

@@ -1,0 +1,325 @@
+// qb_kv4_keep.cu -- drafted trees and what becomes of them (qgemv.h: kv_tree_masks,
+// kv_tree_accept, kv4_keep): masks and depths from parents, the path that the target's
+// tokens take, its rows moved together in the 4-bit cache, the rest given back.
+//
+// All of it is latency: a batch of 64 has a few thousand integers and some megabytes of
+// rows.  The rows of a request are moved by blocks that each decide by themselves, from
+// the state as it is before the call, whether the request is refused; a second launch of one
+// block decides the same and changes the state, so that no list passes through memory.
+#include <algorithm>
+#include <cstdint>
+
+#include "qb_kv4.cuh"
+#include "qb_kv_plan.cuh"
+
+namespace qb {
+
+// ---------------------------------------------------------------- trees
+
+struct TreeK {
+    const int32_t *parents, *q_start;
+    int64_t ntok;
+    int nseq;
+    int *fault;
+};
+
+__device__ __forceinline__ void tree_bounds(const TreeK &t, int s, int64_t &q0, int64_t &q1) {
+    q0 = t.q_start ? t.q_start[s] : s;
+    q1 = t.q_start ? t.q_start[s + 1] : s + 1;
+    q0 = min(max(q0, (int64_t)0), t.ntok);
+    q1 = min(max(q1, q0), t.ntok);
+}
+
+constexpr int kTreeThreads = 128, kTreeHeld = 1024;
+
+// A block a sequence, a thread a token: it walks up through the parents, which have lower
+// numbers, so the mask's words are finished from the last to the first.
+__global__ void __launch_bounds__(kTreeThreads) kv_tree_masks_kernel(const TreeK t, uint32_t *masks, int words, int32_t *depth) {
+    __shared__ int held[kTreeHeld];
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int s = blockIdx.x; s < t.nseq; s += gridDim.x) {
+        int64_t q0, q1;
+        tree_bounds(t, s, q0, q1);
+        const int T = (int)(q1 - q0);
+        __syncthreads();  // the sequence before has been read
+        auto parent_of = [&](int j, bool report) {
+            const int p = t.parents[q0 + j];
+            if (p >= -1 && p < j) return p;
+            if (report) atomicOr(t.fault, kFaultIndex);
+            return -1;
+        };
+        for (int j = threadIdx.x; j < T; j += kTreeThreads) {
+            const int p = parent_of(j, true);
+            if (j < kTreeHeld) held[j] = p;
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < T; j += kTreeThreads) {
+            uint32_t *to = masks + (q0 + j) * words;
+            int a = j, n = 0;
+            for (int w = words - 1; w >= 0; --w) {
+                uint32_t bits = 0;
+                while (a >= 32 * w) {
+                    if (a - 32 * w < 32) bits |= 1u << (a - 32 * w);
+                    a = a < kTreeHeld ? held[a] : parent_of(a, false);
+                    ++n;
+                }
+                to[w] = bits;
+            }
+            if (depth) depth[q0 + j] = n - 1;
+        }
+    }
+}
+
+// A warp a sequence: from token 0 on, the lowest-numbered child that the target chose, as long
+// as there is one.  Children have higher numbers than their parents, so that the walk reads
+// the tokens once from the first to the last.
+__global__ void __launch_bounds__(kTreeThreads) kv_tree_accept_kernel(const TreeK t, const int32_t *tokens, const int32_t *targets,
+                                                                      int32_t *keep, int32_t *nkeep, int32_t *next) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    for (int s = (int)(blockIdx.x * (kTreeThreads / 32) + (threadIdx.x >> 5)); s < t.nseq; s += gridDim.x * (kTreeThreads / 32)) {
+        int64_t q0, q1;
+        tree_bounds(t, s, q0, q1);
+        const int T = (int)(q1 - q0);
+        int cur = -1, n = 0, want = -1;
+        if (T > 0) {
+            for (cur = 0;;) {
+                if (lane == 0) keep[q0 + n] = cur;
+                ++n;
+                want = targets[q0 + cur];
+                int found = -1;
+                for (int j0 = cur + 1; j0 < T && found < 0; j0 += 32) {
+                    const int j = j0 + lane;
+                    const uint32_t ok = __ballot_sync(0xFFFFFFFFu, j < T && t.parents[q0 + min(j, T - 1)] == cur &&
+                                                                       tokens[q0 + min(j, T - 1)] == want);
+                    if (ok) found = j0 + __ffs(ok) - 1;
+                }
+                if (found < 0) break;
+                cur = found;
+            }
+        }
+        for (int k = n + lane; k < T; k += 32) keep[q0 + k] = -1;
+        if (lane == 0) {
+            nkeep[s] = n;
+            next[s] = want;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- keeping drafts
+
+struct KeepK {
+    PagesK p;
+    const int32_t *rows, *q_start, *keep, *nkeep;
+    int64_t ntok;
+    int n;
+    // the rows
+    uint8_t *data;
+    int nlayers, nkv, pshift;
+    int64_t layer_bytes, block_bytes;
+    int blocks;  // of a request
+};
+
+struct KeepReq {
+    int row, len, base, T, cnt, status;
+    int64_t q0;
+};
+
+// Request i, looked at by a whole warp: what it says, and whether it is refused.
+__device__ __forceinline__ KeepReq keep_request(const KeepK &k, int i, int lane, bool report) {
+    KeepReq r = {};
+    r.row = k.rows ? k.rows[i] : i;
+    int64_t q1 = k.q_start[i + 1];
+    r.q0 = min(max((int64_t)k.q_start[i], (int64_t)0), k.ntok);
+    q1 = min(max(q1, r.q0), k.ntok);
+    r.T = (int)min(q1 - r.q0, (int64_t)INT32_MAX);
+    r.cnt = k.nkeep[i];
+    r.status = QB_E_ARG;
+    if (r.row < 0 || r.row >= k.p.nrows) {
+        if (report && lane == 0) atomicOr(k.p.fault, kFaultIndex);
+        return r;
+    }
+    r.len = min(max(k.p.lens[r.row], 0), k.p.maxp * k.p.page);
+    r.base = r.len - r.T;
+    if (r.base < 0 || r.cnt < 0 || r.cnt > r.T) return r;
+    bool ok = true;
+    for (int j = lane; j < r.cnt; j += 32) {  // ascending, each a draft's number
+        const int v = k.keep[r.q0 + j], before = j ? k.keep[r.q0 + j - 1] : -1;
+        ok = ok && v > before && v < r.T;
+    }
+    const int32_t *tab = k.p.tables + (int64_t)r.row * k.p.maxp;
+    const int held = kv_parts(r.len, k.p.page), left = kv_parts(r.base + r.cnt, k.p.page);
+    for (int j = (r.base >> k.pshift) + lane; j < held; j += 32) {
+        const int pg = tab[j];
+        if (pg < 0 || pg >= k.p.npages) {
+            if (report) atomicOr(k.p.fault, kFaultIndex);
+            ok = false;
+        } else if (j < left && r.cnt < r.T && k.p.refs[pg] != 1) {
+            ok = false;  // a page of others' would be changed, or left partly filled
+        }
+    }
+    if (__all_sync(0xFFFFFFFFu, ok)) r.status = QB_OK;
+    return r;
+}
+
+constexpr int kKeepThreads = 256, kKeepRows = 32;
+
+// Blocks k.blocks * i .. of request i: a warp takes a (layer, head) after the other, a lane 16-byte
+// pieces of the rows (their steps a piece of their own).  32 kept drafts at a time are
+// read before they are written: as both their old and their new places ascend, and none moves
+// up, what is written lies below what is still to be read.
+template <int DP>
+__global__ void __launch_bounds__(kKeepThreads) kv4_keep_rows_kernel(const KeepK k) {
+    constexpr int W = DP / 32 < 4 ? DP / 32 : 4, NC = DP / 32, P = 2 * (NC + 1);
+    constexpr int kStep = DP / 16;  // bytes of a row's steps
+    __shared__ KeepReq req;
+    __shared__ int s_from[kKeepRows], s_to[kKeepRows], s_fr[kKeepRows], s_tr[kKeepRows];  // pages, rows
+    pdl_launch_dependents();
+    pdl_wait();
+    const int i = blockIdx.x / k.blocks, part = blockIdx.x - i * k.blocks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        const KeepReq r = keep_request(k, i, lane, false);
+        if (lane == 0) req = r;
+    }
+    __syncthreads();
+    if (req.status != QB_OK || req.cnt == req.T) return;  // refused, or all in their places
+    const int page = 1 << k.pshift, codes = page * DP / 2, area = codes + page * DP / 16;
+    const int32_t *tab = k.p.tables + (int64_t)req.row * k.p.maxp;
+    const int pairs = k.nlayers * k.nkv;
+    for (int c0 = 0; c0 < req.cnt; c0 += kKeepRows) {
+        const int n = min(kKeepRows, req.cnt - c0);
+        if ((int)threadIdx.x < n) {
+            const int from = req.base + k.keep[req.q0 + c0 + threadIdx.x], to = req.base + c0 + (int)threadIdx.x;
+            s_from[threadIdx.x] = from == to ? -1 : tab[from >> k.pshift];
+            s_to[threadIdx.x] = tab[to >> k.pshift];
+            s_fr[threadIdx.x] = from & (page - 1);
+            s_tr[threadIdx.x] = to & (page - 1);
+        }
+        __syncthreads();
+        for (int pair = part * (kKeepThreads / 32) + warp; pair < pairs; pair += k.blocks * (kKeepThreads / 32)) {
+            const int layer = pair / k.nkv, head = pair - layer * k.nkv;
+            uint8_t *base = k.data + layer * k.layer_bytes + head * k.block_bytes;
+            const int64_t page_bytes = k.nkv * k.block_bytes;
+            auto place = [&](int pg, int r, int side, int piece) -> uint8_t * {
+                uint8_t *b = base + pg * page_bytes + side * area;
+                return piece == NC ? b + codes + r * kStep : b + ((piece / W) * page + r) * 16 * W + piece % W * 16;
+            };
+            uint4 x[P];
+#pragma unroll
+            for (int t = 0; t < P; ++t) {
+                const int at = t * 32 + lane, m = at / P, piece = at - m * P;
+                if (m >= n || s_from[m] < 0) continue;
+                const int side = piece > NC, pc = piece - side * (NC + 1);
+                const uint8_t *src = place(s_from[m], s_fr[m], side, pc);
+                if (pc < NC) x[t] = *reinterpret_cast<const uint4 *>(src);
+                else if (kStep == 16) x[t] = *reinterpret_cast<const uint4 *>(src);
+                else if (kStep == 8) *reinterpret_cast<uint2 *>(&x[t]) = *reinterpret_cast<const uint2 *>(src);
+                else x[t].x = *reinterpret_cast<const uint32_t *>(src);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < P; ++t) {
+                const int at = t * 32 + lane, m = at / P, piece = at - m * P;
+                if (m >= n || s_from[m] < 0) continue;
+                const int side = piece > NC, pc = piece - side * (NC + 1);
+                // a value row's eighths lie in halves exchanged where its number's second bit is set
+                const int swap = side && pc < NC && ((s_fr[m] ^ s_tr[m]) >> 1 & 1) ? W / 2 : 0;
+                uint8_t *dst = place(s_to[m], s_tr[m], side, pc < NC ? pc ^ swap : pc);
+                if (pc < NC) *reinterpret_cast<uint4 *>(dst) = x[t];
+                else if (kStep == 16) *reinterpret_cast<uint4 *>(dst) = x[t];
+                else if (kStep == 8) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(&x[t]);
+                else *reinterpret_cast<uint32_t *>(dst) = x[t].x;
+            }
+            __syncwarp();
+        }
+        __syncthreads();
+    }
+}
+
+// The state: lengths, tables, references and free pages.  Every request is decided before any changes it.
+__global__ void __launch_bounds__(kPlanThreads) kv4_keep_state_kernel(const KeepK k, int32_t *status) {
+    extern __shared__ uint32_t freed[];  // a bit a page
+    __shared__ int red[33];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int words = (k.p.npages + 31) / 32;
+    for (int i = tid; i < words; i += kPlanThreads) freed[i] = 0;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int i = warp; i < k.n; i += kPlanThreads / 32) {
+        const KeepReq r = keep_request(k, i, lane, true);
+        if (lane == 0) status[i] = r.status;
+    }
+    const int nfree = min(max(k.p.nfree[0], 0), k.p.npages);
+    __syncthreads();
+    for (int i = warp; i < k.n; i += kPlanThreads / 32) {
+        if (status[i] != QB_OK) continue;
+        const int row = k.rows ? k.rows[i] : i;
+        const int64_t q0 = min(max((int64_t)k.q_start[i], (int64_t)0), k.ntok);
+        const int64_t q1 = min(max((int64_t)k.q_start[i + 1], q0), k.ntok);
+        const int len = min(max(k.p.lens[row], 0), k.p.maxp * k.p.page), now = len - (int)(q1 - q0) + k.nkeep[i];
+        int32_t *tab = k.p.tables + (int64_t)row * k.p.maxp;
+        for (int j = kv_parts(now, k.p.page) + lane; j < kv_parts(len, k.p.page); j += 32) {
+            const int pg = tab[j];
+            if (pg >= 0 && pg < k.p.npages && atomicSub(k.p.refs + pg, 1) == 1) atomicOr(freed + (pg >> 5), 1u << (pg & 31));
+            tab[j] = -1;
+        }
+        __syncwarp();  // every lane has read the length
+        if (lane == 0) k.p.lens[row] = now;
+    }
+    __syncthreads();
+    give_back(k.p, freed, words, nfree, red);
+}
+
+// ---------------------------------------------------------------- launchers
+
+static TreeK tree_k(const int32_t *parents, int64_t ntok, const int32_t *q_start, int nseq) {
+    return TreeK{parents, q_start, ntok, nseq, fault_word()};
+}
+
+int launch_kv_tree_masks(const int32_t *parents, int64_t ntok, const int32_t *q_start, int nseq, uint32_t *masks, int words,
+                         int32_t *depth, cudaStream_t stream) {
+    const TreeK t = tree_k(parents, ntok, q_start, nseq);
+    if (!t.fault) return QB_E_CUDA;
+    return launch_pdl(kv_tree_masks_kernel, dim3((unsigned)nseq), dim3(kTreeThreads), 0, stream, t, masks, words, depth);
+}
+
+int launch_kv_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *targets, int64_t ntok,
+                          const int32_t *q_start, int nseq, int32_t *keep, int32_t *nkeep, int32_t *next, cudaStream_t stream) {
+    const TreeK t = tree_k(parents, ntok, q_start, nseq);
+    if (!t.fault) return QB_E_CUDA;
+    const int blocks = (nseq + kTreeThreads / 32 - 1) / (kTreeThreads / 32);
+    return launch_pdl(kv_tree_accept_kernel, dim3((unsigned)blocks), dim3(kTreeThreads), 0, stream, t, tokens, targets, keep, nkeep, next);
+}
+
+int launch_kv4_keep(const qb_kv_pages &p, void *data, int nlayers, int nkv, int d, const int32_t *rows, const int32_t *q_start,
+                    const int32_t *keep, const int32_t *nkeep, int64_t ntok, int n, int32_t *status, cudaStream_t stream) {
+    const int dp = kv4_padded(d);
+    KeepK k = {};
+    k.p = pages_k(p);
+    if (!k.p.fault) return QB_E_CUDA;
+    k.rows = rows;
+    k.q_start = q_start;
+    k.keep = keep;
+    k.nkeep = nkeep;
+    k.ntok = ntok;
+    k.n = n;
+    k.data = static_cast<uint8_t *>(data);
+    k.nlayers = nlayers;
+    k.nkv = nkv;
+    k.pshift = p.page == 16 ? 4 : p.page == 32 ? 5 : 6;
+    k.block_bytes = kv4_block(p.page, dp);
+    k.layer_bytes = (int64_t)p.npages * nkv * k.block_bytes;
+    // four (layer, head) pairs a warp, as long as the grid stays small
+    const int64_t want = ((int64_t)nlayers * nkv + 31) / 32;
+    k.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t(1) << 22) / n));
+    auto *f = dp == 64 ? kv4_keep_rows_kernel<64> : dp == 128 ? kv4_keep_rows_kernel<128> : kv4_keep_rows_kernel<256>;
+    if (const int rc = launch_pdl(f, dim3((unsigned)(k.blocks * n)), dim3(kKeepThreads), 0, stream, k)) return rc;
+    const int smem = (p.npages + 31) / 32 * 4;
+    if (ensure_smem_limit(reinterpret_cast<const void *>(kv4_keep_state_kernel), smem) != QB_OK) return QB_E_CUDA;
+    return launch_pdl(kv4_keep_state_kernel, dim3(1), dim3(kPlanThreads), (size_t)smem, stream, k, status);
+}
+
+}  // namespace qb

@@ -87,6 +87,7 @@ struct PromptItem {
     int count;           // places of the block's share
     int from_start;
     int fine;            // keys as two f16
+    int hole, jump;      // EXT: tiles below `jump` are numbered from `hole` on and stand for the sinks'
 };
 
 constexpr int kPromptFine = 2048;  // keys; see above
@@ -154,6 +155,15 @@ __device__ __forceinline__ uint32_t prompt_flags(const uint16_t *flags, int lo, 
 // ends at 2^16).
 constexpr float kPromptTop = 11.0f, kPromptMost = 15.9f;
 
+// EXT: the row's token, for the keys that it sees; a row without one has T = 0.
+struct PromptSight {
+    const Kv4AttnArgs *a;
+    KvSight s;
+    int len, T, q0, j, k0;  // k0: of the tile
+    __device__ __forceinline__ uint32_t word(int c) const { return T ? kv4_seen(*a, s, len, T, q0, j, k0 + 32 * c) : 0u; }
+};
+struct PromptNoSight {};
+
 // What a row's softmax carries from tile to tile.
 struct PromptRow {
     float cs, m, l;   // factor of the scores, m of the probabilities, sum
@@ -215,15 +225,22 @@ __device__ __forceinline__ bool prompt_rescale(uint32_t tS, uint32_t tO, int don
 // written).  MASKED: scores outside columns lo..hi count as -infinity; ODD:
 // flagged keys' scores or probabilities are 16 times larger.
 // (The loop over pairs of 32 is not unrolled: its body stays in the instruction cache.)
-template <int DP, bool MASKED, bool ODD>
-__device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow &row, const uint16_t *flags, bool have_o,
-                                            uint64_t *o_done, uint32_t parity, int *fault) {
+template <int DP, bool MASKED, bool ODD, class Sight>
+__device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow &row, const Sight &sight, const uint16_t *flags,
+                                            bool have_o, uint64_t *o_done, uint32_t parity, int *fault) {
     uint32_t s0[32], s1[32];
     const uint64_t cs2 = pair_f32(row.cs, row.cs);
     uint64_t sum = 0;  // (0, 0)
     bool ok = true;
     auto special = [&](uint32_t (&x)[32], int c) {
-        if (ODD || MASKED) {
+        if constexpr ((ODD || MASKED) && std::is_same_v<Sight, PromptSight>) {
+            const uint32_t seen = sight.word(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (ODD && (flags[32 * c + i] & 1)) x[i] = __float_as_uint(__uint_as_float(x[i]) * 16.0f);
+                if (!(seen >> i & 1u)) x[i] = 0xFF800000u;
+            }
+        } else if (ODD || MASKED) {
             const int lo = row.lo - 32 * c, hi = row.hi - 32 * c;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -288,8 +305,18 @@ __device__ __forceinline__ bool prompt_step(uint32_t tS, uint32_t tO, PromptRow 
 __device__ __forceinline__ int prompt_pairs(const PromptK &p, int T) { return (T * p.grp + kPromptRows - 1) / kPromptRows; }
 
 // An item's first tile and its tiles (one at least, should it see no key).
-__device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, int rp, int &t0) {
+// With EXT t0 is the first tile's number, and those below `jump` stand for the sinks' tiles.
+template <bool EXT>
+__device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, int rp, int &t0, int &jump) {
     const int j_lo = rp * kPromptRows / p.grp, j_hi = min(T - 1, (rp * kPromptRows + kPromptRows - 1) / p.grp);
+    jump = 0;
+    if constexpr (EXT) {
+        const KvParts parts = kv_sink_parts(kv4_first_lo(p.a, len, T, j_lo), p.a.sinks, kPromptTile);
+        t0 = parts.hole;
+        jump = parts.jump;
+        const int last = kv4_pos_hi(p.a, len, T, j_hi);
+        return max(1, last < 0 ? 0 : last / kPromptTile + 1 - t0);
+    }
     const int pos_lo = len - T + j_lo, pos_hi = len - T + j_hi;
     t0 = kv_first_seen(pos_lo, p.a.window) / kPromptTile;
     return max(1, pos_hi < 0 ? 0 : pos_hi / kPromptTile + 1 - t0);
@@ -299,21 +326,22 @@ __device__ __forceinline__ int prompt_tiles(const PromptK &p, int len, int T, in
 // counts its own sequence's row pairs, or the warp one sequence after the other where
 // that takes fewer steps (32 sequences of a row pair: 19 us one after the other, counted
 // twice).
+template <bool EXT>
 __device__ __forceinline__ long long prompt_places(const PromptK &p, int c, int lane, bool report, SeqInfo &q) {
     q = seq_info(p.a, c * 32 + lane, report);
     uint32_t left = __ballot_sync(0xFFFFFFFFu, q.T > 0);
     const int pairs = prompt_pairs(p, q.T), most = (int)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)pairs);
     long long mine = 0;
-    int t0;
+    int t0, jump;
     if (most <= 4 * __popc(left)) {
-        for (int rp = 0; rp < pairs; ++rp) mine += prompt_tiles(p, q.len, q.T, rp, t0) + kPromptCost;
+        for (int rp = 0; rp < pairs; ++rp) mine += prompt_tiles<EXT>(p, q.len, q.T, rp, t0, jump) + kPromptCost;
         return mine * p.a.c.nkv;
     }
     for (; left; left &= left - 1) {
         const int l = __ffs(left) - 1;
         const int len = __shfl_sync(0xFFFFFFFFu, q.len, l), T = __shfl_sync(0xFFFFFFFFu, q.T, l);
         long long n = 0;
-        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) n += prompt_tiles(p, len, T, rp, t0) + kPromptCost;
+        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) n += prompt_tiles<EXT>(p, len, T, rp, t0, jump) + kPromptCost;
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
         if (lane == l) mine = n * p.a.c.nkv;
@@ -321,9 +349,10 @@ __device__ __forceinline__ long long prompt_places(const PromptK &p, int c, int 
     return mine;
 }
 
+template <bool EXT>
 __device__ __forceinline__ void prompt_count(const PromptK &p, int c, int lane, long long *chunk_sum) {
     SeqInfo q;
-    long long n = prompt_places(p, c, lane, blockIdx.x == 0, q);
+    long long n = prompt_places<EXT>(p, c, lane, blockIdx.x == 0, q);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
     if (lane == 0) chunk_sum[c] = n;
@@ -331,6 +360,7 @@ __device__ __forceinline__ void prompt_count(const PromptK &p, int c, int lane, 
 
 // By warp 0: the chunks' sums become their first places, and the block's share begins
 // at a tile of an item.
+template <bool EXT>
 __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchunks, long long *chunk_sum,
                                                 long long &x0_out, long long &share_out, PromptItem &out) {
     long long total = 0;
@@ -358,7 +388,7 @@ __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchu
             if (chunk_sum[m] <= x0) lo = m; else hi = m;
         }
         SeqInfo q;
-        const long long n = prompt_places(p, lo, lane, false, q);
+        const long long n = prompt_places<EXT>(p, lo, lane, false, q);
         long long sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -378,8 +408,8 @@ __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchu
         it.kvh = (int)(rem / per_head);
         rem -= it.kvh * per_head;
         for (int rp0 = 0; rp0 < prompt_pairs(p, it.T); rp0 += 32) {  // the row pair, 32 at a time
-            int t0;
-            const int w = rp0 + lane < prompt_pairs(p, it.T) ? prompt_tiles(p, it.len, it.T, rp0 + lane, t0) + kPromptCost : 0;
+            int t0, jump;
+            const int w = rp0 + lane < prompt_pairs(p, it.T) ? prompt_tiles<EXT>(p, it.len, it.T, rp0 + lane, t0, jump) + kPromptCost : 0;
             long long end = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -407,6 +437,7 @@ __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchu
 }
 
 // The block's next piece (n = 0 before the first): false when its share is done.
+template <bool EXT>
 __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptItem &io) {
     PromptItem it = io;
     __syncwarp();
@@ -429,20 +460,30 @@ __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptIt
             }
         }
     }
-    int t0;
-    const int tiles = prompt_tiles(p, it.len, it.T, it.rp, t0);
+    int t0, jump;
+    const int tiles = prompt_tiles<EXT>(p, it.len, it.T, it.rp, t0, jump);
+    if constexpr (EXT) {
+        it.hole = t0;
+        it.jump = jump;
+    }
     it.t0 = t0 + it.u;
     it.rest = tiles - it.u;
     it.n = min(it.rest, it.count - it.place);
     it.from_start = it.u == 0;
     const int seen = it.len - it.T + it.rp * kPromptRows / p.grp + 1;  // by the first row
-    it.fine = (p.a.window ? min(seen, p.a.window) : seen) < kPromptFine;
+    if constexpr (EXT) {
+        const int tree = p.a.masks ? it.len - it.T + 1 : seen;  // its context and itself
+        it.fine = (p.a.window ? (int)min((int64_t)tree, (int64_t)p.a.window + p.a.sinks) : tree) < kPromptFine;
+    } else {
+        it.fine = (p.a.window ? min(seen, p.a.window) : seen) < kPromptFine;
+    }
     if (lane == 0) io = it;
     __syncwarp();
     return true;
 }
 
-template <int DP>
+// EXT: a call with sinks or trees (the same code but for which tiles an item has and which of their keys a row sees)
+template <int DP, bool EXT>
 __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const PromptK p) {
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4;  // groups; one plane (DP <= 128)
     constexpr int kOctStride = kPromptTile * 16;      // bytes between groups of eight dims
@@ -476,11 +517,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
 
     // ---- the work: the block's share of the line of tiles
     const int nchunks = (p.a.s.nseq + 31) / 32;
-    for (int c = warp; c < nchunks; c += kPromptThreads / 32) prompt_count(p, c, lane, sm.chunk_sum);
+    for (int c = warp; c < nchunks; c += kPromptThreads / 32) prompt_count<EXT>(p, c, lane, sm.chunk_sum);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) prompt_find(p, lane, nchunks, sm.chunk_sum, sm.x0, sm.share, sm.it[0]);
+    if (warp == 0) prompt_find<EXT>(p, lane, nchunks, sm.chunk_sum, sm.x0, sm.share, sm.it[0]);
     __syncthreads();
     if (warp > 0 && lane == 0) sm.it[warp] = sm.it[0];
     __syncthreads();  // warp 0 goes on in its own after the others have copied it
@@ -496,7 +537,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         uint32_t tiles = 0, items = 0;  // of this row tile so far
         int goes_on = -1;
         bool ok = true;
-        while (ok && prompt_next(p, lane, it)) {
+        while (ok && prompt_next<EXT>(p, lane, it)) {
             const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
             const bool live = j < it.T;
             const int pos = live ? it.len - it.T + j : -1;
@@ -568,30 +609,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             // tiles whose keys all of this row tile's rows see need no mask
             const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
             const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
-            const int pos_lo = j_lo < it.T ? it.len - it.T + j_lo : INT_MAX;  // no row: whatever comes out
-            const int first_hi = j_lo < it.T ? kv_first_seen(it.len - it.T + j_hi, p.a.window) : 0;
+            int pos_lo = INT_MAX, first_hi = 0;  // no row: whatever comes out
+            if (j_lo < it.T) {
+                pos_lo = EXT ? kv4_pos_lo(p.a, it.len, it.T, j_lo) : it.len - it.T + j_lo;
+                first_hi = EXT ? kv4_first_hi(p.a, it.len, it.T, j_hi) : kv_first_seen(it.len - it.T + j_hi, p.a.window);
+            }
+            std::conditional_t<EXT, PromptSight, PromptNoSight> sight;
+            if constexpr (EXT) {
+                sight = PromptSight{&p.a, KvSight{0, -1, kKvNoKey}, it.len, live ? it.T : 0, it.q0, j, 0};
+                if (live) sight.s = kv4_sight(p.a, it.len, it.T, it.q0, j);
+            }
             PromptRow row = {cs, -INFINITY, 0.0f, 0.0f, 0, 0};
             uint32_t bad = 0;
             const int n_tiles = it.n, t_first = it.t0;
             for (int i = 0; i < n_tiles; ++i, ++tiles) {
-                const int k0 = (t_first + i) * kPromptTile;
+                const int k0 = (EXT ? kv_part(t_first + i, it.hole, it.jump) : t_first + i) * kPromptTile;
                 if (!(ok = prompt_wait(&sm.s_full[q], tiles & 1, p.a.fault))) break;
                 tc_fence_after();
                 const uint32_t sl = tiles & 3, par = (tiles - 1) & 1;
                 const bool odd = (sm.any[sl][0] | sm.any[sl][1] | sm.any[sl][2] | sm.any[sl][3]) != 0;
-                const bool masked = k0 + kPromptTile - 1 > pos_lo || k0 < first_hi;
+                const bool masked = k0 + kPromptTile - 1 > pos_lo || (k0 < first_hi && (!EXT || k0 + kPromptTile > p.a.sinks));
                 const uint16_t *flags = sm.flags[sl];
                 row.hi = pos - k0;
                 row.lo = first - k0;
+                if constexpr (EXT) sight.k0 = k0;
                 if (odd) {
-                    const uint32_t fl = prompt_flags(flags, row.lo, row.hi);
+                    uint32_t fl = 0;
+                    if constexpr (EXT) {
+                        for (int c = 0; c < 4; ++c)
+                            for (uint32_t w = sight.word(c); w; w &= w - 1) fl |= flags[32 * c + __ffs(w) - 1];
+                    } else {
+                        fl = prompt_flags(flags, row.lo, row.hi);
+                    }
                     bad |= fl >> 8;
                     row.up = fl & 2u ? 4.0f : 0.0f;
-                    ok = prompt_step<DP, true, true>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, true>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else if (masked) {
-                    ok = prompt_step<DP, true, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, false>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 } else {
-                    ok = prompt_step<DP, false, false>(tS, tO, row, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, false, false>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
                 }
                 if (!ok) break;
                 tc_wait_st();
@@ -688,7 +744,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         constexpr int NV = DP / 32;  // 16-byte pieces of a row's codes
         uint4 kx[NV], vx[NV];
         uint32_t ks[NG / 2], vs[NG / 2];
-        while (ok && prompt_next(p, lane, it)) {
+        while (ok && prompt_next<EXT>(p, lane, it)) {
             auto load = [&](int tile, uint4 (&kc)[NV], uint32_t (&kst)[NG / 2], uint4 (&vc)[NV], uint32_t (&vst)[NG / 2]) {
                 const int key = tile * kPromptTile + r;
                 if (key < it.len) {
@@ -720,7 +776,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     for (int i = 0; i < NG / 2; ++i) kst[i] = vst[i] = 0u;
                 }
             };
-            load(it.t0, kx, ks, vx, vs);
+            auto tile = [&](int i) { return EXT ? kv_part(it.t0 + i, it.hole, it.jump) : it.t0 + i; };
+            load(tile(0), kx, ks, vx, vs);
             const bool fine = it.fine != 0;
             for (int i = 0; i < it.n; ++i, ++kt) {
                 const int slot = kt & 1;
@@ -737,9 +794,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     kst[i2] = ks[i2];
                     vst[i2] = vs[i2];
                 }
-                if (i + 1 < it.n) load(it.t0 + i + 1, kx, ks, vx, vs);
+                if (i + 1 < it.n) load(tile(i + 1), kx, ks, vx, vs);
                 // what is out of the ordinary
-                const int rr = ((it.t0 + i) * kPromptTile + r) & (page - 1);
+                const int rr = (tile(i) * kPromptTile + r) & (page - 1);
                 uint32_t fl = 0;
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
@@ -888,7 +945,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 }
             }
         };
-        while (ok && prompt_next(p, lane, it)) {
+        while (ok && prompt_next<EXT>(p, lane, it)) {
             for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
             ++items;
             if (!ok) break;
@@ -996,7 +1053,7 @@ inline PromptWs prompt_ws(int64_t grid, int64_t dp) {
     return w;
 }
 
-template <int DP>
+template <int DP, bool EXT = false>
 int launch_kv4_prompt(const Kv4AttnArgs &a, cudaStream_t stream) {
     PromptK p;
     p.a = a;
@@ -1009,7 +1066,7 @@ int launch_kv4_prompt(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.meta = reinterpret_cast<int4 *>(a.ws + w.meta);
     p.last = reinterpret_cast<int *>(a.ws + w.last);
     constexpr int smem = (int)sizeof(PromptSmem<DP>) + 128;
-    auto *f = kv4_prompt_kernel<DP>;
+    auto *f = kv4_prompt_kernel<DP, EXT>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kPromptThreads), smem, stream, p)) return rc;
     return launch_pdl(kv4_prompt_join_kernel<DP>, dim3((unsigned)grid, kPromptRows / kJoinRows), dim3(256), 0, stream, p);

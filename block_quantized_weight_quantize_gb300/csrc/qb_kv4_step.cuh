@@ -153,11 +153,27 @@ __device__ __forceinline__ void seq_units(const SeqInfo &q, int window, int &u0,
     u0 = first / U;
     nu = max(1, kv_parts(q.len, U) - u0);
 }
+// The same with sinks and trees: unit numbers u0 .. u0 + nu - 1, of which those below `jump` stand for the sinks'
+template <int U, bool EXT>
+__device__ __forceinline__ void seq_units(const SeqInfo &q, const Kv4AttnArgs &a, int &u0, int &nu, int &jump) {
+    if constexpr (EXT) {
+        const KvParts p = kv_sink_parts(kv4_first_lo(a, q.len, q.T, 0), a.sinks, U);
+        u0 = p.hole;
+        jump = p.jump;
+        nu = max(1, kv_parts(q.len, U) - u0);
+    } else {
+        seq_units<U>(q, a.window, u0, nu);
+        jump = 0;
+    }
+}
 
 // A place in the call's work: sequence, key head, row tile, unit of the key axis.
 struct StepPos {
     int s, kvh, rt, u, u_end;  // u counts from the sequence's first key
     int row, len;
+    int hole, jump;            // EXT: units below `jump` are numbered from `hole` on
+    template <bool EXT>
+    __device__ __forceinline__ int unit() const { return EXT ? kv_part(u, hole, jump) : u; }
 };
 
 // Sequence s: from the warp's table (those from `base` on), else from memory.
@@ -167,20 +183,24 @@ __device__ __forceinline__ SeqInfo step_seq(const StepK &p, const SeqInfo *tab, 
 }
 
 // Enters the first sequence from x.s on that has new tokens.
-template <int U>
+template <int U, bool EXT>
 __device__ __forceinline__ SeqInfo step_enter(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
     SeqInfo q = step_seq(p, tab, base, x.s);
     while (q.T == 0 && x.s < p.a.s.nseq) q = step_seq(p, tab, base, ++x.s);
-    int nu;
-    seq_units<U>(q, p.a.window, x.u, nu);
+    int nu, jump;
+    seq_units<U, EXT>(q, p.a, x.u, nu, jump);
     x.u_end = x.u + nu;
+    if constexpr (EXT) {
+        x.hole = x.u;
+        x.jump = jump;
+    }
     x.row = q.row;
     x.len = q.len;
     return q;
 }
 
 // The item after the one that x is in; u at its beginning.
-template <int R, int U>
+template <int R, int U, bool EXT>
 __device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, int base, StepPos &x) {
     const SeqInfo q = step_seq(p, tab, base, x.s);
     if (++x.rt == (q.T * p.grp + R - 1) / R) {
@@ -190,7 +210,7 @@ __device__ __forceinline__ void step_item(const StepK &p, const SeqInfo *tab, in
             ++x.s;
         }
     }
-    step_enter<U>(p, tab, base, x);
+    step_enter<U, EXT>(p, tab, base, x);
 }
 
 // A joined row: E elements a lane from el on, over the sum, to (tok, head); lane 0 its lse.
@@ -210,7 +230,8 @@ __device__ __forceinline__ void step_store(const StepK &p, const float (&acc)[E]
     if (lane == 0 && p.a.lse) p.a.lse[(int64_t)tok * p.a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int DP, bool PAIR, bool LOW, int SB>
+// EXT: a call with sinks or trees (the same code but for which units an item has and which of their keys a row sees)
+template <int DP, bool PAIR, bool LOW, int SB, bool EXT>
 __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const StepK p) {
     constexpr int kWarps = step_warps(DP), kStages = step_stages(DP);
     constexpr int U = kUnit, kBytes = step_unit_bytes(DP), NB = U / 16;
@@ -251,8 +272,8 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
     };
     auto weight = [&](const SeqInfo &q) {
         Weight w;
-        int u0;
-        seq_units<U>(q, p.a.window, u0, w.nu);
+        int u0, jump;
+        seq_units<U, EXT>(q, p.a, u0, w.nu, jump);
         w.nrt = (q.T * p.grp + R - 1) / R;
         w.n = (long long)p.a.c.nkv * w.nrt * (w.nu + kItemCost);
         return w;
@@ -349,7 +370,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         cur.s = f.s;
         cur.kvh = f.item / f.nrt;
         cur.rt = f.item - cur.kvh * f.nrt;
-        step_enter<U>(p, tab, base, cur);
+        step_enter<U, EXT>(p, tab, base, cur);
         cur.u += max(0, f.at - kItemCost);
         place = max(0, kItemCost - f.at);
     }
@@ -378,7 +399,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
     // page numbers of the sequence at `ahead`: lane l has the one of page pbase + l
     int pbase = 0, pcache = 0;
     auto find_pages = [&](bool fresh) {
-        const int pi = (ahead.u * U) >> p.a.c.pshift;
+        const int pi = (ahead.unit<EXT>() * U) >> p.a.c.pshift;
         if (!fresh && pi + 3 < pbase + 32) return;  // a unit has four pages at most
         pbase = pi;
         pcache = 0;
@@ -406,13 +427,14 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
     int islot = 0;
     auto issue = [&]() {
         if (place_ahead < count) {
-            const int pg = __shfl_sync(0xFFFFFFFFu, pcache, ((ahead.u * U + sub_key) >> p.a.c.pshift) - pbase);
+            const int au = ahead.unit<EXT>();
+            const int pg = __shfl_sync(0xFFFFFFFFu, pcache, ((au * U + sub_key) >> p.a.c.pshift) - pbase);
             if (nbytes) {  // each lane announces and issues its own piece
-                if (ahead.u * U + sub_key < ahead.len) {
+                if (au * U + sub_key < ahead.len) {
                     mbar_arrive_expect_tx(full + islot, (uint32_t)nbytes);
                     bulk_g2s(ring + islot * kBytes + dst_off,
                              src + ((int64_t)pg * p.a.c.nkv + ahead.kvh) * p.a.c.block_bytes +
-                                 ((ahead.u & 1) ? half_mul : 0),
+                                 ((au & 1) ? half_mul : 0),
                              (uint32_t)nbytes, full + islot);
                 } else {
                     mbar_arrive(full + islot);
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             }
             ++place_ahead;
             if (++ahead.u == ahead.u_end) {
-                step_item<R, U>(p, tab, base, ahead);
+                step_item<R, U, EXT>(p, tab, base, ahead);
                 place_ahead += kItemCost;
                 if (place_ahead < count) {
                     find_pages(true);
@@ -453,8 +475,8 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         const int s_kvh = cur.kvh, s_rt = cur.rt, s_len = cur.len;
         const SeqInfo sq = step_seq(p, tab, base, cur.s);
         const int s_q0 = sq.q0, s_T = sq.T;
-        int u0, nu;
-        seq_units<U>(sq, p.a.window, u0, nu);
+        int u0, nu, jump;
+        seq_units<U, EXT>(sq, p.a, u0, nu, jump);
         const bool from_start = cur.u == u0;
         const int item_left = cur.u_end - cur.u;  // units of the item from here on
         const int units = min(item_left, count - place);
@@ -540,10 +562,20 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
             }
         }
         // units whose keys every row sees need no mask
-        const int pos_lo = s_len - s_T + (s_rt * R) / p.grp;
-        const int pos_hi = s_len - s_T + min(s_T - 1, (s_rt * R + R - 1) / p.grp);
-        const int first_hi = kv_first_seen(pos_hi, p.a.window);
-        const int first_lo = kv_first_seen(pos_lo, p.a.window);
+        const int j_lo = (s_rt * R) / p.grp, j_hi = min(s_T - 1, (s_rt * R + R - 1) / p.grp);
+        const int pos_lo = EXT ? kv4_pos_lo(p.a, s_len, s_T, j_lo) : s_len - s_T + j_lo;
+        const int pos_hi = EXT ? kv4_pos_hi(p.a, s_len, s_T, j_hi) : s_len - s_T + j_hi;
+        const int first_hi = EXT ? kv4_first_hi(p.a, s_len, s_T, j_hi) : kv_first_seen(pos_hi, p.a.window);
+        const int first_lo = EXT ? kv4_first_lo(p.a, s_len, s_T, j_lo) : kv_first_seen(pos_lo, p.a.window);
+        [[maybe_unused]] KvSight sight[NH];
+        if constexpr (EXT) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const int jr = (s_rt * R + (PAIR ? t : 2 * t + h)) / p.grp;
+                sight[h] = KvSight{0, -1, kKvNoKey};
+                if (jr < s_T) sight[h] = kv4_sight(p.a, s_len, s_T, s_q0, jr);
+            }
+        }
 
         float O[NG][2][4];
         float m[NH], l[NH];
@@ -625,13 +657,20 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     const int j = (s_rt * R + (PAIR ? t : 2 * t + h)) / p.grp;
-                    const int pos = j < s_T ? s_len - s_T + j : -1;
-                    const int first = kv_first_seen(pos, p.a.window);
-                    seen[h] = 0;
+                    if constexpr (EXT) {
+                        // of the unit's 32 keys those of this lane, krow + 8 k, as bit k: bits 0, 8, 16, 24 to 24..27
+                        const uint32_t w = j < s_T ? kv4_seen(p.a, sight[h], s_len, s_T, s_q0, j, k0) : 0u;
+                        static_assert(U == 32, "a word of seen keys a unit");
+                        seen[h] = ((w >> krow & 0x01010101u) * 0x01020408u) >> 24 & 15u;
+                    } else {
+                        const int pos = j < s_T ? s_len - s_T + j : -1;
+                        const int first = kv_first_seen(pos, p.a.window);
+                        seen[h] = 0;
 #pragma unroll
-                    for (int k = 0; k < 2 * NB; ++k) {
-                        const int key = k0 + 8 * k + krow;
-                        if (key >= first && key <= pos) seen[h] |= 1u << k;
+                        for (int k = 0; k < 2 * NB; ++k) {
+                            const int key = k0 + 8 * k + krow;
+                            if (key >= first && key <= pos) seen[h] |= 1u << k;
+                        }
                     }
                 }
             }
@@ -775,7 +814,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         };
 
         for (int u = cur.u; u < cur.u + units; ++u) {
-            const int k0 = u * U;
+            const int k0 = (EXT ? kv_part(u, cur.hole, cur.jump) : u) * U;
             const bool landed = mbar_wait_bounded(full + slot, phase, p.a.fault);
             if (!__all_sync(0xFFFFFFFFu, landed)) {  // a copy never completed: fault word raised
                 failed = 1;
@@ -784,9 +823,9 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
                 break;
             }
             const uint8_t *ub = ring + slot * kBytes;
-            if (k0 > pos_hi || k0 <= first_lo - U)
+            if (k0 > pos_hi || (k0 <= first_lo - U && (!EXT || k0 >= p.a.sinks)))
                 ;  // no row sees it: the sequence's other row tiles do
-            else if (k0 + U - 1 > pos_lo || k0 < first_hi)
+            else if (k0 + U - 1 > pos_lo || (k0 < first_hi && (!EXT || k0 + U > p.a.sinks)))
                 unit(ub, k0, std::true_type());
             else
                 unit(ub, k0, std::false_type());
@@ -855,7 +894,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
         }
         place += units;
         if (to_end) {
-            step_item<R, U>(p, tab, base, cur);
+            step_item<R, U, EXT>(p, tab, base, cur);
             place += kItemCost;
         } else {
             cur.u += units;
@@ -866,7 +905,7 @@ __global__ void __launch_bounds__(step_warps(DP) * 32, 1) kv4_step_kernel(const 
     if (count < 0) {
 #pragma unroll 1
         for (int i = 1; i < kStages; ++i) {
-            if (++cur.u == cur.u_end) step_item<R, U>(p, tab, base, cur);
+            if (++cur.u == cur.u_end) step_item<R, U, EXT>(p, tab, base, cur);
             if (cur.u == ahead.u && cur.rt == ahead.rt && cur.kvh == ahead.kvh && cur.s == ahead.s) break;
             slot = slot + 1 == kStages ? 0 : slot + 1;
             phase ^= slot == 0 ? 1u : 0u;
@@ -1035,7 +1074,7 @@ constexpr int kNoSplitKeys = 256;
 // bf16: 12.4, 12.7, 13.3 us; one on 600: 11.9, 11.7, 12.0).
 constexpr int kMinShareKeys = 128;
 
-template <int DP, bool PAIR, bool LOW, int SB>
+template <int DP, bool PAIR, bool LOW, int SB, bool EXT>
 static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     constexpr int kWarps = step_warps(DP), R = step_rows(PAIR);
     constexpr int smem = kWarps * step_stages(DP) * step_unit_bytes(DP);
@@ -1047,14 +1086,14 @@ static int launch_step_k(StepK &p, int grid, cudaStream_t stream) {
     p.cstat = reinterpret_cast<float2 *>(p.a.ws + w.cstat);
     p.last = reinterpret_cast<int *>(p.a.ws + w.last);
     p.meta = reinterpret_cast<int4 *>(p.a.ws + w.meta);
-    auto *f = kv4_step_kernel<DP, PAIR, LOW, SB>;
+    auto *f = kv4_step_kernel<DP, PAIR, LOW, SB, EXT>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p)) return rc;
     if (p.nosplit) return QB_OK;
     return launch_pdl(kv4_combine_kernel<DP, R>, dim3((unsigned)grid), dim3(256), 0, stream, p, grid);
 }
 
-template <int DP>
+template <int DP, bool EXT = false>
 int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     StepK p = {};
     p.a = a;
@@ -1072,10 +1111,10 @@ int launch_kv4_step(const Kv4AttnArgs &a, cudaStream_t stream) {
     // 180 in f32.)
     const bool low = a.type == QB_T_F32, few = a.ntok * p.grp <= (low ? 8 : 4) * (int64_t)a.s.nseq;
     if (a.c.page == 16)
-        return few ? launch_step_k<DP, true, false, 16>(p, grid, stream)
-               : low ? launch_step_k<DP, false, true, 16>(p, grid, stream) : launch_step_k<DP, false, false, 16>(p, grid, stream);
-    return few ? launch_step_k<DP, true, false, 32>(p, grid, stream)
-           : low ? launch_step_k<DP, false, true, 32>(p, grid, stream) : launch_step_k<DP, false, false, 32>(p, grid, stream);
+        return few ? launch_step_k<DP, true, false, 16, EXT>(p, grid, stream)
+               : low ? launch_step_k<DP, false, true, 16, EXT>(p, grid, stream) : launch_step_k<DP, false, false, 16, EXT>(p, grid, stream);
+    return few ? launch_step_k<DP, true, false, 32, EXT>(p, grid, stream)
+           : low ? launch_step_k<DP, false, true, 32, EXT>(p, grid, stream) : launch_step_k<DP, false, false, 32, EXT>(p, grid, stream);
 }
 
 }  // namespace qb

@@ -14,16 +14,9 @@
 #include <cstdint>
 
 #include "qb_kv4.cuh"
+#include "qb_kv_plan.cuh"
 
 namespace qb {
-
-constexpr int kPlanThreads = 1024;
-
-struct PagesK {
-    int32_t *nfree, *free_pages, *refs, *lens, *tables;
-    int page, npages, nrows, maxp;
-    int *fault;
-};
 
 // workspace: [0] pairs listed, [1] pages held (compact); then src, dst, map
 struct PlanWs {
@@ -40,37 +33,6 @@ static PlanWs plan_ws(void *ws, int npages, int nrows) {
     w.dst = w.src + plan_pairs(npages, nrows);
     w.map = w.dst + plan_pairs(npages, nrows);
     return w;
-}
-
-static PagesK pages_k(const qb_kv_pages &p) {
-    return PagesK{p.nfree, p.free_pages, p.refs, p.lens, p.tables, p.page, p.npages, p.nrows, p.maxp, fault_word()};
-}
-
-// Exclusive prefix sum of x over the block's threads, and the total; red has 33 entries.
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T *red, T &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();  // red of an earlier scan has been read
-    if (lane == 31) red[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-        T y = red[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const T z = __shfl_up_sync(0xFFFFFFFFu, y, o);
-            if (lane >= o) y += z;
-        }
-        red[lane] = y;
-    }
-    __syncthreads();
-    total = red[31];
-    return s - x + (warp ? red[warp - 1] : T(0));
 }
 
 // ---------------------------------------------------------------- reset
@@ -299,18 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_free_kernel(const Pages
         if (lane == 0) p.lens[row] = 0;
     }
     __syncthreads();
-    // the freed pages in ascending order
-    const int per = (words + kPlanThreads - 1) / kPlanThreads, w0 = min(tid * per, words), w1 = min(w0 + per, words);
-    int cnt = 0;
-    for (int i = w0; i < w1; ++i) cnt += __popc(freed[i]);
-    int total;
-    int at = nfree + block_scan(cnt, red, total);
-    for (int i = w0; i < w1; ++i)
-        for (uint32_t b = freed[i]; b; b &= b - 1) {
-            if (at < p.npages) p.free_pages[at] = i * 32 + __ffs(b) - 1;
-            ++at;
-        }
-    if (tid == 0) p.nfree[0] = min(nfree + total, p.npages);
+    give_back(p, freed, words, nfree, red);
 }
 
 // ---------------------------------------------------------------- compact

@@ -1,5 +1,6 @@
 """Binding of the paged 4-bit key/value cache: rows in and out, attention over
-it, and its pages (``kv4_*`` and ``kv_pages_*`` of ``include/qgemv.h``).
+it, and its pages (``kv4_*`` and ``kv_pages_*`` of ``include/qgemv.h``); drafted
+trees over it (``kv_tree_*``) and log probabilities (``q_logprobs``).
 
 A cache, its sequences and its pages are small handles made once; each call
 marshals pointers and raises on a non-zero status.  Tensors keep the layouts
@@ -42,6 +43,12 @@ _SIGNATURES = {
     "kv4_read": ([_P, _I, _P, _L, _P, _L, _P, _L, _P], _I),
     "kv4_attn_workspace_bytes": ([_P, _I], _L),
     "kv4_attn": ([_P, _P, _I, _P, _L, _L, _I, ctypes.c_float, _I, _P, _L, _P, _P, ctypes.c_size_t, _P], _I),
+    "kv4_attn_sinks": ([_P, _P, _I, _P, _L, _L, _I, ctypes.c_float, _I, _I, _P, _L, _P, _P, ctypes.c_size_t, _P], _I),
+    "kv4_attn_tree": ([_P, _P, _I, _P, _L, _L, _I, ctypes.c_float, _I, _I, _P, _I, _P, _L, _P, _P, ctypes.c_size_t, _P], _I),
+    "kv_tree_masks": ([_P, _L, _P, _I, _P, _I, _P, _P], _I),
+    "kv_tree_accept": ([_P, _P, _P, _L, _P, _I, _P, _P, _P, _P], _I),
+    "q_logprobs": ([_I, _P, _L, _L, _L, ctypes.c_float, _P, _I, _P, _P, _P, _I, _P, _P, _P], _I),
+    "kv4_keep": ([_P, _P, _I, _I, _I, _P, _P, _P, _P, _L, _I, _P, _P], _I),
     "kv_pages_workspace_bytes": ([_P], _L),
     "kv_pages_reset": ([_P, _P], _I),
     "kv_pages_extend": ([_P, _P, _P, _I, _P, _L, _P, _P], _I),
@@ -211,10 +218,7 @@ def kv4_attn_workspace_bytes(cache: Kv4, q, seqs: KvSeqs = None) -> int:
     return _bytes(_c.kv4_attn_workspace_bytes(cache.ref, q.shape[1]), "kv4_attn_workspace_bytes")
 
 
-def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: int = 0, workspace=None,
-             stream=None) -> None:
-    """Causal attention of the new tokens q [ntok, nh, d] over the cache: out like q, lse f32 [ntok, nh] (optional);
-    window > 0: only the last `window` keys.  workspace: uint8, kv4_attn_workspace_bytes long (allocated here when None)."""
+def _attn(call, more, cache: Kv4, q, seqs: KvSeqs, scale, window, out, lse, workspace, stream, where: str) -> None:
     nh, dev = q.shape[1], cache.dev
     if seqs.dev != dev:
         raise ValueError(f"seqs: on cuda:{seqs.dev}, where the cache is on cuda:{dev}")
@@ -229,9 +233,96 @@ def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: i
             raise ValueError("lse: [ntok, nh] expected")
     if workspace is None:
         workspace = _workspace(kv4_attn_workspace_bytes(cache, q), q, stream)
-    _check(_c.kv4_attn(cache.ref, seqs.ref, _TYPE[q.dtype], qp, qs, q.shape[0], nh, scale, window, op, os_, lp,
-                       _dev(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
-                       _stream(stream, dev)), "kv4_attn")
+    _check(call(cache.ref, seqs.ref, _TYPE[q.dtype], qp, qs, q.shape[0], nh, scale, window, *more, op, os_, lp,
+                _dev(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
+                _stream(stream, dev)), where)
+
+
+def kv4_attn(cache: Kv4, q, seqs: KvSeqs, scale: float, out, lse=None, window: int = 0, workspace=None,
+             stream=None) -> None:
+    """Causal attention of the new tokens q [ntok, nh, d] over the cache: out like q, lse f32 [ntok, nh] (optional);
+    window > 0: only the last `window` keys.  workspace: uint8, kv4_attn_workspace_bytes long (allocated here when None)."""
+    _attn(_c.kv4_attn, (), cache, q, seqs, scale, window, out, lse, workspace, stream, "kv4_attn")
+
+
+def kv4_attn_sinks(cache: Kv4, q, seqs: KvSeqs, scale: float, out, window: int, sinks: int, lse=None, workspace=None,
+                   stream=None) -> None:
+    """kv4_attn where a token sees the last `window` keys and, of those before them, the sequence's first `sinks`."""
+    _attn(_c.kv4_attn_sinks, (sinks,), cache, q, seqs, scale, window, out, lse, workspace, stream, "kv4_attn_sinks")
+
+
+def kv4_attn_tree(cache: Kv4, q, seqs: KvSeqs, masks, scale: float, out, lse=None, window: int = 0, sinks: int = 0,
+                  workspace=None, stream=None) -> None:
+    """kv4_attn over drafted trees: masks int32 [ntok, words], bit i % 32 of word i / 32: the token sees draft i of its
+    sequence (kv_tree_masks); a token's window is over the keys before the drafts and its marked drafts."""
+    if masks.dim() != 2 or masks.shape[0] != q.shape[0]:
+        raise ValueError("masks: [ntok, words] expected")
+    more = (sinks, _dev(masks, torch.int32, "masks", cache.dev), masks.shape[1])
+    _attn(_c.kv4_attn_tree, more, cache, q, seqs, scale, window, out, lse, workspace, stream, "kv4_attn_tree")
+
+
+# ------------------------------------------------------------------ drafted trees, log probabilities
+
+def _tree(parents, q_start):
+    """Device, tokens, address of q_start and sequences of a tree call."""
+    n, dev = parents.numel(), _on(parents, "parents")
+    if q_start is None:
+        return dev, n, None, n
+    if q_start.numel() < 1:
+        raise ValueError("q_start: nseq + 1 entries expected")
+    return dev, n, _dev(q_start, torch.int32, "q_start", dev), q_start.numel() - 1
+
+
+def kv_tree_masks(parents, masks, depth=None, q_start=None, stream=None) -> None:
+    """parents int32 [ntok] (the number of the draft that a token follows, within its sequence; -1: none) -> masks int32
+    [ntok, words] for kv4_attn_tree and depth int32 [ntok] (optional); q_start int32 [nseq + 1] bounds the sequences."""
+    i32, (dev, n, sp, nseq) = torch.int32, _tree(parents, q_start)
+    if masks.dim() != 2 or masks.shape[0] != n or (depth is not None and depth.numel() != n):
+        raise ValueError("masks [ntok, words], depth [ntok] expected")
+    _check(_c.kv_tree_masks(_dev(parents, i32, "parents", dev), n, sp, nseq, _dev(masks, i32, "masks", dev), masks.shape[1],
+                            None if depth is None else _dev(depth, i32, "depth", dev), _stream(stream, dev)), "kv_tree_masks")
+
+
+def kv_tree_accept(parents, tokens, targets, keep, nkeep, next, q_start=None, stream=None) -> None:
+    """The path that the target's choices take through each tree: keep int32 [ntok] (accepted drafts' numbers, then -1),
+    nkeep and next int32 [nseq] (how many, and the target's token after the last)."""
+    i32, (dev, n, sp, nseq) = torch.int32, _tree(parents, q_start)
+    if tokens.numel() != n or targets.numel() != n or keep.numel() != n or nkeep.numel() != nseq or next.numel() != nseq:
+        raise ValueError("tokens, targets, keep [ntok], nkeep, next [nseq] expected")
+    _check(_c.kv_tree_accept(_dev(parents, i32, "parents", dev), _dev(tokens, i32, "tokens", dev), _dev(targets, i32, "targets", dev),
+                             n, sp, nseq, _dev(keep, i32, "keep", dev), _dev(nkeep, i32, "nkeep", dev), _dev(next, i32, "next", dev),
+                             _stream(stream, dev)), "kv_tree_accept")
+
+
+def q_logprobs(logits, tokens=None, scale: float = 1.0, logprobs=None, entropy=None, lse=None, top_tokens=None, top_logprobs=None,
+               stream=None) -> None:
+    """From logits [n, vocab] (float32, float16 or bfloat16; rows contiguous) times `scale`: logprobs f32 [n, m] of tokens
+    int32 [n, m], entropy and lse f32 [n], the k largest logits' places top_tokens int32 [n, k] and log probabilities
+    top_logprobs f32 [n, k].  What is None is not computed."""
+    f32, dev = torch.float32, _on(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in _TYPE or logits.stride(1) != 1 and logits.shape[1] != 1:
+        raise ValueError("logits: float32, float16 or bfloat16 [n, vocab] with contiguous rows expected")
+    n, vocab = logits.shape
+    m = k = 0
+    tp = lp = None
+    if tokens is not None:
+        if logprobs is None or tokens.dim() != 2 or tokens.shape[0] != n or logprobs.shape != tokens.shape:
+            raise ValueError("tokens and logprobs: [n, m] expected")
+        m, tp, lp = tokens.shape[1], _dev(tokens, torch.int32, "tokens", dev), _dev(logprobs, f32, "logprobs", dev)
+    elif logprobs is not None:
+        raise ValueError("logprobs: of which tokens?")
+    for t, what in ((entropy, "entropy"), (lse, "lse")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what}: [n] expected")
+    for t in (top_tokens, top_logprobs):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] != n or k and t.shape[1] != k:
+                raise ValueError("top_tokens, top_logprobs: [n, k] expected")
+            k = t.shape[1]
+    _check(_c.q_logprobs(_TYPE[logits.dtype], logits.data_ptr(), logits.stride(0) if n > 1 else vocab, n, vocab, scale, tp, m, lp,
+                         None if entropy is None else _dev(entropy, f32, "entropy", dev), None if lse is None else _dev(lse, f32, "lse", dev), k,
+                         None if top_tokens is None else _dev(top_tokens, torch.int32, "top_tokens", dev),
+                         None if top_logprobs is None else _dev(top_logprobs, f32, "top_logprobs", dev), _stream(stream, dev)), "q_logprobs")
 
 
 # ------------------------------------------------------------------ pages
@@ -288,6 +379,21 @@ def kv_pages_free(pages: KvPages, rows, stream=None) -> None:
     """Sequences rows (int32) become empty; pages nobody holds go back to the stack."""
     _check(_c.kv_pages_free(pages.ref, _dev(rows, torch.int32, "rows", pages.dev), rows.numel(), _stream(stream, pages.dev)),
            "kv_pages_free")
+
+
+def kv4_keep(pages: KvPages, data, nkv: int, d: int, rows, q_start, keep, nkeep, status, stream=None) -> None:
+    """Of sequence rows[i]'s last q_start[i + 1] - q_start[i] tokens those numbered keep[q_start[i]:][:nkeep[i]] (ascending)
+    stay: their rows in every layer of data [layers, npages, ...] (4-bit caches of nkv heads of d) move together, the length
+    is lowered, pages past it are given back.  rows None: sequence i.  All int32 device tensors (kv_tree_accept's)."""
+    i32, n, dev = torch.int32, nkeep.numel(), pages.dev
+    if q_start.numel() != n + 1 or status.numel() < n or (rows is not None and rows.numel() != n):
+        raise ValueError("rows, nkeep, status: one entry a request, q_start one more, expected")
+    dp, layers, pb = _pool(data, pages.c.npages, dev)
+    if pb != nkv * kv4_block_bytes(pages.page, d):
+        raise ValueError(f"data: pages of {nkv * kv4_block_bytes(pages.page, d)} bytes expected, got {pb}")
+    _check(_c.kv4_keep(pages.ref, dp, layers, nkv, d, None if rows is None else _dev(rows, i32, "rows", dev),
+                       _dev(q_start, i32, "q_start", dev), _dev(keep, i32, "keep", dev), _dev(nkeep, i32, "nkeep", dev), keep.numel(), n,
+                       _dev(status, i32, "status", dev), _stream(stream, dev)), "kv4_keep")
 
 
 def kv_pages_compact(pages: KvPages, data, workspace=None, stream=None) -> None:

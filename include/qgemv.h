@@ -514,6 +514,74 @@ QB_API int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, c
                     int64_t ntok, int nh, float scale, int window, void *out, int64_t out_stride, float *lse,
                     void *workspace, size_t workspace_bytes, void *stream);
 
+/* kv4_attn with sinks: with window > 0 a token sees the last `window` keys up
+ * to its own place and, of those before them, the sequence's first `sinks`
+ * (sinks >= 0; more than there are: all).  window 0: every key up to its place,
+ * whatever sinks is.  All else as kv4_attn (with no sinks its very results);
+ * keys that no token of a call sees are not read. */
+QB_API int kv4_attn_sinks(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void *q, int64_t q_stride,
+                          int64_t ntok, int nh, float scale, int window, int sinks, void *out, int64_t out_stride,
+                          float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* kv4_attn over drafted trees.  The new tokens of a sequence, its last keys, are
+ * drafts 0, 1, .. of it; masks [ntok][mask_words] says which of them a token
+ * sees: bit i % 32 of its word i / 32 is draft i (its ancestors and itself, as
+ * kv_tree_masks writes them, though any marks will do).  A token's keys in order
+ * are those before the drafts and its marked drafts; with window > 0 it sees the
+ * last `window` of these and, of the rest, those among the sequence's first
+ * `sinks` keys.  Marks of drafts that there are not, or that have no key (in a
+ * sequence shorter than its new tokens), say nothing; drafts past
+ * 32 * mask_words are seen by no token.  1 <= mask_words <= 32. */
+QB_API int kv4_attn_tree(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void *q, int64_t q_stride,
+                         int64_t ntok, int nh, float scale, int window, int sinks, const uint32_t *masks,
+                         int mask_words, void *out, int64_t out_stride, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* ---- Drafted trees: a sequence's drafts are tokens q_start[s] ..
+ * q_start[s+1]-1 of the call's ntok (q_start NULL: the one token s), and
+ * parents[j] is the number, within its sequence, of the draft that token j
+ * follows, or -1; a parent's number is lower than its child's (another is
+ * reported by q_device_status and counts as -1).  ntok <= 2^24, nseq <= 2^20. */
+
+/* masks [ntok][mask_words]: each draft's ancestors and itself, as kv4_attn_tree
+ * takes them (1 <= mask_words <= 32; drafts past 32 * mask_words in no mask);
+ * depth [ntok]: how many ancestors it has (NULL: not wanted). */
+QB_API int kv_tree_masks(const int32_t *parents, int64_t ntok, const int32_t *q_start, int nseq, uint32_t *masks,
+                         int mask_words, int32_t *depth, void *stream);
+
+/* The path that a target model takes through each tree.  tokens [ntok]: the
+ * drafts' tokens; targets [ntok]: the token that the target chose after each
+ * draft.  Draft 0 is accepted (the token that was chosen before); after an
+ * accepted draft its child whose token the target chose (the lowest-numbered
+ * one), until there is none.  keep [ntok]: the accepted drafts' numbers at the
+ * sequence's first places, then -1; nkeep [nseq]: how many; next [nseq]: the
+ * target's token after the last of them (a sequence without drafts: 0 and -1). */
+QB_API int kv_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *targets, int64_t ntok,
+                          const int32_t *q_start, int nseq, int32_t *keep, int32_t *nkeep, int32_t *next,
+                          void *stream);
+
+/* ---- Log probabilities. */
+
+#define QB_MAX_ALTERNATIVES 64
+#define QB_MAX_GIVEN 1024
+
+/* From n rows of logits x (row i at logits + i*row_stride, elements of `type`,
+ * vocab of them, at any alignment of their own size) with z = scale * x:
+ *     lse [n] = log sum exp(z),  entropy [n] = lse - sum z exp(z - lse),
+ *     logprobs [n][ngiven] = z - lse at tokens [n][ngiven],
+ *     top_tokens, top_logprobs [n][k]: the k largest logits' places, the largest
+ *     first and the lower place first where two are equal, and their z - lse.
+ * Any output may be NULL (logprobs where ngiven is 0).  A logit of -infinity has
+ * probability 0 and log probability -infinity, as has a given token outside
+ * 0..vocab-1; a row of them alone has lse -infinity and entropy 0.  A row with a
+ * NaN or +infinity has no distribution: its values are NaN, its top_tokens -1.
+ * Sums are f32.  1 <= vocab <= 2^24, n <= 2^26, 0 <= ngiven <= QB_MAX_GIVEN,
+ * 0 <= k <= QB_MAX_ALTERNATIVES, k <= vocab, 2^-20 <= scale <= 2^20.  One
+ * launch, no workspace. */
+QB_API int q_logprobs(qb_type type, const void *logits, int64_t row_stride, int64_t n, int64_t vocab, float scale,
+                      const int32_t *tokens, int ngiven, float *logprobs, float *entropy, float *lse, int k,
+                      int32_t *top_tokens, float *top_logprobs, void *stream);
+
 /* ---- The pages of a cache: who holds which.
  *
  * A pool of npages pages serves nrows sequences; its state is device memory:
@@ -522,8 +590,8 @@ QB_API int kv4_attn(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, c
  * each sequence its length lens[nrows] and its table row
  * tables[nrows][maxp]: ceil(len/page) page numbers, then -1.  A page held
  * more than once is full.  Lengths and table rows are changed by the calls
- * below alone: a length lowered by hand loses the pages past it, and no call
- * takes tokens back.  The pages' bytes are opaque here: any cache laid
+ * below alone (a length lowered by hand loses the pages past it; kv4_keep takes
+ * tokens back).  The pages' bytes are opaque here: any cache laid
  * out [layers][npages][page_bytes] can use these calls, page_bytes % 16 == 0.
  * npages <= 2^20.  Every call is asynchronous on stream and gives the same
  * state whatever the order its threads run in.  Sequence numbers
@@ -568,6 +636,20 @@ QB_API int kv_pages_fork(const qb_kv_pages *pages, void *data, int nlayers, int6
 /* Sequences rows[i], i < n (distinct), become empty; pages that nobody holds
  * any more go back to the stack in ascending order. */
 QB_API int kv_pages_free(const qb_kv_pages *pages, const int32_t *rows, int n, void *stream);
+
+/* Of sequence rows[i]'s drafts (its last q_start[i+1] - q_start[i] tokens), i < n
+ * (rows distinct; NULL: rows[i] = i), those numbered keep[q_start[i]] ..
+ * keep[q_start[i] + nkeep[i] - 1] (ascending) stay: their rows, keys and values of
+ * every head and layer, move together behind the tokens before the drafts, the
+ * others are forgotten, the length is lowered and pages past it are given back as
+ * by kv_pages_free.  data: 4-bit caches [nlayers][npages] of pages->page tokens of
+ * nkv heads of d.  keep has ntok entries.  status[i]: QB_OK, or QB_E_ARG and
+ * nothing of the request done: keep not ascending within the drafts, more drafts
+ * than tokens, or a page that would hold kept drafts, or be left partly filled,
+ * held more than once (unless all drafts stay).  Two launches, no workspace. */
+QB_API int kv4_keep(const qb_kv_pages *pages, void *data, int nlayers, int nkv, int d, const int32_t *rows,
+                    const int32_t *q_start, const int32_t *keep, const int32_t *nkeep, int64_t ntok, int n,
+                    int32_t *status, void *stream);
 
 /* Moves the pool together: with U pages held, the i-th held page from U up
  * (ascending) is moved, in every layer of data, to the i-th free page below U;
