@@ -1,21 +1,31 @@
 // qb_logprobs.cu -- log probabilities of given tokens, entropy and the largest alternatives of rows of
 // logits (qgemv.h: q_logprobs).
 //
-// Mathematics.  With z = scale * x, X a row's largest logit and, over the row,
-//     S = sum 2^d, T = sum d 2^d,  d = (x - X) * scale * log2(e),
-// lse = scale X + ln S, log p(x) = scale (x - X) - ln S, and the entropy is ln S - ln(2) T / S: one pass
-// gives all of it.  A thread's d is relative to a reference of its own that follows its largest element
-// when that is more than 2^kLazy above it, so that a rescaling is rare; differences of
-// logits are formed before they are scaled, so that rows of the type's lowest values have the
-// uniform distribution that they stand for.
+// Mathematics.  With d = (scale x - M) log2(e) and, over a row, S = sum 2^d, T = sum d 2^d, the log of the
+// sum is M + ln S and the entropy ln S - ln(2) T / S: one pass gives all of it.  A thread's M is a
+// whole number (in units of log 2) that follows its largest element when that is kLpLazy above it, so
+// that a rescaling is rare and exact; in the end all sums are taken relative to the row's largest logit
+// X, with the factors formed to twice f32's bits (an error of a factor is that of all it scales: the
+// entropy of a row of 49152 was off by 1.3e-6 of itself, 3e-7 now).  Where |scale x| passes kLpFar (rows
+// of the type's lowest value alone, which stand for the uniform distribution; logits of 10^30), the
+// block reads its part again and scales differences of logits.
 //
-// Alternatives.  A thread remembers its largest logit and where it lies.  The j-th largest of
-// these in a warp, j = ceil(k / warps), the least of the warps': at least k elements are as
-// large, few are larger, and only threads whose largest reaches it can hold one.  So the row's candidates are found
-// by reading those threads' elements once more (from L2), and ordered by counting.
+// Alternatives.  A thread remembers its largest logit, and the largest of each of up to kLpSlots parts of
+// its elements.  The k-th of the warps' largest threads (each as if it were the last element of its
+// place) is a lower bound of the k-th largest element; parts whose largest reaches it are read once
+// more (from L2), their elements that reach it ordered by counting.  (Reading all elements of such
+// threads instead: 3000 rows of 100000 in bf16, k = 20 158 us, 147 with the parts; k = 1 129, 137.)
 //
 // Work: a row is read by a cluster of 1 to 16 blocks, which join their sums and candidates in
-// the first one's shared memory: no workspace, one launch.
+// the first one's shared memory: no workspace, one launch.  Blocks go on to further rows, whose first
+// chunks are under way while a row is finished.  Three groups of two chunks of 16 bytes a thread
+// are in registers or under way: four blocks of 256 threads a multiprocessor (128 threads: the same for
+// k <= 1, 185 us for k = 20).  A block's shared memory is kept below 30 KB, as what it takes from the
+// first-level cache bounds the loads under way (50 KB: 152 us instead of 140).
+//
+// Measured: 3001 rows of 100003 in bf16 (600 MB), k = 3: 141 us, 4.3 TB/s; without alternatives 120.  In f32
+// 1500 rows of 100000: 118 us, 5.1 TB/s.  Instructions bound it in half precision (2.6 a cycle and
+// multiprocessor), latency where there are few rows: 64 rows of 128256 in f32, k = 20: 16.5 us.
 #include <algorithm>
 #include <cmath>
 #include <cooperative_groups.h>
@@ -28,9 +38,16 @@ namespace qb {
 namespace cg = cooperative_groups;
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpBlocks = 4;  // a multiprocessor
 constexpr int kLpMaxK = QB_MAX_ALTERNATIVES, kLpMaxCluster = 16;
-constexpr int kLpCand = 2048;    // candidates a block holds
-constexpr float kLpLazy = 32.0f; // 2^32 times 2^24 elements stay far below f32's top
+constexpr int kLpCand = 1024;    // candidates a block holds
+constexpr int kLpNth = kLpMaxK + 2 * kLpWarps;  // largest of the warps' threads, at the most
+constexpr int kLpGroup = 2, kLpAhead = 3;
+constexpr int kLpSlots = 8;     // parts of a thread's elements whose largest is remembered
+constexpr int kLpChosen = 1024;  // of these, as many are looked at again
+constexpr float kLpLazy = 32.0f;     // 2^32 times 2^24 elements stay far below f32's top
+constexpr float kLpFar = 0x1p22f;    // scaled logits up to here are whole numbers' neighbours
+constexpr float kLpFloor = -0x1p100f;  // what -infinity counts as: its probability is 0, and 0 times it 0
 
 struct LpK {
     const void *x;
@@ -44,6 +61,7 @@ struct LpK {
     int32_t *top_tok;
     float *top_logp;
     int cluster;
+    int shift;  // a part is 2^shift steps of a thread
 };
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -76,6 +94,12 @@ __device__ __forceinline__ void lp_unpack(const uint4 &u, float (&x)[lp_vec<TYPE
         unpack8<TYPE>(u, x);
     }
 }
+// A chunk of -infinity.
+template <int TYPE>
+__device__ __forceinline__ uint4 lp_nothing() {
+    const uint32_t w = TYPE == QB_T_F32 ? 0xFF800000u : TYPE == QB_T_F16 ? 0xFC00FC00u : 0xFF80FF80u;
+    return make_uint4(w, w, w, w);
+}
 template <int TYPE>
 __device__ __forceinline__ float lp_load(const void *row, int64_t i) {
     if constexpr (TYPE == QB_T_F32) return static_cast<const float *>(row)[i];
@@ -83,19 +107,75 @@ __device__ __forceinline__ float lp_load(const void *row, int64_t i) {
     else return __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]);
 }
 
+// The largest of a chunk's logits; NaN where there is one.
+template <int TYPE>
+__device__ __forceinline__ float lp_most(const uint4 &u) {
+    if constexpr (TYPE == QB_T_F32) {
+        float m;
+        asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, %3, %4;\n\tmax.NaN.f32 %0, %0, t;\n\t}"
+            : "=&f"(m)
+            : "f"(__uint_as_float(u.x)), "f"(__uint_as_float(u.y)), "f"(__uint_as_float(u.z)), "f"(__uint_as_float(u.w)));
+        return m;
+    } else if constexpr (TYPE == QB_T_F16) {
+        const auto h = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
+        const __half2 m = __hmax2_nan(__hmax2_nan(h(u.x), h(u.y)), __hmax2_nan(h(u.z), h(u.w)));
+        return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+    } else {
+        const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(u.x), h(u.y)), __hmax2_nan(h(u.z), h(u.w)));
+        return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+    }
+}
+
+// -infinity (and what is next to it) as kLpFloor.  In f16, where that is no number, after unpacking
+template <int TYPE>
+__device__ __forceinline__ void lp_floor(uint4 &u) {
+    if constexpr (TYPE == QB_T_F32) {
+        u.x = __float_as_uint(fmaxf(__uint_as_float(u.x), kLpFloor));
+        u.y = __float_as_uint(fmaxf(__uint_as_float(u.y), kLpFloor));
+        u.z = __float_as_uint(fmaxf(__uint_as_float(u.z), kLpFloor));
+        u.w = __float_as_uint(fmaxf(__uint_as_float(u.w), kLpFloor));
+    } else if constexpr (TYPE == QB_T_BF16) {
+        const __nv_bfloat162 f = __float2bfloat162_rn(kLpFloor);
+        const auto h = [&](uint32_t w) {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w), f);
+            return *reinterpret_cast<const uint32_t *>(&m);
+        };
+        u = make_uint4(h(u.x), h(u.y), h(u.z), h(u.w));
+    }
+}
+
 struct LpSums {
     float X, S, T;
     int bad;  // a NaN or +infinity
 };
-__device__ __forceinline__ LpSums lp_join(const LpSums &a, const LpSums &b, float s2) {
-    LpSums r;
-    r.X = fmaxf(a.X, b.X);
-    r.bad = a.bad | b.bad;
-    const float da = a.S > 0.0f ? fmaxf((a.X - r.X) * s2, -1e4f) : 0.0f, db = b.S > 0.0f ? fmaxf((b.X - r.X) * s2, -1e4f) : 0.0f;
-    const float fa = lp_ex2(da), fb = lp_ex2(db);
-    r.S = a.S * fa + b.S * fb;
-    r.T = (a.T + a.S * da) * fa + (b.T + b.S * db) * fb;
-    return r;
+// The sums relative to X, no less than their own reference.  The exponent is formed to twice f32's
+// bits: a thread's or a block's sums all share this factor's error.
+__device__ __forceinline__ void lp_rescale(LpSums &a, float X, float s2) {
+    if (a.S > 0.0f && a.X != X) {
+        const float t = a.X - X, b = t - a.X, lo = (a.X - (t - b)) - (X + b);
+        const float d = t * s2, dl = fmaf(t, s2, -d) + lo * s2;
+        if (d > -150.0f) {
+            const float f = lp_ex2(d) * fmaf(dl, 0.6931471805599453f, 1.0f);
+            a.T = (a.T + a.S * (d + dl)) * f;
+            a.S *= f;
+        } else {
+            a.S = a.T = 0.0f;
+        }
+    }
+    a.X = X;
+}
+// The sums of the 2^n lanes that differ in the lowest n bits, in each of them.
+__device__ __forceinline__ LpSums lp_reduce(LpSums a, int lanes, float s2) {
+    float X = a.X;
+    for (int o = lanes / 2; o; o >>= 1) X = fmaxf(X, __shfl_xor_sync(0xFFFFFFFFu, X, o));
+    lp_rescale(a, X, s2);
+    for (int o = lanes / 2; o; o >>= 1) {
+        a.S += __shfl_xor_sync(0xFFFFFFFFu, a.S, o);
+        a.T += __shfl_xor_sync(0xFFFFFFFFu, a.T, o);
+        a.bad |= __shfl_xor_sync(0xFFFFFFFFu, a.bad, o);
+    }
+    return a;
 }
 
 struct LpSmem {
@@ -104,8 +184,11 @@ struct LpSmem {
     LpSums sums[kLpMaxCluster];
     LpSums warp_sums[kLpWarps];
     uint64_t warp_key[kLpWarps];
-    uint64_t thread_key[kLpThreads];
-    int count;
+    uint64_t nth[kLpNth];            // each warp's largest
+    uint64_t bound;
+    float slot[kLpSlots][kLpThreads];  // the largest of each part
+    uint16_t chosen[kLpChosen];        // parts that may hold candidates: slot, thread
+    int nchosen, count;
 };
 
 // The j-th largest of the lanes' keys (zero where fewer lanes have one).
@@ -147,6 +230,7 @@ __device__ __forceinline__ void lp_select(LpSmem &sm, uint64_t *list, int count,
     for (int i = tid; i < count; i += kLpThreads) {
         const uint64_t key = list[i];
         int rank = 0;
+#pragma unroll 8
         for (int o = 0; o < count; ++o) rank += list[o] > key;
         if (rank < k) out[rank] = key;
     }
@@ -190,203 +274,347 @@ struct LpRow {
 };
 
 template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpK p) {
+__global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const LpK p) {
     constexpr int V = lp_vec<TYPE>();
-    constexpr int kAhead = 4;  // loads under way a thread
+    constexpr int kGroup = kLpGroup, kAhead = kLpAhead;  // chunks that are worked on together; such groups in registers, the rest under way
+    constexpr int kStride = kGroup * kLpThreads, kSpan = kLpThreads * V + V - 1;  // from a group's first element to its last
     __shared__ LpSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
-    const int64_t row_i = blockIdx.x / p.cluster;
+    const int64_t rows_ahead = gridDim.x / p.cluster;
+    const float s2 = p.scale * 1.4426950408889634f;
+    auto the_row = [&](int64_t i) {
+        return LpRow<TYPE>(static_cast<const uint8_t *>(p.x) + i * p.stride * type_bytes(TYPE), p.vocab);
+    };
+    // the block's chunks that lie in the row whole; chunk 0 and the last one are looked at apart where they do not
+    auto part = [&](const LpRow<TYPE> &r) {
+        const int c0 = (int)((int64_t)r.nchunks * rank / p.cluster), c1 = (int)((int64_t)r.nchunks * (rank + 1) / p.cluster);
+        return make_int2(max(c0, r.i0), min(c1, r.i1));
+    };
     pdl_launch_dependents();
     pdl_wait();
-    if (p.cluster > 1) cg::this_cluster().barrier_arrive();
-    const LpRow<TYPE> row(static_cast<const uint8_t *>(p.x) + row_i * p.stride * type_bytes(TYPE), p.vocab);
-    const int nchunks = row.nchunks;
-    const int c0 = (int)((int64_t)nchunks * rank / p.cluster), c1 = (int)((int64_t)nchunks * (rank + 1) / p.cluster);
-    const float s2 = p.scale * 1.4426950408889634f;
-    const float lazy = kLpLazy / s2;
-
-    // ---- one pass
-    LpSums a = {-INFINITY, 0.0f, 0.0f, 0};
-    float top = __uint_as_float(0x7FC00000u);  // the thread's largest; NaN: none yet
-    int top_at = -1;                           // the chunk that holds it
-    auto take = [&](const uint4 &u, int c) {
-        float x[V];
-        lp_unpack<TYPE>(u, x);
-        if (!row.whole(c)) row.edge(c, x);
-        float most = x[0];
+    if (p.cluster > 1) cg::this_cluster().sync();  // every block of it has begun
+    uint4 u[kAhead][kGroup];
+    auto fetch = [&](uint4 (&w)[kGroup], const LpRow<TYPE> &r, int c, int end) {
 #pragma unroll
-        for (int i = 1; i < V; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(x[i]));
-        if (!(most <= top)) {
-            if (!(most < INFINITY)) a.bad = 1;  // a NaN or +infinity
-            else {
-                top = most;
-                top_at = c;
-                if (most > a.X + lazy) {
-                    const float d = a.S > 0.0f ? fmaxf((a.X - most) * s2, -1e4f) : 0.0f, f = lp_ex2(d);
-                    a.T = (a.T + a.S * d) * f;
-                    a.S *= f;
-                    a.X = most;
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float d = fmaxf((x[i] - a.X) * s2, -200.0f);  // 0 from -126 on
-            const float e = lp_ex2(d);
-            a.S += e;
-            a.T += e * d;
+        for (int i = 0; i < kGroup; ++i) {
+            w[i] = lp_nothing<TYPE>();
+            if (c + i * kLpThreads < end) w[i] = r.chunk(c + i * kLpThreads);
         }
     };
-    int c = c0 + tid;
-    for (; c + (kAhead - 1) * kLpThreads < c1; c += kAhead * kLpThreads) {
-        uint4 u[kAhead];
+    int64_t row_i = blockIdx.x / p.cluster;
+    {
+        const LpRow<TYPE> r = the_row(row_i);
+        const int2 c = part(r);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) u[i] = row.whole(c + i * kLpThreads) ? row.chunk(c + i * kLpThreads) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) take(u[i], c + i * kLpThreads);
+        for (int g = 0; g < kAhead; ++g) fetch(u[g], r, c.x + tid + g * kStride, c.y);
     }
-    for (; c < c1; c += kLpThreads) take(row.whole(c) ? row.chunk(c) : make_uint4(0u, 0u, 0u, 0u), c);
+    for (; row_i < p.n; row_i += rows_ahead) {
+        const LpRow<TYPE> row = the_row(row_i);
+        const int c0 = part(row).x, c1 = part(row).y;
+        // this thread's chunk that does not lie in the row whole, of those there are: -1
+        const int edge = rank == 0 && tid == 0 && row.i0 > 0              ? 0
+                         : rank == p.cluster - 1 && tid == 1 && row.i1 < row.nchunks && row.nchunks > row.i0 ? row.nchunks - 1
+                                                                          : -1;
 
-    // ---- the block's sums
-    if (top_at >= 0 && a.X != top) a = lp_join(a, LpSums{top, 0.0f, 0.0f, 0}, s2);
+        // ---- one pass
+        float top = __uint_as_float(0x7FC00000u);  // the thread's largest; NaN: none yet
+        int top_at = -1, bad = 0;                  // the group's first chunk that holds it; 1: a NaN or +infinity, 2: past kLpFar
+        float M = -INFINITY;
+        uint64_t S = 0, T = 0;                     // two sums each
+        auto see = [&](float most, int c) {
+            if (!(most < INFINITY)) {
+                bad |= 1;
+                return;
+            }
+            top = most;
+            top_at = c;
+            const float y = most * s2;
+            if (y > kLpFar) bad |= 2;
+            if (y > M + kLpLazy && y >= -kLpFar && y <= kLpFar) {
+                const float m = ceilf(y), d = M - m, f = lp_ex2(fmaxf(d, -150.0f));  // a power of two
+                const uint64_t d2 = pair_f32(d, d), f2 = pair_f32(f, f);
+                T = M == -INFINITY ? 0 : mul_f32x2(fma_f32x2(S, d2, T), f2);
+                S = mul_f32x2(S, f2);
+                M = m;
+            }
+        };
+        auto add = [&](const float (&x)[V]) {
+            const uint64_t f2 = pair_f32(s2, s2), m2 = pair_f32(-M, -M);
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        a = lp_join(a, LpSums{__shfl_xor_sync(0xFFFFFFFFu, a.X, o), __shfl_xor_sync(0xFFFFFFFFu, a.S, o),
-                              __shfl_xor_sync(0xFFFFFFFFu, a.T, o), (int)__shfl_xor_sync(0xFFFFFFFFu, a.bad, o)}, s2);
-    if (lane == 0) sm.warp_sums[warp] = a;
-    // a lower bound of the block's k-th largest: the thread's largest, as if it were its chunk's last element
-    const uint64_t mine = top_at < 0 ? 0 : lp_key(top, (uint32_t)(row.at(top_at) + V - 1));
-    if (p.k) {
-        sm.thread_key[tid] = mine;
-        const int full = min(kLpWarps, (c1 - c0) / 32);  // warps whose threads all have elements
-        const uint64_t nth = full ? lp_warp_nth(mine, (p.k + full - 1) / max(full, 1)) : 0;
-        if (lane == 0) sm.warp_key[warp] = warp < full ? nth : ~uint64_t(0);
-        if (tid == 0) sm.count = 0;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        LpSums b = sm.warp_sums[0];
-        for (int w = 1; w < kLpWarps; ++w) b = lp_join(b, sm.warp_sums[w], s2);
-        sm.warp_sums[0] = b;
-    }
-    if (p.k) {
-        uint64_t bound = sm.warp_key[0];
-        for (int w = 1; w < kLpWarps; ++w) bound = min(bound, sm.warp_key[w]);
-        if (bound == ~uint64_t(0)) bound = 0;
-        // ---- the candidates: a warp reads the elements of a thread that may hold some
-        const int per = (c1 - c0 + kLpThreads - 1) / kLpThreads;
-        for (int t = warp; t < kLpThreads; t += kLpWarps) {
-            // its largest may be its chunk's first element
-            if (sm.thread_key[t] + (V - 1) < bound || sm.thread_key[t] == 0) continue;
-            for (int i = lane; i < per; i += 32) {
-                const int ch = c0 + t + i * kLpThreads;
-                if (ch >= c1) break;
+            for (int i = 0; i < V; i += 2) {
+                const uint64_t d = fma_f32x2(pair_f32(x[i], x[i + 1]), f2, m2);
+                const float2 y = unpair_f32(d);
+                const uint64_t e = pair_f32(lp_ex2(y.x), lp_ex2(y.y));
+                S = add_f32x2(S, e);
+                T = fma_f32x2(e, d, T);
+            }
+        };
+        auto take = [&](uint4 (&w)[kGroup], int c) {
+            float most = lp_most<TYPE>(w[0]);
+#pragma unroll
+            for (int i = 1; i < kGroup; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(lp_most<TYPE>(w[i])));
+            if (!(most <= top)) see(most, c);
+            if (M == -INFINITY) return most;  // nothing that counts yet
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
                 float x[V];
-                row.load(ch, x);
+                lp_floor<TYPE>(w[i]);
+                lp_unpack<TYPE>(w[i], x);
+                if constexpr (TYPE == QB_T_F16) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[e] = fmaxf(x[e], kLpFloor);
+                }
+                add(x);
+            }
+            return most;
+        };
+        if (edge >= 0) {
+            float x[V], most;
+            row.edge(edge, x);
+            most = x[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(x[i]));
+            see(most, edge);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = fmaxf(x[i], kLpFloor);
+            if (M != -INFINITY) add(x);
+        }
+        float part_most = 0.0f;
+        for (int c = c0 + tid, i = 0; c < c1; c += kAhead * kStride, ++i) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < kAhead; ++g) {
+                if (c + g * kStride >= c1) break;
+                most = fmaxf(most, take(u[g], c + g * kStride));
+                fetch(u[g], row, c + (kAhead + g) * kStride, c1);
+            }
+            if (p.k) {
+                part_most = i & ((1 << p.shift) - 1) ? fmaxf(part_most, most) : most;
+                sm.slot[i >> p.shift][tid] = part_most;
+            }
+        }
+        if (row_i + rows_ahead < p.n) {  // the next row's, under way during what follows
+            const LpRow<TYPE> r = the_row(row_i + rows_ahead);
+            const int2 c = part(r);
+#pragma unroll
+            for (int g = 0; g < kAhead; ++g) fetch(u[g], r, c.x + tid + g * kStride, c.y);
+        }
+
+        // a row's reference is its largest logit in the end
+        const float2 sums = unpair_f32(S), sums_t = unpair_f32(T);
+        LpSums a = {top_at >= 0 ? top : -INFINITY, sums.x + sums.y, sums_t.x + sums_t.y, bad};
+        if (a.S > 0.0f) {
+            const float y = a.X * s2, yl = fmaf(a.X, s2, -y), d = M - y, b = d - M, lo = (M - (d - b)) - (y + b) - yl;
+            const float f = lp_ex2(d) * fmaf(lo, 0.6931471805599453f, 1.0f);
+            a.T = (a.T + a.S * (d + lo)) * f;
+            a.S *= f;
+        }
+
+        // ---- the block's sums
+        a = lp_reduce(a, 32, s2);
+        if (lane == 0) sm.warp_sums[warp] = a;
+        // the thread's largest as if it were its group's last element: one of its elements reaches that
+        uint64_t mine = 0;
+        int listed = 0;
+        if (p.k) {
+            if (top_at >= 0) mine = lp_key(top, (uint32_t)(row.at(top_at) + kSpan));
+            const int full = min(kLpWarps, (c1 - c0) / 32);  // warps whose threads all have elements
+            if (full) {
+                const int j = (p.k + full - 1) / full + (full == kLpWarps ? 2 : 0);
+                listed = j <= 32 ? full * j : 0;
+                uint64_t key = mine;
+                if (warp < full && listed)
+                    for (int i = 0; i < j; ++i) {
+                        const uint64_t t = lp_warp_nth(key, 1);
+                        if (key == t) key = 0;
+                        if (lane == 0) sm.nth[warp * j + i] = t;
+                    }
+            }
+            if (tid == 0) {
+                sm.count = sm.nchosen = 0;
+                sm.bound = 0;
+            }
+        }
+        __syncthreads();
+        a = lp_reduce(sm.warp_sums[lane & (kLpWarps - 1)], kLpWarps, s2);
+        if (!(a.bad & 1) && ((a.bad & 2) || a.X * s2 < -0.5f * kLpFar) && a.X > -INFINITY) {
+            // logits of such magnitudes, or rows of the type's lowest value alone: differences of logits are
+            // scaled instead of scaled logits subtracted
+            LpSums b = {a.X, 0.0f, 0.0f, 0};
+            for (int c = edge >= 0 ? edge : c0 + tid; edge >= 0 || c < c1;) {
+                float x[V];
+                row.load(c, x);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = fmaxf((x[i] - a.X) * s2, -200.0f), e = lp_ex2(d);
+                    b.S += e;
+                    b.T += e * d;
+                }
+                c = c == edge ? c0 + tid : c + kLpThreads;
+                if (c >= c1) break;
+            }
+            b = lp_reduce(b, 32, s2);
+            __syncthreads();
+            if (lane == 0) sm.warp_sums[warp] = b;
+            __syncthreads();
+            a = lp_reduce(sm.warp_sums[lane & (kLpWarps - 1)], kLpWarps, s2);
+        }
+        a.bad &= 1;
+        if (p.k) {
+            // a lower bound of the block's k-th largest: the k-th of those listed
+            if (tid < listed) {
+                const uint64_t key = sm.nth[tid];
+                int above = 0;
+                for (int i = 0; i < listed; ++i) above += sm.nth[i] > key;
+                if (above == p.k - 1 && key) sm.bound = key;
+            }
+            __syncthreads();
+            const uint64_t bound = sm.bound;
+            const float least = bound ? lp_key_value(bound) : -INFINITY;
+            // ---- the candidates: elements of the parts whose largest reaches the bound; of equal ones
+            // those that begin at its place or before it
+            const int step = kAhead * kStride << p.shift, parts = (c1 - c0 - tid + step - 1) / step;
+            const int last = (int)(0xFFFFFFFFu - (uint32_t)bound);
+            for (int i = 0; i < parts; ++i) {
+                const float v = sm.slot[i][tid];
+                if (v > least || (v == least && (bound == 0 || row.at(c0 + tid + i * step) <= last))) {
+                    const int to = atomicAdd(&sm.nchosen, 1);
+                    if (to < kLpChosen) sm.chosen[to] = (uint16_t)(i * kLpThreads + tid);
+                }
+            }
+            __syncthreads();
+            auto offer = [&](const float (&x)[V], int ch) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
+                    if (!(x[e] >= least)) continue;
                     const uint64_t key = row.key(ch, e, x[e]);
                     if (key < bound || key == 0) continue;
                     const int to = atomicAdd(&sm.count, 1);
                     if (to < kLpCand) sm.cand[to] = key;
                 }
-            }
-        }
-    }
-    __syncthreads();
-    LpSmem *first = &sm;
-    if (p.cluster > 1) cg::this_cluster().barrier_wait();  // every block has begun
-    if (p.cluster > 1) first = cg::this_cluster().map_shared_rank(&sm, 0);
-    if (tid == 0) first->sums[rank] = sm.warp_sums[0];
-    if (p.k) {
-        const int found = sm.count;
-        __syncthreads();
-        uint64_t *out = first->joined + rank * p.k;
-        for (int i = tid; i < p.k; i += kLpThreads)
-            if (i >= found) out[i] = 0;  // fewer elements than that
-        if (found <= kLpCand) {
-            lp_select(sm, sm.cand, found, p.k, out);
-        } else {
-            // more elements than fit reach the bound (long runs of rising logits): one largest after the other
-            uint64_t last = ~uint64_t(0);
-            for (int r = 0; r < p.k; ++r) {
-                uint64_t best = 0;
-                for (int ch = c0 + tid; ch < c1; ch += kLpThreads) {
+            };
+            const int per = kAhead * kGroup << p.shift, nchosen = sm.nchosen;
+            if (nchosen > kLpChosen && tid == 0) sm.count = kLpCand + 1;  // too many: see below
+            if (nchosen <= kLpChosen)
+                for (int i = tid; i < nchosen * per; i += kLpThreads) {
+                    const int e = i / per, t = sm.chosen[e] % kLpThreads, slot = sm.chosen[e] / kLpThreads;
+                    const int ch = c0 + t + (slot * per + (i - e * per)) * kLpThreads;
+                    if (ch >= c1) continue;
+                    const uint4 w = row.chunk(ch);
+                    if (lp_most<TYPE>(w) < least) continue;
                     float x[V];
-                    row.load(ch, x);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const uint64_t key = row.key(ch, e, x[e]);
-                        if (key < last) best = max(best, key);
-                    }
+                    lp_unpack<TYPE>(w, x);
+                    offer(x, ch);
                 }
-                best = lp_warp_nth(best, 1);
-                if (lane == 0) sm.warp_key[warp] = best;
-                __syncthreads();
-                for (int w = 0; w < kLpWarps; ++w) best = max(best, sm.warp_key[w]);
-                __syncthreads();
-                if (tid == 0) out[r] = best;
-                last = best;
+            if (edge >= 0) {
+                float x[V];
+                row.edge(edge, x);
+                offer(x, edge);
             }
         }
-    }
-    if (p.cluster > 1) {
-        cg::this_cluster().sync();
-        if (rank != 0) return;
-    } else {
         __syncthreads();
-    }
-
-    // ---- the row's, in its first block
-    LpSums r = sm.sums[0];
-    for (int w = 1; w < p.cluster; ++w) r = lp_join(r, sm.sums[w], s2);
-    const float nan = __uint_as_float(0x7FC00000u);
-    const float ln = logf(r.S);
-    // (x - X) first: exact where the two are near
-    auto logp = [&](float x) { return r.bad ? nan : r.S > 0.0f ? (x - r.X) * p.scale - ln : -INFINITY; };
-    if (tid == 0) {
-        if (p.lse) p.lse[row_i] = r.bad ? nan : r.S > 0.0f ? r.X * p.scale + ln : -INFINITY;
-        if (p.entropy) p.entropy[row_i] = r.bad ? nan : r.S > 0.0f ? fmaxf(ln - 0.6931471805599453f * (r.T / r.S), 0.0f) : 0.0f;
-    }
-    for (int i = tid; i < p.m; i += kLpThreads) {
-        const int t = p.tokens[row_i * p.m + i];
-        p.logp[row_i * p.m + i] = t < 0 || t >= p.vocab ? (r.bad ? nan : -INFINITY) : logp(lp_load<TYPE>(row.row, t));
-    }
-    if (p.k) {
-        uint64_t *best = sm.joined;
-        if (p.cluster > 1) {
-            best = sm.cand;
-            const int all = p.cluster * p.k;
-            if (all > kLpThreads) {
-                lp_select(sm, sm.joined, all, p.k, best);
+        LpSmem *first = &sm;
+        if (p.cluster > 1) first = cg::this_cluster().map_shared_rank(&sm, 0);
+        if (tid == 0) first->sums[rank] = a;
+        if (p.k) {
+            const int found = sm.count;
+            uint64_t *out = first->joined + rank * p.k;
+            for (int i = tid; i < p.k; i += kLpThreads)
+                if (i >= found) out[i] = 0;  // fewer elements than that
+            if (found <= kLpCand) {
+                lp_select(sm, sm.cand, found, p.k, out);
             } else {
-                for (int i = tid; i < all; i += kLpThreads) {
-                    const uint64_t key = sm.joined[i];
-                    int above = 0;
-                    for (int o = 0; o < all; ++o) above += sm.joined[o] > key;
-                    if (key && above < p.k) best[above] = key;
+                // more elements than fit reach the bound (long runs of rising logits): one largest after the other
+                uint64_t last = ~uint64_t(0);
+                for (int r = 0; r < p.k; ++r) {
+                    uint64_t best = 0;
+                    for (int ch = edge >= 0 ? edge : c0 + tid; edge >= 0 || ch < c1;) {
+                        float x[V];
+                        row.load(ch, x);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const uint64_t key = row.key(ch, e, x[e]);
+                            if (key < last) best = max(best, key);
+                        }
+                        ch = ch == edge ? c0 + tid : ch + kLpThreads;
+                        if (ch >= c1) break;
+                    }
+                    best = lp_warp_nth(best, 1);
+                    __syncthreads();
+                    if (lane == 0) sm.warp_key[warp] = best;
+                    __syncthreads();
+                    for (int w = 0; w < kLpWarps; ++w) best = max(best, sm.warp_key[w]);
+                    if (tid == 0) out[r] = best;
+                    last = best;
                 }
             }
-            __syncthreads();
         }
-        for (int i = tid; i < p.k; i += kLpThreads) {
-            const uint64_t key = best[i];
-            if (p.top_tok) p.top_tok[row_i * p.k + i] = r.bad ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
-            if (p.top_logp) p.top_logp[row_i * p.k + i] = logp(lp_key_value(key));
+        if (p.cluster > 1) cg::this_cluster().sync();
+        else __syncthreads();
+
+        // ---- the row's, in its first block
+        if (rank == 0) {
+            const LpSums r = lp_reduce(sm.sums[lane & (p.cluster - 1)], p.cluster, s2);
+            const float nan = __uint_as_float(0x7FC00000u);
+            const float ln = logf(r.S);
+            // (x - X) first: exact where the two are near
+            auto logp = [&](float x) { return r.bad ? nan : r.S > 0.0f ? (x - r.X) * p.scale - ln : -INFINITY; };
+            if (tid == 0) {
+                if (p.lse) p.lse[row_i] = r.bad ? nan : r.S > 0.0f ? r.X * p.scale + ln : -INFINITY;
+                if (p.entropy)
+                    p.entropy[row_i] = r.bad ? nan : r.S > 0.0f ? fmaxf(ln - 0.6931471805599453f * (r.T / r.S), 0.0f) : 0.0f;
+            }
+            for (int i = tid; i < p.m; i += kLpThreads) {
+                const int t = p.tokens[row_i * p.m + i];
+                p.logp[row_i * p.m + i] = t < 0 || t >= p.vocab ? (r.bad ? nan : -INFINITY) : logp(lp_load<TYPE>(row.row, t));
+            }
+            if (p.k) {
+                uint64_t *best = sm.joined;
+                if (p.cluster > 1) {
+                    best = sm.cand;
+                    const int all = p.cluster * p.k;
+                    if (all > kLpThreads) {
+                        lp_select(sm, sm.joined, all, p.k, best);
+                    } else {
+                        for (int i = tid; i < all; i += kLpThreads) {
+                            const uint64_t key = sm.joined[i];
+                            int above = 0;
+#pragma unroll 8
+                            for (int o = 0; o < all; ++o) above += sm.joined[o] > key;
+                            if (key && above < p.k) best[above] = key;
+                        }
+                    }
+                    __syncthreads();
+                }
+                for (int i = tid; i < p.k; i += kLpThreads) {
+                    const uint64_t key = best[i];
+                    if (p.top_tok) p.top_tok[row_i * p.k + i] = r.bad ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
+                    if (p.top_logp) p.top_logp[row_i * p.k + i] = logp(lp_key_value(key));
+                }
+            }
+        }
+        // what the next row writes, in the first block too, has been read
+        if (row_i + rows_ahead < p.n) {
+            if (p.cluster > 1) cg::this_cluster().sync();
+            else __syncthreads();
         }
     }
 }
 
 int launch_q_logprobs(int type, const void *x, int64_t stride, int64_t n, int vocab, float scale, const int32_t *tokens, int m,
                       float *logp, float *entropy, float *lse, int k, int32_t *top_tok, float *top_logp, cudaStream_t stream) {
-    LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1};
-    // a cluster a row where there are few rows: two blocks a multiprocessor, each at least 2048 elements
-    while (p.cluster < kLpMaxCluster && n * p.cluster < 2 * num_sms() && vocab / (2 * p.cluster) >= 2048) p.cluster *= 2;
+    LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1, 0};
+    // a cluster a row where there are few rows: as long as all blocks run at once, each at least 2048 elements
+    const int64_t slots = (int64_t)kLpBlocks * num_sms();
+    while (p.cluster < kLpMaxCluster && n * p.cluster * 2 <= slots && vocab / (2 * p.cluster) >= 2048) p.cluster *= 2;
+    const int steps = (vocab / (type == QB_T_F32 ? 4 : 8) / p.cluster + 3) / (kLpAhead * kLpGroup * kLpThreads) + 1;  // at the most
+    while (steps > kLpSlots << p.shift) ++p.shift;
+    const int64_t grid = p.cluster > 1 ? n * p.cluster : std::min<int64_t>(n, slots);
     auto *f = type == QB_T_F32 ? logprobs_kernel<QB_T_F32> : type == QB_T_F16 ? logprobs_kernel<QB_T_F16> : logprobs_kernel<QB_T_BF16>;
     if (p.cluster > 8 && cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return QB_E_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(n * p.cluster));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kLpThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
