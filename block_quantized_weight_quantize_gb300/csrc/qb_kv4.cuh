@@ -238,6 +238,8 @@ int launch_kv4_step_ext_128(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_step_ext_256(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_prompt_ext_64(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_kv4_prompt_ext_128(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_split_64(const Kv4AttnArgs &a, cudaStream_t stream);
+int launch_kv4_prompt_split_128(const Kv4AttnArgs &a, cudaStream_t stream);
 
 int launch_kv_tree_masks(const int32_t *parents, int64_t ntok, const int32_t *q_start, int nseq, uint32_t *masks, int words,
                          int32_t *depth, cudaStream_t stream);

@@ -30,11 +30,17 @@ int64_t kv4_attn_ws(int dp) {
 // The rule takes the slower kernel where one short sequence fills little of the card
 // (from 96 rows) and where much work has 64 to 95 rows.
 constexpr int kPromptFrom = 96;
+constexpr int kPromptExtFrom = 40, kPromptExtMid = 48, kPromptSplitTo = 128;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     if (kv4_attn_ext(a)) {
-        if (a.type != QB_T_F32 && a.c.dp <= 128 && a.ntok * (a.nh / a.c.nkv) >= (int64_t)kPromptFrom * a.s.nseq)
+        const int64_t rows = a.ntok * (a.nh / a.c.nkv), items = (int64_t)a.s.nseq * a.c.nkv;
+        const int64_t from = items >= num_sms() ? kPromptExtFrom : 3 * items >= num_sms() ? kPromptExtMid : kPromptFrom;
+        if (a.type != QB_T_F32 && a.c.dp <= 128 && rows >= from * a.s.nseq) {
+            if (rows <= (int64_t)kPromptSplitTo * a.s.nseq)
+                return a.c.dp == 64 ? launch_kv4_prompt_split_64(a, stream) : launch_kv4_prompt_split_128(a, stream);
             return a.c.dp == 64 ? launch_kv4_prompt_ext_64(a, stream) : launch_kv4_prompt_ext_128(a, stream);
+        }
         return a.c.dp == 64 ? launch_kv4_step_ext_64(a, stream)
                : a.c.dp == 128 ? launch_kv4_step_ext_128(a, stream) : launch_kv4_step_ext_256(a, stream);
     }

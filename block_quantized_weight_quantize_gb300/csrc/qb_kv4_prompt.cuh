@@ -71,6 +71,7 @@ struct PromptK {
     Kv4AttnArgs a;
     int grp;
     int min_share;  // tiles a block
+    int cost;       // EXT: what an item costs beside its tiles, in tiles
     float *part;    // [grid][2][kPromptRows][DP]: a block's pieces (0: of an item begun before it)
     float2 *stat;   // [grid][2][kPromptRows] m of the probabilities, sum
     int *last;      // [grid] the last block that holds a piece of the item that starts here and goes on; -1: none
@@ -87,11 +88,17 @@ struct PromptItem {
     int count;           // places of the block's share
     int from_start;
     int fine;            // keys as two f16
+    int split;           // SPLIT: its rows fill one row tile at the most
     int hole, jump;      // EXT: tiles below `jump` are numbered from `hole` on and stand for the sinks'
 };
 
 constexpr int kPromptFine = 2048;  // keys; see above
 constexpr int kPromptCost = 1;  // what an item costs beside its tiles, in tiles
+// The same for calls with sinks or trees, whose items are mostly short (an item's own cost is some 10 us),
+// and where row tiles take half of the tiles each.
+constexpr int kPromptExtCost = 5, kPromptSplitCost = 12;
+template <bool EXT>
+__device__ __forceinline__ int prompt_cost(const PromptK &p) { return EXT ? p.cost : kPromptCost; }
 
 template <int DP>
 struct PromptSmem {
@@ -103,6 +110,9 @@ struct PromptSmem {
     uint32_t any[4][4];              // whether a decoder warp's keys have one
     uint64_t q_full[kPromptQ], q_free[kPromptQ], s_full[kPromptQ], p_ready[kPromptQ], o_done[kPromptQ];
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2], drained;
+    uint64_t x_full, x_free;         // SPLIT: half of row tile 1's outputs on their way to tile 0's, in q[1]
+    float2 x_stat[kPromptTile];      // and its rows' m and sum
+    uint32_t x_bad[kPromptTile];
     uint32_t tmem;
     long long chunk_sum[8192 / 32 + 1];
     long long x0, share;             // the block's share: its first place, its places
@@ -334,14 +344,14 @@ __device__ __forceinline__ long long prompt_places(const PromptK &p, int c, int 
     long long mine = 0;
     int t0, jump;
     if (most <= 4 * __popc(left)) {
-        for (int rp = 0; rp < pairs; ++rp) mine += prompt_tiles<EXT>(p, q.len, q.T, rp, t0, jump) + kPromptCost;
+        for (int rp = 0; rp < pairs; ++rp) mine += prompt_tiles<EXT>(p, q.len, q.T, rp, t0, jump) + prompt_cost<EXT>(p);
         return mine * p.a.c.nkv;
     }
     for (; left; left &= left - 1) {
         const int l = __ffs(left) - 1;
         const int len = __shfl_sync(0xFFFFFFFFu, q.len, l), T = __shfl_sync(0xFFFFFFFFu, q.T, l);
         long long n = 0;
-        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) n += prompt_tiles<EXT>(p, len, T, rp, t0, jump) + kPromptCost;
+        for (int rp = lane; rp < prompt_pairs(p, T); rp += 32) n += prompt_tiles<EXT>(p, len, T, rp, t0, jump) + prompt_cost<EXT>(p);
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
         if (lane == l) mine = n * p.a.c.nkv;
@@ -409,7 +419,7 @@ __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchu
         rem -= it.kvh * per_head;
         for (int rp0 = 0; rp0 < prompt_pairs(p, it.T); rp0 += 32) {  // the row pair, 32 at a time
             int t0, jump;
-            const int w = rp0 + lane < prompt_pairs(p, it.T) ? prompt_tiles<EXT>(p, it.len, it.T, rp0 + lane, t0, jump) + kPromptCost : 0;
+            const int w = rp0 + lane < prompt_pairs(p, it.T) ? prompt_tiles<EXT>(p, it.len, it.T, rp0 + lane, t0, jump) + prompt_cost<EXT>(p) : 0;
             long long end = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -426,8 +436,8 @@ __device__ __forceinline__ void prompt_find(const PromptK &p, int lane, int nchu
             rem -= __shfl_sync(0xFFFFFFFFu, end, 31);
         }
         // now `rem` is the place in the item
-        it.u = max(0, (int)rem - kPromptCost);
-        it.place = max(0, kPromptCost - (int)rem);
+        it.u = max(0, (int)rem - prompt_cost<EXT>(p));
+        it.place = max(0, prompt_cost<EXT>(p) - (int)rem);
     }
     if (lane == 0) {
         x0_out = x0;
@@ -443,7 +453,7 @@ __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptIt
     __syncwarp();
     if (it.place + it.n >= it.count) return false;
     if (it.n) {  // past the piece before, which ended its item
-        it.place += it.n + kPromptCost;
+        it.place += it.n + prompt_cost<EXT>(p);
         if (it.place >= it.count) return false;
         it.u = 0;
         if (++it.rp == prompt_pairs(p, it.T)) {
@@ -465,6 +475,7 @@ __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptIt
     if constexpr (EXT) {
         it.hole = t0;
         it.jump = jump;
+        it.split = it.T * p.grp - it.rp * kPromptRows <= kPromptTile;
     }
     it.t0 = t0 + it.u;
     it.rest = tiles - it.u;
@@ -482,8 +493,9 @@ __device__ __forceinline__ bool prompt_next(const PromptK &p, int lane, PromptIt
     return true;
 }
 
-// EXT: a call with sinks or trees (the same code but for which tiles an item has and which of their keys a row sees)
-template <int DP, bool EXT>
+// EXT: a call with sinks or trees (the same code but for which tiles an item has and which of their keys a row sees).
+// SPLIT: items whose rows fill one row tile at the most are taken by both, every second key tile each.
+template <int DP, bool EXT, bool SPLIT>
 __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const PromptK p) {
     constexpr int NG = DP / 32, W = NG < 4 ? NG : 4;  // groups; one plane (DP <= 128)
     constexpr int kOctStride = kPromptTile * 16;      // bytes between groups of eight dims
@@ -506,6 +518,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             mbar_init(&sm.v_free[i], 1);
         }
         mbar_init(&sm.drained, 1);
+        mbar_init(&sm.x_full, kPromptTile);
+        mbar_init(&sm.x_free, kPromptTile);
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -535,10 +549,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tb + lanes + 128u * q, tO = tb + lanes + 256u + (uint32_t)DP * q;
         uint32_t tiles = 0, items = 0;  // of this row tile so far
+        [[maybe_unused]] uint32_t kt0 = 0, passed = 0;  // SPLIT: key tiles of the items before; halves of outputs passed on
         int goes_on = -1;
         bool ok = true;
         while (ok && prompt_next<EXT>(p, lane, it)) {
-            const int rho = it.rp * kPromptRows + q * kPromptTile + r, j = rho / p.grp;
+            const bool split = SPLIT && it.split;
+            const int rho0 = it.rp * kPromptRows + (split ? 0 : q * kPromptTile), rho = rho0 + r, j = rho / p.grp;
             const bool live = j < it.T;
             const int pos = live ? it.len - it.T + j : -1;
             const int first = kv_first_seen(pos, p.a.window);
@@ -555,7 +571,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 const bool f16 = p.a.type == QB_T_F16;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int rho2 = it.rp * kPromptRows + q * kPromptTile + (r & 96) + 8 * k + (lane >> 2), j2 = rho2 / p.grp;
+                    const int rho2 = rho0 + (r & 96) + 8 * k + (lane >> 2), j2 = rho2 / p.grp;
                     const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (it.q0 + (int64_t)j2) * p.a.q_stride +
                                           (int64_t)(it.kvh * p.grp + rho2 - j2 * p.grp) * p.a.c.d;
 #pragma unroll
@@ -607,8 +623,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 mbar_arrive(&sm.q_full[q]);
             }
             // tiles whose keys all of this row tile's rows see need no mask
-            const int j_lo = (it.rp * kPromptRows + q * kPromptTile) / p.grp;
-            const int j_hi = min(it.T - 1, (it.rp * kPromptRows + q * kPromptTile + kPromptTile - 1) / p.grp);
+            const int j_lo = rho0 / p.grp;
+            const int j_hi = min(it.T - 1, (rho0 + kPromptTile - 1) / p.grp);
             int pos_lo = INT_MAX, first_hi = 0;  // no row: whatever comes out
             if (j_lo < it.T) {
                 pos_lo = EXT ? kv4_pos_lo(p.a, it.len, it.T, j_lo) : it.len - it.T + j_lo;
@@ -622,11 +638,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
             PromptRow row = {cs, -INFINITY, 0.0f, 0.0f, 0, 0};
             uint32_t bad = 0;
             const int n_tiles = it.n, t_first = it.t0;
-            for (int i = 0; i < n_tiles; ++i, ++tiles) {
+            const int i_first = split ? q : 0;
+            for (int i = i_first; i < n_tiles; i += split ? 2 : 1, ++tiles) {
                 const int k0 = (EXT ? kv_part(t_first + i, it.hole, it.jump) : t_first + i) * kPromptTile;
                 if (!(ok = prompt_wait(&sm.s_full[q], tiles & 1, p.a.fault))) break;
                 tc_fence_after();
-                const uint32_t sl = tiles & 3, par = (tiles - 1) & 1;
+                const uint32_t sl = (SPLIT ? kt0 + i : tiles) & 3, par = (tiles - 1) & 1;
                 const bool odd = (sm.any[sl][0] | sm.any[sl][1] | sm.any[sl][2] | sm.any[sl][3]) != 0;
                 const bool masked = k0 + kPromptTile - 1 > pos_lo || (k0 < first_hi && (!EXT || k0 + kPromptTile > p.a.sinks));
                 const uint16_t *flags = sm.flags[sl];
@@ -643,21 +660,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     }
                     bad |= fl >> 8;
                     row.up = fl & 2u ? 4.0f : 0.0f;
-                    ok = prompt_step<DP, true, true>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, true>(tS, tO, row, sight, flags, i > i_first, &sm.o_done[q], par, p.a.fault);
                 } else if (masked) {
-                    ok = prompt_step<DP, true, false>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, true, false>(tS, tO, row, sight, flags, i > i_first, &sm.o_done[q], par, p.a.fault);
                 } else {
-                    ok = prompt_step<DP, false, false>(tS, tO, row, sight, flags, i > 0, &sm.o_done[q], par, p.a.fault);
+                    ok = prompt_step<DP, false, false>(tS, tO, row, sight, flags, i > i_first, &sm.o_done[q], par, p.a.fault);
                 }
                 if (!ok) break;
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_ready[q]);
             }
-            const float m = row.m, l = row.l;
+            float m = row.m, l = row.l;
             if (!ok) break;
-            if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
-            tc_fence_after();
+            if (!SPLIT || n_tiles > i_first) {
+                if (!(ok = prompt_wait(&sm.o_done[q], (tiles - 1) & 1, p.a.fault))) break;
+                tc_fence_after();
+            }
+            // a split item's rows: tile 1's sums go to tile 0's through shared memory, half of the columns at a
+            // time ([column][row]), where tile 1's queries were
+            [[maybe_unused]] float f0 = 1.0f, f1 = 0.0f;
+            [[maybe_unused]] float *const xbuf = reinterpret_cast<float *>(sm.q[1]) + r;
+            const bool joined = split && n_tiles > 1;
+            if constexpr (SPLIT) {
+                kt0 += n_tiles;
+                if (split && q == 1) {
+                    if (joined) {
+                        sm.x_stat[r] = make_float2(m, l);
+                        sm.x_bad[r] = bad;
+#pragma unroll 1
+                        for (int h = 0; h < 2 && ok; ++h) {
+                            if (passed && !(ok = prompt_wait(&sm.x_free, (passed - 1) & 1, p.a.fault))) break;
+#pragma unroll 1
+                            for (int c = 0; c < DP / 2; c += 32) {
+                                uint32_t o[32];
+                                __syncwarp();
+                                tc_ld32(tO + h * (DP / 2) + c, o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) xbuf[(c + e) * kPromptTile] = __uint_as_float(o[e]);
+                            }
+                            mbar_arrive(&sm.x_full);
+                            ++passed;
+                        }
+                        if (!ok || !(ok = prompt_wait(&sm.x_free, (passed - 1) & 1, p.a.fault))) break;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_free[q]);
+                    tc_fence_before();
+                    continue;
+                }
+                if (joined) {
+                    if (!(ok = prompt_wait(&sm.x_full, passed & 1, p.a.fault))) break;
+                    const float2 st = sm.x_stat[r];
+                    bad |= sm.x_bad[r];
+                    const float mm = fmaxf(m, st.x), ms = mm == -INFINITY ? 0.0f : mm;
+                    f0 = prompt_ex2(m - ms);
+                    f1 = prompt_ex2(st.x - ms);
+                    l = l * f0 + st.y * f1;
+                    m = mm;
+                }
+            }
             const bool whole = it.from_start && it.n == it.rest;
             const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
             const int64_t rec = (int64_t)(blockIdx.x * 2 + (it.from_start ? 1 : 0)) * kPromptRows + q * kPromptTile + r;
@@ -675,6 +737,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 uint32_t o[32];
                 __syncwarp();
                 tc_ld32(tO + 32 * kk, o);
+                if constexpr (SPLIT) {
+                    if (joined) {
+                        constexpr int kHalf = DP / 64;  // of 32 columns
+                        if (kk == kHalf && !(ok = prompt_wait(&sm.x_full, passed & 1, p.a.fault))) break;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + xbuf[(kk % kHalf * 32 + e) * kPromptTile] * f1);
+                        if ((kk + 1) % kHalf == 0) {
+                            mbar_arrive(&sm.x_free);
+                            ++passed;
+                        }
+                    }
+                }
                 // column (c * (W / 2) + u) * 8 + 2 j + h is dim (2 u + h) * 32 + 4 c + j
                 constexpr int CPL = 8 / W;  // chunks in 32 columns
 #pragma unroll
@@ -711,6 +786,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     }
                 }
             }
+            if (SPLIT && !ok) break;
             __syncwarp();
             if (whole) {
 #pragma unroll 4
@@ -880,9 +956,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
         // ================================================= products
         const uint32_t idS = tc_idesc_f16(kPromptTile, false), idO = tc_idesc_f16(DP, true);
         uint32_t kt = 0, fill = 0, items = 0;  // key tiles, fills of K's buffers, items so far
+        [[maybe_unused]] uint32_t done[kPromptQ] = {0, 0};  // SPLIT: a row tile's key tiles so far
         bool ok = warp == 12;
         // S = Q K^T with the key tile of fill f (and f + 1, what its rounding left)
-        auto scores = [&](int q, uint32_t f, auto fine_t) {
+        auto scores = [&](int q, uint32_t f, auto fine_t, bool last = false) {
             constexpr bool fine = decltype(fine_t)::value;
             const uint32_t qa = smem_u32(sm.q[q]);
             if (elect_one()) {
@@ -899,7 +976,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                                   tc_desc(kb + 2 * s * kOctStride, kOctStride, 128), idS, true);
                 }
                 tc_commit(&sm.s_full[q]);
-                if (q == kPromptQ - 1) {
+                if (q == kPromptQ - 1 || last) {
                     tc_commit(&sm.k_free[f & 1]);
                     if (fine) tc_commit(&sm.k_free[(f + 1) & 1]);
                 }
@@ -911,7 +988,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                    (!decltype(fine_t)::value || prompt_wait(&sm.k_full[(f + 1) & 1], (f + 1) >> 1 & 1, p.a.fault));
         };
         // O (+)= P V
-        auto outputs = [&](int q, uint32_t t, bool first) {
+        auto outputs = [&](int q, uint32_t t, bool first, bool last = false) {
             const uint32_t va = smem_u32(sm.v[t & 1]);
             if (elect_one()) {
 #pragma unroll
@@ -919,7 +996,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                     tc_mma_ts(tb + 256u + (uint32_t)DP * q, tb + 128u * q + 8u * s, tc_desc(va + 256 * s, 128, kOctStride),
                               idO, !first || s != 0);
                 tc_commit(&sm.o_done[q]);
-                if (q == kPromptQ - 1) tc_commit(&sm.v_free[t & 1]);
+                if (q == kPromptQ - 1 || last) tc_commit(&sm.v_free[t & 1]);
             }
             __syncwarp();
         };
@@ -933,22 +1010,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt_kernel(const Pro
                 if (!(ok = prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault))) return;
                 if (more && !(ok = keys_there(fill + step, fine))) return;
                 for (int q = 0; q < kPromptQ; ++q) {
-                    if (!(ok = prompt_wait(&sm.p_ready[q], kt & 1, p.a.fault))) return;
+                    const uint32_t par = (SPLIT ? done[q]++ : kt) & 1;
+                    if (!(ok = prompt_wait(&sm.p_ready[q], par, p.a.fault))) return;
                     tc_fence_after();
                     outputs(q, kt, i == 0);
                     if (!more) continue;
                     // products with different accumulators are not ordered: the next scores,
                     // which go where P is, wait until it has been read
-                    if (!(ok = prompt_wait(&sm.o_done[q], kt & 1, p.a.fault))) return;
+                    if (!(ok = prompt_wait(&sm.o_done[q], par, p.a.fault))) return;
                     tc_fence_after();
                     scores(q, fill + step, fine);
                 }
+            }
+        };
+        // an item that both row tiles take: every second key tile each
+        auto item_split = [&](auto fine) {
+            constexpr uint32_t step = decltype(fine)::value ? 2 : 1;
+            for (int q = 0; q < min(kPromptQ, it.n); ++q) {
+                if (!(ok = keys_there(fill + q * step, fine))) return;
+                tc_fence_after();
+                scores(q, fill + q * step, fine, true);
+            }
+            for (int i = 0; i < it.n; ++i, ++kt, fill += step) {
+                const int q = i & 1;
+                const uint32_t par = done[q]++ & 1;
+                if (!(ok = prompt_wait(&sm.v_full[kt & 1], (kt >> 1) & 1, p.a.fault))) return;
+                if (!(ok = prompt_wait(&sm.p_ready[q], par, p.a.fault))) return;
+                tc_fence_after();
+                outputs(q, kt, i < kPromptQ, true);
+                if (i + kPromptQ >= it.n) continue;
+                if (!(ok = keys_there(fill + 2 * step, fine))) return;
+                if (!(ok = prompt_wait(&sm.o_done[q], par, p.a.fault))) return;
+                tc_fence_after();
+                scores(q, fill + 2 * step, fine, true);
             }
         };
         while (ok && prompt_next<EXT>(p, lane, it)) {
             for (int q = 0; q < kPromptQ && ok; ++q) ok = prompt_wait(&sm.q_full[q], items & 1, p.a.fault);
             ++items;
             if (!ok) break;
+            if constexpr (SPLIT) {
+                if (it.split) {
+                    if (it.fine) item_split(std::true_type());
+                    else item_split(std::false_type());
+                    continue;
+                }
+            }
             if (it.fine) item(std::true_type());
             else item(std::false_type());
         }
@@ -1053,12 +1160,13 @@ inline PromptWs prompt_ws(int64_t grid, int64_t dp) {
     return w;
 }
 
-template <int DP, bool EXT = false>
+template <int DP, bool EXT = false, bool SPLIT = false>
 int launch_kv4_prompt(const Kv4AttnArgs &a, cudaStream_t stream) {
     PromptK p;
     p.a = a;
     p.grp = a.nh / a.c.nkv;
     p.min_share = 4;
+    p.cost = SPLIT ? kPromptSplitCost : kPromptExtCost;
     const int grid = attn_grid();
     const PromptWs w = prompt_ws(grid, DP);
     p.part = reinterpret_cast<float *>(a.ws + w.part);
@@ -1066,7 +1174,7 @@ int launch_kv4_prompt(const Kv4AttnArgs &a, cudaStream_t stream) {
     p.meta = reinterpret_cast<int4 *>(a.ws + w.meta);
     p.last = reinterpret_cast<int *>(a.ws + w.last);
     constexpr int smem = (int)sizeof(PromptSmem<DP>) + 128;
-    auto *f = kv4_prompt_kernel<DP, EXT>;
+    auto *f = kv4_prompt_kernel<DP, EXT, SPLIT>;
     if (ensure_smem_limit(reinterpret_cast<const void *>(f), smem) != QB_OK) return QB_E_CUDA;
     if (const int rc = launch_pdl(f, dim3((unsigned)grid), dim3(kPromptThreads), smem, stream, p)) return rc;
     return launch_pdl(kv4_prompt_join_kernel<DP>, dim3((unsigned)grid, kPromptRows / kJoinRows), dim3(256), 0, stream, p);

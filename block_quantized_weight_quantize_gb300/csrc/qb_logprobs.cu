@@ -23,13 +23,15 @@
 // k <= 1, 185 us for k = 20).  A block's shared memory is kept below 30 KB, as what it takes from the
 // first-level cache bounds the loads under way (50 KB: 152 us instead of 140).
 //
-// Measured: 3001 rows of 100003 in bf16 (600 MB), k = 3: 141 us, 4.3 TB/s; without alternatives 120.  In f32
-// 1500 rows of 100000: 118 us, 5.1 TB/s.  Instructions bound it in half precision (2.6 a cycle and
-// multiprocessor), latency where there are few rows: 64 rows of 128256 in f32, k = 20: 16.5 us.
+// Measured: 3001 rows of 100003 in bf16 (600 MB), k = 3: 125 us, 4.8 TB/s; without alternatives 104, 5.8.  In
+// f32 1500 rows of 100000: 99 us without, 6.0 TB/s, 110 with five.  What alternatives add is a row's end: its
+// barriers and the reading of the parts.  Few rows are latency: 64 rows of 128256 in f32, k = 20: 15 us
+// (9.7 without); one of 49152, k = 5: 6.7 us.
 #include <algorithm>
 #include <cmath>
 #include <cooperative_groups.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "qb_kv4.cuh"
 
@@ -60,7 +62,7 @@ struct LpK {
     int k;
     int32_t *top_tok;
     float *top_logp;
-    int cluster;
+    int cluster, log_cluster;
     int shift;  // a part is 2^shift steps of a thread
 };
 
@@ -107,24 +109,35 @@ __device__ __forceinline__ float lp_load(const void *row, int64_t i) {
     else return __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]);
 }
 
-// The largest of a chunk's logits; NaN where there is one.
+// The largest of N chunks' logits; NaN where there is one.
+template <int TYPE, int N>
+__device__ __forceinline__ float lp_most(const uint4 (&u)[N]) {
+    if constexpr (TYPE == QB_T_F32) {
+        float m = __uint_as_float(u[0].x);
+        const auto with = [&](uint32_t w) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__uint_as_float(w))); };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i) with(u[i].x);
+            with(u[i].y);
+            with(u[i].z);
+            with(u[i].w);
+        }
+        return m;
+    } else {
+        using H2 = std::conditional_t<TYPE == QB_T_F16, __half2, __nv_bfloat162>;
+        const auto h = [](const uint32_t &w) { return *reinterpret_cast<const H2 *>(&w); };
+        H2 m = __hmax2_nan(__hmax2_nan(h(u[0].x), h(u[0].y)), __hmax2_nan(h(u[0].z), h(u[0].w)));
+#pragma unroll
+        for (int i = 1; i < N; ++i)
+            m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(h(u[i].x), h(u[i].y)), __hmax2_nan(h(u[i].z), h(u[i].w))));
+        if constexpr (TYPE == QB_T_F16) return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+        else return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+    }
+}
 template <int TYPE>
 __device__ __forceinline__ float lp_most(const uint4 &u) {
-    if constexpr (TYPE == QB_T_F32) {
-        float m;
-        asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, %3, %4;\n\tmax.NaN.f32 %0, %0, t;\n\t}"
-            : "=&f"(m)
-            : "f"(__uint_as_float(u.x)), "f"(__uint_as_float(u.y)), "f"(__uint_as_float(u.z)), "f"(__uint_as_float(u.w)));
-        return m;
-    } else if constexpr (TYPE == QB_T_F16) {
-        const auto h = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
-        const __half2 m = __hmax2_nan(__hmax2_nan(h(u.x), h(u.y)), __hmax2_nan(h(u.z), h(u.w)));
-        return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
-    } else {
-        const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
-        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(u.x), h(u.y)), __hmax2_nan(h(u.z), h(u.w)));
-        return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
-    }
+    const uint4 a[1] = {u};
+    return lp_most<TYPE>(a);
 }
 
 // -infinity (and what is next to it) as kLpFloor.  In f16, where that is no number, after unpacking
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
     };
     // the block's chunks that lie in the row whole; chunk 0 and the last one are looked at apart where they do not
     auto part = [&](const LpRow<TYPE> &r) {
-        const int c0 = (int)((int64_t)r.nchunks * rank / p.cluster), c1 = (int)((int64_t)r.nchunks * (rank + 1) / p.cluster);
+        const int c0 = (int)((uint32_t)(r.nchunks * rank) >> p.log_cluster), c1 = (int)((uint32_t)(r.nchunks * (rank + 1)) >> p.log_cluster);
         return make_int2(max(c0, r.i0), min(c1, r.i1));
     };
     pdl_launch_dependents();
@@ -296,10 +309,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
     if (p.cluster > 1) cg::this_cluster().sync();  // every block of it has begun
     uint4 u[kAhead][kGroup];
     auto fetch = [&](uint4 (&w)[kGroup], const LpRow<TYPE> &r, int c, int end) {
+        if (c + (kGroup - 1) * kLpThreads < end) {
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            w[i] = lp_nothing<TYPE>();
-            if (c + i * kLpThreads < end) w[i] = r.chunk(c + i * kLpThreads);
+            for (int i = 0; i < kGroup; ++i) w[i] = r.chunk(c + i * kLpThreads);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                w[i] = lp_nothing<TYPE>();
+                if (c + i * kLpThreads < end) w[i] = r.chunk(c + i * kLpThreads);
+            }
         }
     };
     int64_t row_i = blockIdx.x / p.cluster;
@@ -351,9 +369,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             }
         };
         auto take = [&](uint4 (&w)[kGroup], int c) {
-            float most = lp_most<TYPE>(w[0]);
-#pragma unroll
-            for (int i = 1; i < kGroup; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(lp_most<TYPE>(w[i])));
+            const float most = lp_most<TYPE>(w);
             if (!(most <= top)) see(most, c);
             if (M == -INFINITY) return most;  // nothing that counts yet
 #pragma unroll
@@ -421,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             if (top_at >= 0) mine = lp_key(top, (uint32_t)(row.at(top_at) + kSpan));
             const int full = min(kLpWarps, (c1 - c0) / 32);  // warps whose threads all have elements
             if (full) {
-                const int j = (p.k + full - 1) / full + (full == kLpWarps ? 2 : 0);
+                const int j = (p.k + full - 1) / full + (full == kLpWarps ? (2 * p.k > full) + (p.k > full) : 0);
                 listed = j <= 32 ? full * j : 0;
                 uint64_t key = mine;
                 if (warp < full && listed)
@@ -466,6 +482,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             if (tid < listed) {
                 const uint64_t key = sm.nth[tid];
                 int above = 0;
+#pragma unroll 8
                 for (int i = 0; i < listed; ++i) above += sm.nth[i] > key;
                 if (above == p.k - 1 && key) sm.bound = key;
             }
@@ -604,10 +621,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
 
 int launch_q_logprobs(int type, const void *x, int64_t stride, int64_t n, int vocab, float scale, const int32_t *tokens, int m,
                       float *logp, float *entropy, float *lse, int k, int32_t *top_tok, float *top_logp, cudaStream_t stream) {
-    LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1, 0};
+    LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1, 0, 0};
     // a cluster a row where there are few rows: as long as all blocks run at once, each at least 2048 elements
     const int64_t slots = (int64_t)kLpBlocks * num_sms();
-    while (p.cluster < kLpMaxCluster && n * p.cluster * 2 <= slots && vocab / (2 * p.cluster) >= 2048) p.cluster *= 2;
+    while (p.cluster < kLpMaxCluster && n * p.cluster * 2 <= slots && vocab / (2 * p.cluster) >= 2048) {
+        p.cluster *= 2;
+        ++p.log_cluster;
+    }
     const int steps = (vocab / (type == QB_T_F32 ? 4 : 8) / p.cluster + 3) / (kLpAhead * kLpGroup * kLpThreads) + 1;  // at the most
     while (steps > kLpSlots << p.shift) ++p.shift;
     const int64_t grid = p.cluster > 1 ? n * p.cluster : std::min<int64_t>(n, slots);

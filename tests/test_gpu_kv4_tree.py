@@ -154,6 +154,53 @@ def test_wide_trees(name, kind, window, sinks, nh, nkv, d, page):
     Ext(window + nh, lens, news, nh, nkv, d, page, name, sinks=sinks, marks=trees(window, news, kind)).check(window=window)
 
 
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 5), (700, 300)])
+@pytest.mark.parametrize("nh,nkv,d,page", [(8, 2, 128, 16), (8, 1, 64, 64), (9, 1, 96, 32)])
+def test_trees_of_one_row_tile(name, window, sinks, nh, nkv, d, page):
+    """Sequences whose rows fill one tile of 128 at the most: one key tile, two, three, many; some with more rows between them."""
+    lens, news = [100, 200, 300, 30, 2500, 1000, 129, 128, 5000, 400], [16, 12, 31, 30, 14, 60, 20, 13, 9, 40]
+    Ext(window + nh, lens, news, nh, nkv, d, page, name, sinks=sinks, marks=trees(window, news)).check(window=window)
+
+
+@pytest.mark.parametrize("nkv", [1, 8])
+def test_a_row_tile_is_joined_with_other_blocks(nkv):
+    """Long sequences with few rows: pieces of an item in several blocks, each of two halves."""
+    news = [20, 25, 17]
+    Ext(nkv, [6001, 900, 3000], news, 4 * nkv, nkv, 128, 16, "f16", marks=trees(1, news)).check()
+    Ext(nkv, [6001, 900, 3000], news, 4 * nkv, nkv, 64, 16, "bf16", sinks=200).check(window=2500)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_large_steps_in_a_row_tile(name):
+    """Steps past 2^12 and steps that are not finite, in values of a sequence of one row tile.  Scores of magnitudes of some 10 and
+    values in f16 are off by 2^-11 each at the most, a probability by 2^-11 and as much by its score's: less than 2^-9 of the
+    weighed magnitudes together."""
+    import torch
+    news = [24, 20]
+    b = Ext(7, [700, 300], news, 8, 2, 128, 16, name, marks=trees(5, news), sinks=3)
+    before = b.run(0.1, 130)
+    place = np.array([550, 600])  # of sequence 0: out of the window and in it
+    slots = _i32(b.tables[0, place // 16] * 16 + place % 16)
+    k, v = torch.zeros((2, 2, 128), device="cuda"), torch.zeros((2, 2, 128), device="cuda")
+    v[:, 0, :32] = 50000.0
+    v[0, 1] = 1e30
+    qb.kv4_append(b.cache, k, v, slots)
+    kb, vb = torch.empty_like(k), torch.empty_like(v)
+    qb.kv4_read(b.cache, slots, kb, vb)
+    b.k[place], b.v[place] = kb.double().cpu().numpy(), vb.double().cpu().numpy()
+    seen = [seen_keys(700, 24, j, 130, 3, b.marks[0][j]) for j in range(24)]
+    out, lse = b.run(0.1, 130)
+    assert torch.equal(out[24:], before[0][24:])
+    for j in range(24):  # key 550 is seen by the tokens whose path is short
+        assert bool(torch.isnan(out[j, 4:]).all()) == (550 in seen[j]) and 600 in seen[j]
+        assert not bool(torch.isnan(out[j, :4]).any())
+    b.v[550, 1] = 0.0
+    want = attention(b.q[:24].double().cpu().numpy(), b.k[:700], b.v[:700], 700, 24, 0.1, seen)
+    got = out[:24, :4].double().cpu().numpy()
+    assert np.all(np.abs(got - want[0][:, :4]) <= 2.0 ** -9 * want[3][:, :4] + 2.0 ** -8 * np.abs(want[0][:, :4]) + 2.0 ** -24)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 def test_trees_on_long_sequences_are_split(name):
     news = [7, 1, 12]
