@@ -30,6 +30,19 @@ int64_t kv4_attn_ws(int dp) {
 // The rule takes the slower kernel where one short sequence fills little of the card
 // (from 96 rows) and where much work has 64 to 95 rows.
 constexpr int kPromptFrom = 96;
+// With trees or sinks, where items' own cost is weighed and row tiles share the key tiles of few rows: step against
+// prompt kernel, us, trees of rows / 4 tokens, otherwise as above:
+//     rows                        32          48          64          96          128
+//     1 sequence of 2000 keys     18 / 34     18 / 35     19 / 35     23 / 35     25 / 35
+//     1 of 8000                   25 / 31     28 / 31     32 / 31     40 / 31     48 / 32
+//     8 of 300                    18 / 25     21 / 25     25 / 25     30 / 25     42 / 26
+//     8 of 2000                   34 / 45     42 / 45     51 / 45     70 / 45     86 / 46
+//     8 of 8000                   79 / 69     110 / 69    139 / 69    200 / 70    260 / 70
+//     32 of 1000                  62 / 74     95 / 74     116 / 74    154 / 74    202 / 75
+//     64 of 300                   52 / 71     66 / 71     81 / 71     131 / 71    133 / 73
+//     64 of 2000                  155 / 205   218 / 209   284 / 207   407 / 205   534 / 210
+// Row tiles share key tiles (twice 128 rows take 250 us of the last line instead) where an average sequence's rows
+// fill one.
 constexpr int kPromptExtFrom = 40, kPromptExtMid = 48, kPromptSplitTo = 128;
 
 int launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
