@@ -108,7 +108,8 @@ def _on(t, what: str, dev=None) -> int:
 
 def _dev(t, dtype, what: str, dev: int):
     """Address of a contiguous tensor of `dtype` on device `dev`."""
-    _on(t, what, dev)
+    if t.get_device() != dev:
+        _on(t, what, dev)
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
     if not t.is_contiguous():
@@ -118,7 +119,8 @@ def _dev(t, dtype, what: str, dev: int):
 
 def _rows(t, heads: int, d: int, what: str, dev: int):
     """Address and token stride of [n, heads, d] rows on device `dev` whose last two axes are contiguous."""
-    _on(t, what, dev)
+    if t.get_device() != dev:
+        _on(t, what, dev)
     n, h, e = t.shape if t.dim() == 3 else (0, 0, 0)
     if h != heads or e != d:
         raise ValueError(f"{what}: [n, {heads}, {d}] expected, got {tuple(t.shape)}")
@@ -299,30 +301,42 @@ def q_logprobs(logits, tokens=None, scale: float = 1.0, logprobs=None, entropy=N
     """From logits [n, vocab] (float32, float16 or bfloat16; rows contiguous) times `scale`: logprobs f32 [n, m] of tokens
     int32 [n, m], entropy and lse f32 [n], the k largest logits' places top_tokens int32 [n, k] and log probabilities
     top_logprobs f32 [n, k].  What is None is not computed."""
-    f32, dev = torch.float32, _on(logits, "logits")
-    if logits.dim() != 2 or logits.dtype not in _TYPE or logits.stride(1) != 1 and logits.shape[1] != 1:
-        raise ValueError("logits: float32, float16 or bfloat16 [n, vocab] with contiguous rows expected")
+    f32, dev, typ = torch.float32, logits.get_device(), _TYPE.get(logits.dtype)
+    if dev < 0:
+        _on(logits, "logits")
+    if logits.dim() != 2 or typ is None:
+        raise ValueError("logits: float32, float16 or bfloat16 [n, vocab] expected")
     n, vocab = logits.shape
+    stride, one = logits.stride()
+    if one != 1 and vocab != 1:
+        raise ValueError("logits: contiguous rows expected")
     m = k = 0
-    tp = lp = None
+    tp = lp = ep = sp = ttp = tlp = None
     if tokens is not None:
         if logprobs is None or tokens.dim() != 2 or tokens.shape[0] != n or logprobs.shape != tokens.shape:
             raise ValueError("tokens and logprobs: [n, m] expected")
         m, tp, lp = tokens.shape[1], _dev(tokens, torch.int32, "tokens", dev), _dev(logprobs, f32, "logprobs", dev)
     elif logprobs is not None:
         raise ValueError("logprobs: of which tokens?")
-    for t, what in ((entropy, "entropy"), (lse, "lse")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{what}: [n] expected")
-    for t in (top_tokens, top_logprobs):
-        if t is not None:
-            if t.dim() != 2 or t.shape[0] != n or k and t.shape[1] != k:
-                raise ValueError("top_tokens, top_logprobs: [n, k] expected")
-            k = t.shape[1]
-    _check(_c.q_logprobs(_TYPE[logits.dtype], logits.data_ptr(), logits.stride(0) if n > 1 else vocab, n, vocab, scale, tp, m, lp,
-                         None if entropy is None else _dev(entropy, f32, "entropy", dev), None if lse is None else _dev(lse, f32, "lse", dev), k,
-                         None if top_tokens is None else _dev(top_tokens, torch.int32, "top_tokens", dev),
-                         None if top_logprobs is None else _dev(top_logprobs, f32, "top_logprobs", dev), _stream(stream, dev)), "q_logprobs")
+    if entropy is not None:
+        ep = _dev(entropy, f32, "entropy", dev)
+        if entropy.numel() != n:
+            raise ValueError("entropy: [n] expected")
+    if lse is not None:
+        sp = _dev(lse, f32, "lse", dev)
+        if lse.numel() != n:
+            raise ValueError("lse: [n] expected")
+    if top_tokens is not None:
+        if top_tokens.dim() != 2 or top_tokens.shape[0] != n:
+            raise ValueError("top_tokens: [n, k] expected")
+        k, ttp = top_tokens.shape[1], _dev(top_tokens, torch.int32, "top_tokens", dev)
+    if top_logprobs is not None:
+        if top_logprobs.dim() != 2 or top_logprobs.shape[0] != n or (ttp is not None and top_logprobs.shape[1] != k):
+            raise ValueError("top_logprobs: [n, k] expected, with top_tokens' k")
+        k, tlp = top_logprobs.shape[1], _dev(top_logprobs, f32, "top_logprobs", dev)
+    _check(_c.q_logprobs(typ, logits.data_ptr(), stride if n > 1 else vocab, n, vocab, scale, tp, m, lp, ep, sp, k, ttp, tlp,
+                         _stream(stream, dev)), "q_logprobs")
+
 
 
 # ------------------------------------------------------------------ pages
