@@ -20,7 +20,7 @@
 // the first one's shared memory: no workspace, one launch.  Blocks go on to further rows, whose first
 // chunks are under way while a row is finished.  Three groups of two chunks of 16 bytes a thread
 // are in registers or under way: four blocks of 256 threads a multiprocessor (128 threads: the same for
-// k <= 1, 185 us for k = 20).  A block's shared memory is kept below 30 KB, as what it takes from the
+// k <= 1, a fourth more for k = 20).  A block's shared memory is kept below 30 KB, as what it takes from the
 // first-level cache bounds the loads under way (50 KB: 152 us instead of 140).
 //
 // Measured: 3001 rows of 100003 in bf16 (600 MB), k = 3: 125 us, 4.8 TB/s; without alternatives 104, 5.8.  In
@@ -39,14 +39,21 @@ namespace qb {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpBlocks = 4;  // a multiprocessor
 constexpr int kLpMaxK = QB_MAX_ALTERNATIVES, kLpMaxCluster = 16;
+constexpr int kLpGroup = 2, kLpAhead = 3;  // chunks that are worked on together; such groups in registers, most of them under way
 constexpr int kLpCand = 1024;    // candidates a block holds
-constexpr int kLpNth = kLpMaxK + 2 * kLpWarps;  // largest of the warps' threads, at the most
-constexpr int kLpGroup = 2, kLpAhead = 3;
-constexpr int kLpSlots = 8;     // parts of a thread's elements whose largest is remembered
+constexpr int kLpSlots = 8;      // parts of a thread's elements whose largest is remembered
 constexpr int kLpChosen = 1024;  // of these, as many are looked at again
+// Blocks of 256 threads, or of 64 for many short rows, whose end takes longer than their elements.  4000
+// rows in f32, us with 256 threads, with 64:
+//     elements a row     300         1000        4000        8000        8000 in bf16
+//     k = 0              19.5 11.7   21.3 12.6   24.4 22.1   31.3 34.6   27.4 23.4
+//     k = 5              39.1 22.1   41.4 23.0   46.1 32.9   54.0 46.8   51.0 35.6
+//     k = 20             44.4 28.0   48.2 28.9   51.6 40.5   59.7 55.2   56.5 44.6
+//     k = 64             81.8 80.2   63.9 85.4   65.7 126    74.1 159    73.3 152
+// Where all rows run at once in 256 threads, these are as fast or faster (100 of 1000, k = 20: 6.3, 7.0).
+constexpr int kLpShort = 64, kLpLong = 256, kLpShortRow = 8192, kLpShortK = 32;
+constexpr int lp_blocks(int threads) { return threads == kLpLong ? 4 : 16; }  // a multiprocessor
 constexpr float kLpLazy = 32.0f;     // 2^32 times 2^24 elements stay far below f32's top
 constexpr float kLpFar = 0x1p22f;    // scaled logits up to here are whole numbers' neighbours
 constexpr float kLpFloor = -0x1p100f;  // what -infinity counts as: its probability is 0, and 0 times it 0
@@ -191,16 +198,19 @@ __device__ __forceinline__ LpSums lp_reduce(LpSums a, int lanes, float s2) {
     return a;
 }
 
+template <int THREADS>
 struct LpSmem {
+    static constexpr int kWarps = THREADS / 32;
+    static constexpr int kNth = kLpMaxK + 2 * kWarps;  // largest of the warps' threads, at the most
     uint64_t cand[kLpCand];
-    uint64_t joined[kLpMaxCluster * kLpMaxK];  // of the first block: every block's largest
+    uint64_t joined[(THREADS == kLpLong ? kLpMaxCluster : 1) * kLpMaxK];  // of the first block: every block's largest
     LpSums sums[kLpMaxCluster];
-    LpSums warp_sums[kLpWarps];
-    uint64_t warp_key[kLpWarps];
-    uint64_t nth[kLpNth];            // each warp's largest
+    LpSums warp_sums[kWarps];
+    uint64_t warp_key[kWarps];
+    uint64_t nth[kNth];              // each warp's largest
     uint64_t bound;
-    float slot[kLpSlots][kLpThreads];  // the largest of each part
-    uint16_t chosen[kLpChosen];        // parts that may hold candidates: slot, thread
+    float slot[kLpSlots][THREADS];     // the largest of each part
+    uint16_t chosen[kLpSlots * THREADS < kLpChosen ? kLpSlots * THREADS : kLpChosen];  // parts that may hold candidates: slot, thread
     int nchosen, count;
 };
 
@@ -217,30 +227,31 @@ __device__ __forceinline__ uint64_t lp_warp_nth(uint64_t key, int j) {
 }
 
 // Thins `list` (keys all different) out to few more than its k largest, then writes these in order to `out`.  By the whole block.
-__device__ __forceinline__ void lp_select(LpSmem &sm, uint64_t *list, int count, int k, uint64_t *out) {
+template <int THREADS>
+__device__ __forceinline__ void lp_select(LpSmem<THREADS> &sm, uint64_t *list, int count, int k, uint64_t *out) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int turn = 0; turn < 3 && count > kLpThreads; ++turn) {
-        uint64_t mine[kLpCand / kLpThreads], top = 0;
+    for (int turn = 0; turn < 3 && count > THREADS; ++turn) {
+        uint64_t mine[kLpCand / THREADS], top = 0;
 #pragma unroll
-        for (int i = 0; i < kLpCand / kLpThreads; ++i) {
-            mine[i] = tid + i * kLpThreads < count ? list[tid + i * kLpThreads] : 0;
+        for (int i = 0; i < kLpCand / THREADS; ++i) {
+            mine[i] = tid + i * THREADS < count ? list[tid + i * THREADS] : 0;
             top = max(top, mine[i]);
         }
-        const uint64_t nth = lp_warp_nth(top, (k + kLpWarps - 1) / kLpWarps);
+        const uint64_t nth = lp_warp_nth(top, (k + (THREADS / 32) - 1) / (THREADS / 32));
         if (lane == 0) sm.warp_key[warp] = nth;
         __syncthreads();  // the list has been read
         if (tid == 0) sm.count = 0;
         uint64_t bound = sm.warp_key[0];
-        for (int w = 1; w < kLpWarps; ++w) bound = min(bound, sm.warp_key[w]);
+        for (int w = 1; w < (THREADS / 32); ++w) bound = min(bound, sm.warp_key[w]);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kLpCand / kLpThreads; ++i)
+        for (int i = 0; i < kLpCand / THREADS; ++i)
             if (mine[i] >= bound && mine[i] != 0) list[atomicAdd(&sm.count, 1)] = mine[i];
         __syncthreads();
         count = sm.count;
         __syncthreads();
     }
-    for (int i = tid; i < count; i += kLpThreads) {
+    for (int i = tid; i < count; i += THREADS) {
         const uint64_t key = list[i];
         int rank = 0;
 #pragma unroll 8
@@ -286,12 +297,13 @@ struct LpRow {
     }
 };
 
-template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const LpK p) {
+template <int TYPE, int THREADS>
+__global__ void __launch_bounds__(THREADS, lp_blocks(THREADS)) logprobs_kernel(const LpK p) {
+    constexpr int kWarps = THREADS / 32;
     constexpr int V = lp_vec<TYPE>();
     constexpr int kGroup = kLpGroup, kAhead = kLpAhead;  // chunks that are worked on together; such groups in registers, the rest under way
-    constexpr int kStride = kGroup * kLpThreads, kSpan = kLpThreads * V + V - 1;  // from a group's first element to its last
-    __shared__ LpSmem sm;
+    constexpr int kStride = kGroup * THREADS, kSpan = THREADS * V + V - 1;  // from a group's first element to its last
+    __shared__ LpSmem<THREADS> sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
     const int64_t rows_ahead = gridDim.x / p.cluster;
@@ -309,14 +321,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
     if (p.cluster > 1) cg::this_cluster().sync();  // every block of it has begun
     uint4 u[kAhead][kGroup];
     auto fetch = [&](uint4 (&w)[kGroup], const LpRow<TYPE> &r, int c, int end) {
-        if (c + (kGroup - 1) * kLpThreads < end) {
+        if (c + (kGroup - 1) * THREADS < end) {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) w[i] = r.chunk(c + i * kLpThreads);
+            for (int i = 0; i < kGroup; ++i) w[i] = r.chunk(c + i * THREADS);
         } else {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 w[i] = lp_nothing<TYPE>();
-                if (c + i * kLpThreads < end) w[i] = r.chunk(c + i * kLpThreads);
+                if (c + i * THREADS < end) w[i] = r.chunk(c + i * THREADS);
             }
         }
     };
@@ -435,10 +447,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
         int listed = 0;
         if (p.k) {
             if (top_at >= 0) mine = lp_key(top, (uint32_t)(row.at(top_at) + kSpan));
-            const int full = min(kLpWarps, (c1 - c0) / 32);  // warps whose threads all have elements
+            const int full = min(kWarps, (c1 - c0) / 32);  // warps whose threads all have elements
             if (full) {
-                const int j = (p.k + full - 1) / full + (full == kLpWarps ? (2 * p.k > full) + (p.k > full) : 0);
-                listed = j <= 32 ? full * j : 0;
+                const int j = min(32, (p.k + full - 1) / full + (full == kWarps ? (2 * p.k > full) + (p.k > full) : 0));
+                listed = full * j >= p.k ? full * j : 0;
                 uint64_t key = mine;
                 if (warp < full && listed)
                     for (int i = 0; i < j; ++i) {
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             }
         }
         __syncthreads();
-        a = lp_reduce(sm.warp_sums[lane & (kLpWarps - 1)], kLpWarps, s2);
+        a = lp_reduce(sm.warp_sums[lane & (kWarps - 1)], kWarps, s2);
         if (!(a.bad & 1) && ((a.bad & 2) || a.X * s2 < -0.5f * kLpFar) && a.X > -INFINITY) {
             // logits of such magnitudes, or rows of the type's lowest value alone: differences of logits are
             // scaled instead of scaled logits subtracted
@@ -467,14 +479,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                     b.S += e;
                     b.T += e * d;
                 }
-                c = c == edge ? c0 + tid : c + kLpThreads;
+                c = c == edge ? c0 + tid : c + THREADS;
                 if (c >= c1) break;
             }
             b = lp_reduce(b, 32, s2);
             __syncthreads();
             if (lane == 0) sm.warp_sums[warp] = b;
             __syncthreads();
-            a = lp_reduce(sm.warp_sums[lane & (kLpWarps - 1)], kLpWarps, s2);
+            a = lp_reduce(sm.warp_sums[lane & (kWarps - 1)], kWarps, s2);
         }
         a.bad &= 1;
         if (p.k) {
@@ -497,7 +509,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                 const float v = sm.slot[i][tid];
                 if (v > least || (v == least && (bound == 0 || row.at(c0 + tid + i * step) <= last))) {
                     const int to = atomicAdd(&sm.nchosen, 1);
-                    if (to < kLpChosen) sm.chosen[to] = (uint16_t)(i * kLpThreads + tid);
+                    if (to < kLpChosen) sm.chosen[to] = (uint16_t)(i * THREADS + tid);
                 }
             }
             __syncthreads();
@@ -514,9 +526,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             const int per = kAhead * kGroup << p.shift, nchosen = sm.nchosen;
             if (nchosen > kLpChosen && tid == 0) sm.count = kLpCand + 1;  // too many: see below
             if (nchosen <= kLpChosen)
-                for (int i = tid; i < nchosen * per; i += kLpThreads) {
-                    const int e = i / per, t = sm.chosen[e] % kLpThreads, slot = sm.chosen[e] / kLpThreads;
-                    const int ch = c0 + t + (slot * per + (i - e * per)) * kLpThreads;
+                for (int i = tid; i < nchosen * per; i += THREADS) {
+                    const int e = i / per, t = sm.chosen[e] % THREADS, slot = sm.chosen[e] / THREADS;
+                    const int ch = c0 + t + (slot * per + (i - e * per)) * THREADS;
                     if (ch >= c1) continue;
                     const uint4 w = row.chunk(ch);
                     if (lp_most<TYPE>(w) < least) continue;
@@ -531,13 +543,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
             }
         }
         __syncthreads();
-        LpSmem *first = &sm;
+        LpSmem<THREADS> *first = &sm;
         if (p.cluster > 1) first = cg::this_cluster().map_shared_rank(&sm, 0);
         if (tid == 0) first->sums[rank] = a;
         if (p.k) {
             const int found = sm.count;
             uint64_t *out = first->joined + rank * p.k;
-            for (int i = tid; i < p.k; i += kLpThreads)
+            for (int i = tid; i < p.k; i += THREADS)
                 if (i >= found) out[i] = 0;  // fewer elements than that
             if (found <= kLpCand) {
                 lp_select(sm, sm.cand, found, p.k, out);
@@ -554,14 +566,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                             const uint64_t key = row.key(ch, e, x[e]);
                             if (key < last) best = max(best, key);
                         }
-                        ch = ch == edge ? c0 + tid : ch + kLpThreads;
+                        ch = ch == edge ? c0 + tid : ch + THREADS;
                         if (ch >= c1) break;
                     }
                     best = lp_warp_nth(best, 1);
                     __syncthreads();
                     if (lane == 0) sm.warp_key[warp] = best;
                     __syncthreads();
-                    for (int w = 0; w < kLpWarps; ++w) best = max(best, sm.warp_key[w]);
+                    for (int w = 0; w < kWarps; ++w) best = max(best, sm.warp_key[w]);
                     if (tid == 0) out[r] = best;
                     last = best;
                 }
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                 if (p.entropy)
                     p.entropy[row_i] = r.bad ? nan : r.S > 0.0f ? fmaxf(ln - 0.6931471805599453f * (r.T / r.S), 0.0f) : 0.0f;
             }
-            for (int i = tid; i < p.m; i += kLpThreads) {
+            for (int i = tid; i < p.m; i += THREADS) {
                 const int t = p.tokens[row_i * p.m + i];
                 p.logp[row_i * p.m + i] = t < 0 || t >= p.vocab ? (r.bad ? nan : -INFINITY) : logp(lp_load<TYPE>(row.row, t));
             }
@@ -591,10 +603,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                 if (p.cluster > 1) {
                     best = sm.cand;
                     const int all = p.cluster * p.k;
-                    if (all > kLpThreads) {
+                    if (all > THREADS) {
                         lp_select(sm, sm.joined, all, p.k, best);
                     } else {
-                        for (int i = tid; i < all; i += kLpThreads) {
+                        for (int i = tid; i < all; i += THREADS) {
                             const uint64_t key = sm.joined[i];
                             int above = 0;
 #pragma unroll 8
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
                     }
                     __syncthreads();
                 }
-                for (int i = tid; i < p.k; i += kLpThreads) {
+                for (int i = tid; i < p.k; i += THREADS) {
                     const uint64_t key = best[i];
                     if (p.top_tok) p.top_tok[row_i * p.k + i] = r.bad ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
                     if (p.top_logp) p.top_logp[row_i * p.k + i] = logp(lp_key_value(key));
@@ -619,23 +631,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const L
     }
 }
 
-int launch_q_logprobs(int type, const void *x, int64_t stride, int64_t n, int vocab, float scale, const int32_t *tokens, int m,
-                      float *logp, float *entropy, float *lse, int k, int32_t *top_tok, float *top_logp, cudaStream_t stream) {
-    LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1, 0, 0};
+template <int THREADS>
+static int launch_lp(LpK p, int type, cudaStream_t stream) {
     // a cluster a row where there are few rows: as long as all blocks run at once, each at least 2048 elements
-    const int64_t slots = (int64_t)kLpBlocks * num_sms();
-    while (p.cluster < kLpMaxCluster && n * p.cluster * 2 <= slots && vocab / (2 * p.cluster) >= 2048) {
-        p.cluster *= 2;
-        ++p.log_cluster;
-    }
-    const int steps = (vocab / (type == QB_T_F32 ? 4 : 8) / p.cluster + 3) / (kLpAhead * kLpGroup * kLpThreads) + 1;  // at the most
+    const int64_t slots = (int64_t)lp_blocks(THREADS) * num_sms();
+    if (THREADS == kLpLong)
+        while (p.cluster < kLpMaxCluster && p.n * p.cluster * 2 <= slots && p.vocab / (2 * p.cluster) >= 2048) {
+            p.cluster *= 2;
+            ++p.log_cluster;
+        }
+    const int steps = (p.vocab / (type == QB_T_F32 ? 4 : 8) / p.cluster + 3) / (kLpAhead * kLpGroup * THREADS) + 1;  // at the most
     while (steps > kLpSlots << p.shift) ++p.shift;
-    const int64_t grid = p.cluster > 1 ? n * p.cluster : std::min<int64_t>(n, slots);
-    auto *f = type == QB_T_F32 ? logprobs_kernel<QB_T_F32> : type == QB_T_F16 ? logprobs_kernel<QB_T_F16> : logprobs_kernel<QB_T_BF16>;
+    const int64_t grid = p.cluster > 1 ? p.n * p.cluster : std::min<int64_t>(p.n, slots);
+    auto *f = type == QB_T_F32   ? logprobs_kernel<QB_T_F32, THREADS>
+              : type == QB_T_F16 ? logprobs_kernel<QB_T_F16, THREADS> : logprobs_kernel<QB_T_BF16, THREADS>;
     if (p.cluster > 8 && cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return QB_E_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -646,6 +659,13 @@ int launch_q_logprobs(int type, const void *x, int64_t stride, int64_t n, int vo
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, f, p) == cudaSuccess ? QB_OK : QB_E_CUDA;
+}
+
+int launch_q_logprobs(int type, const void *x, int64_t stride, int64_t n, int vocab, float scale, const int32_t *tokens, int m,
+                      float *logp, float *entropy, float *lse, int k, int32_t *top_tok, float *top_logp, cudaStream_t stream) {
+    const LpK p = {x, stride, n, vocab, scale, tokens, m, logp, entropy, lse, k, top_tok, top_logp, 1, 0, 0};
+    const bool many = n > (int64_t)lp_blocks(kLpLong) * num_sms();
+    return many && vocab <= kLpShortRow && k <= kLpShortK ? launch_lp<kLpShort>(p, type, stream) : launch_lp<kLpLong>(p, type, stream);
 }
 
 }  // namespace qb

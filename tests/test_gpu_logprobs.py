@@ -114,6 +114,23 @@ def test_sizes(name, n, vocab, k, m):
     check(logits(vocab + k, n, vocab, name), given(k, n, m, vocab) if m else None, k, scale=1.0 if n % 2 else 0.7)
 
 
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab,k,m", [(1, 1, 1), (3, 2, 0), (63, 32, 1), (515, 20, 1), (1024, 5, 0), (2100, 32, 2), (8192, 3, 1)])
+def test_many_short_rows(name, vocab, k, m):
+    """More rows than blocks run at once; the last ones masked, equal, rising, without a distribution."""
+    import torch
+    n = 640
+    x = logits(vocab, n, vocab, name)
+    x[-1] = -float("inf")
+    x[-2] = 0.5
+    x[-3] = torch.arange(vocab, device="cuda") * 0.01
+    x[-4, vocab // 2] = float("nan")
+    x[-5, vocab // 3] = float("inf")
+    x[-6] = torch.finfo(x.dtype).min
+    x[-7, 1:] = -float("inf")
+    check(x, given(k, n, m, vocab) if m else None, k, scale=0.9)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("lead", [0, 1, 3, 7])
 def test_strides_and_alignments(name, lead):
@@ -145,6 +162,23 @@ def test_orders(name, kind):
     check(x, given(2, n, 3, vocab), k)
     check(x, None, 64)
     check(x.expand(3, -1).repeat(110, 1)[:, :3000].contiguous(), None, k)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(1, 200003), (700, 30000), (640, 8000)])
+def test_the_largest_in_few_threads(name, n, vocab):
+    """Large logits in runs of 16 bytes that recur with every 256th (64th) run: a few threads of each block have them all."""
+    import torch
+    x = logits(11, n, vocab, name, 0.1)
+    per = 4 if name == "f32" else 8
+    run = torch.arange(vocab, device="cuda") // per
+    x += (5.0 * ((run % 256 < 70) | (run % 64 < 5))).to(x.dtype)
+    rows = [0, n // 2, n - 1]
+    got = {k: call(x, None, k) for k in (5, 32, 64)}
+    for k, g in got.items():
+        for i in rows:
+            row = x[i].double().cpu().numpy()
+            assert np.array_equal(g["top_tokens"][i], np.lexsort((np.arange(vocab), -row))[:k])
 
 
 def test_signed_zeros_are_equal():
