@@ -127,8 +127,8 @@ struct KeepReq {
     int64_t q0;
 };
 
-// Request i, looked at by a whole warp: what it says, and whether it is refused.
-__device__ __forceinline__ KeepReq keep_request(const KeepK &k, int i, int lane, bool report) {
+// Request i: its sequence's length, its drafts (status QB_E_ARG; len 0 where there is no such sequence).
+__device__ __forceinline__ KeepReq keep_request_ends(const KeepK &k, int i) {
     KeepReq r = {};
     r.row = k.rows ? k.rows[i] : i;
     int64_t q1 = k.q_start[i + 1];
@@ -137,12 +137,17 @@ __device__ __forceinline__ KeepReq keep_request(const KeepK &k, int i, int lane,
     r.T = (int)min(q1 - r.q0, (int64_t)INT32_MAX);
     r.cnt = k.nkeep[i];
     r.status = QB_E_ARG;
+    if (r.row >= 0 && r.row < k.p.nrows) r.len = min(max(k.p.lens[r.row], 0), k.p.maxp * k.p.page);
+    r.base = r.len - r.T;
+    return r;
+}
+// The same looked at by a whole warp: whether it is refused.
+__device__ __forceinline__ KeepReq keep_request(const KeepK &k, int i, int lane, bool report) {
+    KeepReq r = keep_request_ends(k, i);
     if (r.row < 0 || r.row >= k.p.nrows) {
         if (report && lane == 0) atomicOr(k.p.fault, kFaultIndex);
         return r;
     }
-    r.len = min(max(k.p.lens[r.row], 0), k.p.maxp * k.p.page);
-    r.base = r.len - r.T;
     if (r.base < 0 || r.cnt < 0 || r.cnt > r.T) return r;
     bool ok = true;
     for (int j = lane; j < r.cnt; j += 32) {  // ascending, each a draft's number
@@ -210,6 +215,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv4_keep_rows_kernel(const KeepK
             uint4 x[P];
 #pragma unroll
             for (int t = 0; t < P; ++t) {
+                if (t * 32 >= n * P) break;  // few drafts are kept, mostly
                 const int at = t * 32 + lane, m = at / P, piece = at - m * P;
                 if (m >= n || s_from[m] < 0) continue;
                 const int side = piece > NC, pc = piece - side * (NC + 1);
@@ -222,6 +228,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv4_keep_rows_kernel(const KeepK
             __syncwarp();
 #pragma unroll
             for (int t = 0; t < P; ++t) {
+                if (t * 32 >= n * P) break;  // few drafts are kept, mostly
                 const int at = t * 32 + lane, m = at / P, piece = at - m * P;
                 if (m >= n || s_from[m] < 0) continue;
                 const int side = piece > NC, pc = piece - side * (NC + 1);
@@ -243,6 +250,8 @@ __global__ void __launch_bounds__(kKeepThreads) kv4_keep_rows_kernel(const KeepK
 __global__ void __launch_bounds__(kPlanThreads) kv4_keep_state_kernel(const KeepK k, int32_t *status) {
     extern __shared__ uint32_t freed[];  // a bit a page
     __shared__ int red[33];
+    constexpr int kHeld = 256;
+    __shared__ int4 held[kHeld];  // of the first requests: row, length, new length, status
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int words = (k.p.npages + 31) / 32;
     for (int i = tid; i < words; i += kPlanThreads) freed[i] = 0;
@@ -250,16 +259,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_keep_state_kernel(const Keep
     pdl_wait();
     for (int i = warp; i < k.n; i += kPlanThreads / 32) {
         const KeepReq r = keep_request(k, i, lane, true);
-        if (lane == 0) status[i] = r.status;
+        if (lane == 0) {
+            status[i] = r.status;
+            if (i < kHeld) held[i] = make_int4(r.row, r.len, r.base + r.cnt, r.status);
+        }
     }
     const int nfree = min(max(k.p.nfree[0], 0), k.p.npages);
     __syncthreads();
     for (int i = warp; i < k.n; i += kPlanThreads / 32) {
-        if (status[i] != QB_OK) continue;
-        const int row = k.rows ? k.rows[i] : i;
-        const int64_t q0 = min(max((int64_t)k.q_start[i], (int64_t)0), k.ntok);
-        const int64_t q1 = min(max((int64_t)k.q_start[i + 1], q0), k.ntok);
-        const int len = min(max(k.p.lens[row], 0), k.p.maxp * k.p.page), now = len - (int)(q1 - q0) + k.nkeep[i];
+        int4 h;
+        if (i < kHeld) {
+            h = held[i];
+        } else {
+            const KeepReq r = keep_request_ends(k, i);
+            h = make_int4(r.row, r.len, r.base + r.cnt, status[i]);
+        }
+        if (h.w != QB_OK) continue;
+        const int row = h.x, len = h.y, now = h.z;
         int32_t *tab = k.p.tables + (int64_t)row * k.p.maxp;
         for (int j = kv_parts(now, k.p.page) + lane; j < kv_parts(len, k.p.page); j += 32) {
             const int pg = tab[j];
