@@ -99,7 +99,7 @@ int attend(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type type, const void
 }
 
 bool tree_bad(int64_t ntok, const int32_t *q_start, int nseq) {
-    return ntok < 0 || ntok > (int64_t(1) << 24) || nseq < 0 || nseq > (1 << 20) || off(q_start, 4) || (nseq == 0 && ntok != 0) ||
+    return ntok < 0 || ntok > (int64_t(1) << 20) || nseq < 0 || nseq > (1 << 20) || off(q_start, 4) || (nseq == 0 && ntok != 0) ||
            (!q_start && ntok != nseq);
 }
 

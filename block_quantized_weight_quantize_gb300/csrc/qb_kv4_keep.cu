@@ -30,44 +30,49 @@ __device__ __forceinline__ void tree_bounds(const TreeK &t, int s, int64_t &q0, 
     q1 = min(max(q1, q0), t.ntok);
 }
 
-constexpr int kTreeThreads = 128, kTreeHeld = 1024;
+constexpr int kTreeThreads = 128;
 
-// A block a sequence, a thread a token: it walks up through the parents, which have lower
-// numbers, so the mask's words are finished from the last to the first.
+// A block a sequence, 128 tokens at a time, a thread a token: it walks up through the parents, which have
+// lower numbers, to its first ancestor before these 128, and takes over what is written for that one; so a long
+// chain costs no more than its tokens.
 __global__ void __launch_bounds__(kTreeThreads) kv_tree_masks_kernel(const TreeK t, uint32_t *masks, int words, int32_t *depth) {
-    __shared__ int held[kTreeHeld];
+    __shared__ int held[kTreeThreads];
     pdl_launch_dependents();
     pdl_wait();
-    for (int s = blockIdx.x; s < t.nseq; s += gridDim.x) {
-        int64_t q0, q1;
-        tree_bounds(t, s, q0, q1);
-        const int T = (int)(q1 - q0);
-        __syncthreads();  // the sequence before has been read
-        auto parent_of = [&](int j, bool report) {
-            const int p = t.parents[q0 + j];
-            if (p >= -1 && p < j) return p;
-            if (report) atomicOr(t.fault, kFaultIndex);
-            return -1;
-        };
-        for (int j = threadIdx.x; j < T; j += kTreeThreads) {
-            const int p = parent_of(j, true);
-            if (j < kTreeHeld) held[j] = p;
+    int64_t q0, q1;
+    tree_bounds(t, blockIdx.x, q0, q1);
+    const int T = (int)(q1 - q0);
+    for (int c = 0; c < T; c += kTreeThreads) {
+        const int j = c + (int)threadIdx.x;
+        if (j < T) {
+            int p = t.parents[q0 + j];
+            if (p < -1 || p >= j) {
+                atomicOr(t.fault, kFaultIndex);
+                p = -1;
+            }
+            held[threadIdx.x] = p;
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < T; j += kTreeThreads) {
-            uint32_t *to = masks + (q0 + j) * words;
+        if (j < T) {
+            uint32_t own[kTreeThreads / 32] = {};  // ancestors among these 128
             int a = j, n = 0;
-            for (int w = words - 1; w >= 0; --w) {
-                uint32_t bits = 0;
-                while (a >= 32 * w) {
-                    if (a - 32 * w < 32) bits |= 1u << (a - 32 * w);
-                    a = a < kTreeHeld ? held[a] : parent_of(a, false);
-                    ++n;
-                }
+            for (; a >= c; a = held[a - c], ++n) {
+#pragma unroll
+                for (int w = 0; w < kTreeThreads / 32; ++w)
+                    if ((a - c) >> 5 == w) own[w] |= 1u << (a & 31);
+            }
+            const uint32_t *from = masks + (q0 + a) * words;
+            uint32_t *to = masks + (q0 + j) * words;
+            for (int w = 0; w < words; ++w) {
+                uint32_t bits = a >= 0 ? from[w] : 0u;
+#pragma unroll
+                for (int i = 0; i < kTreeThreads / 32; ++i)
+                    if (c / 32 + i == w) bits |= own[i];
                 to[w] = bits;
             }
-            if (depth) depth[q0 + j] = n - 1;
+            if (depth) depth[q0 + j] = n - 1 + (a >= 0 ? depth[q0 + a] + 1 : 0);
         }
+        __syncthreads();  // written, and `held` has been read
     }
 }
 

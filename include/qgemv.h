@@ -542,7 +542,7 @@ QB_API int kv4_attn_tree(const qb_kv4 *cache, const qb_kv_seqs *seqs, qb_type ty
  * parents[j] is the number, within its sequence, of the draft that token j
  * follows, or -1; a parent's number is lower than its child's (another is
  * reported by q_device_status and counts as -1).  Entries of tokens that no
- * sequence holds are not written.  ntok <= 2^24, nseq <= 2^20.  One launch each. */
+ * sequence holds are not written.  ntok, nseq <= 2^20.  One launch each. */
 
 /* masks [ntok][mask_words]: each draft's ancestors and itself, as kv4_attn_tree
  * takes them (1 <= mask_words <= 32; drafts past 32 * mask_words in no mask);

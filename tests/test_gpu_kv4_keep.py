@@ -64,6 +64,22 @@ def test_masks_and_depths(kind, news, words):
     assert bool((again == masks).all())
 
 
+def test_a_long_chain():
+    """200000 drafts one after the other, then the path along all of them: a matter of milliseconds."""
+    import torch
+    T = 200000
+    parents = torch.arange(-1, T - 1, dtype=torch.int32, device="cuda")
+    masks, depth, start = _zeros(T, 2), _zeros(T), _i32([0, T])
+    qb.kv_tree_masks(parents, masks, depth, q_start=start)
+    at = torch.arange(T, device="cuda")
+    assert torch.equal(depth, at.int())
+    want = torch.stack([((1 << (at + 1 - 32 * w).clamp(0, 32)) - 1) for w in (0, 1)], 1)
+    assert torch.equal(masks.long() & 0xFFFFFFFF, want)
+    keep, nkeep, nxt, ones = _zeros(T), _zeros(1), _zeros(1), torch.ones(T, dtype=torch.int32, device="cuda")
+    qb.kv_tree_accept(parents, ones, ones, keep, nkeep, nxt, q_start=start)
+    assert torch.equal(keep, at.int()) and nkeep.tolist() == [T] and nxt.tolist() == [1]
+
+
 def test_masks_of_single_tokens_and_bad_parents():
     masks, depth = _zeros(3, 2), _zeros(3)
     qb.kv_tree_masks(_i32([-1, -1, -1]), masks, depth)

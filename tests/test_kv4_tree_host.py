@@ -140,7 +140,7 @@ def test_tree_arguments():
     def accept(parents=A, tokens=A, targets=A, ntok=3, q_start=A, nseq=2, keep=A, nkeep=A, next_=A):
         return f.kv_tree_accept(parents, tokens, targets, ntok, q_start, nseq, keep, nkeep, next_, None)
 
-    for bad in (dict(parents=None), dict(parents=4097), dict(ntok=-1), dict(ntok=(1 << 24) + 1), dict(nseq=0), dict(nseq=-1), dict(q_start=None), dict(q_start=4098),
+    for bad in (dict(parents=None), dict(parents=4097), dict(ntok=-1), dict(ntok=(1 << 20) + 1), dict(nseq=0), dict(nseq=-1), dict(q_start=None), dict(q_start=4098),
                 dict(m=None), dict(m=4098), dict(words=0), dict(words=33), dict(depth=4097)):
         assert masks(**bad) == qb.QB_E_ARG, bad
     assert masks(ntok=0, parents=None, m=None) == qb.QB_OK and masks(ntok=0, nseq=0, parents=None, m=None) == qb.QB_OK
