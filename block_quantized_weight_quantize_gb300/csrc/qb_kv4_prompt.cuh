@@ -106,7 +106,7 @@ constexpr int kPromptCost = 1;  // what an item costs beside its tiles, in tiles
 // The same for calls with sinks or trees, whose items are mostly short (an item's own cost is some 10 us),
 // and where row tiles take half of the tiles each.  (1, 3, 5, 8 tiles: a prompt's chunk with sinks 129, 124, 124, 122
 // us, wide trees 110, 105, 100, 97, but 8 sequences of 2000 keys with 256 rows 49 with 3, 58 with 8.  Split,
-// 1, 6, 12, 16: a batch's trees 144, 115, 109, 110, 64 sequences of 300 keys - , 85, 71, 78.)
+// 6, 8, 12, 16: a batch's trees 115, 114, 109, 110, 64 sequences of 300 keys with 64 rows 85, 84, 71, 79.)
 constexpr int kPromptExtCost = 5, kPromptSplitCost = 12;
 template <bool EXT>
 __device__ __forceinline__ int prompt_cost(const PromptK &p) { return EXT ? p.cost : kPromptCost; }
