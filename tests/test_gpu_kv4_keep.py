@@ -263,6 +263,32 @@ def test_a_bad_page_in_a_table_is_reported():
     assert qb.q_device_status() == qb.QB_E_INDEX and qb.q_device_status() == qb.QB_OK
 
 
+def test_places_past_32_bits():
+    """Two layers of more than 2^31 bytes each, the drafts on the last pages."""
+    import torch
+    nkv, d, page, npages = 8, 128, 64, 30000
+    data = torch.empty((2, npages, nkv * qb.kv4_block_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    assert data.numel() > 2 ** 32
+    table = [[npages - 1, npages - 3, npages - 2, -1]]
+    pages = qb.KvPages(page, _i32([0]), _i32([-1] * npages), _i32([0] * (npages - 3) + [1] * 3), _i32([150]), _i32(table))
+    slots = _i32([table[0][t // page] * page + t % page for t in range(150)])
+    rows = torch.randn((2, 2, 150, nkv, d), generator=torch.Generator().manual_seed(1)).cuda()
+    held, got = torch.empty_like(rows), torch.empty_like(rows)
+    caches = [qb.Kv4(data[layer], page, nkv, d) for layer in (0, 1)]
+    for cache, x, y in zip(caches, rows, held):
+        qb.kv4_append(cache, x[0], x[1], slots)
+        qb.kv4_read(cache, slots, y[0], y[1])
+    kept, status = [1, 20, 59], _zeros(1)
+    qb.kv4_keep(pages, data, nkv, d, None, _i32([0, 60]), _i32(kept + [-1] * 57), _i32([3]), status)
+    for cache, y in zip(caches, got):
+        qb.kv4_read(cache, slots, y[0], y[1])
+    want = held.clone()
+    want[:, :, 90:93] = held[:, :, [90 + k for k in kept]]
+    assert status.tolist() == [0] and torch.equal(got, want)
+    assert pages.lens.tolist() == [93] and pages.tables.tolist() == [[npages - 1, npages - 3, -1, -1]]
+    assert int(pages.nfree) == 1 and int(pages.free[0]) == npages - 2
+
+
 def test_nothing_to_do_and_refusals():
     import torch
     pool = Pool(8, [20], 16, 2, 64)

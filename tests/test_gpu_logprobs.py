@@ -142,6 +142,15 @@ def test_strides_and_alignments(name, lead):
     check(x, given(1, 6, 2, 3001), 9)
 
 
+def test_rows_further_apart_than_32_bits_count():
+    import torch
+    n, vocab, stride = 3, 5003, 2 ** 31 + 3
+    wide = torch.empty(2 * stride + vocab, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((n, vocab), (stride, 1))
+    x.copy_(logits(12, n, vocab, "bf16"))
+    check(x, given(1, n, 2, vocab), 9)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["equal", "rising", "falling", "masked", "few", "lowest", "halves", "saw"])
 def test_orders(name, kind):
