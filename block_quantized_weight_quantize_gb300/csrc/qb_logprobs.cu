@@ -13,7 +13,9 @@
 // Alternatives.  A thread remembers its largest logit, and the largest of each of up to kLpSlots parts of
 // its elements.  The k-th of the warps' largest threads (each as if it were the last element of its
 // place) is a lower bound of the k-th largest element; parts whose largest reaches it are read once
-// more (from L2), their elements that reach it ordered by counting.  (Reading all elements of such
+// more (from L2), their elements that reach it ordered by counting.  Where too many reach it, as where most tokens
+// are forbidden, those above its value are taken and the first that equal it (120 rows of 41549 in bf16, of
+// which 42 are allowed, k = 20: 14 us; one largest after the other 150).  (Reading all elements of such
 // threads instead: 3000 rows of 100000 in bf16, k = 20 158 us, 147 with the parts; k = 1 129, 137.)
 //
 // Work: a row is read by a cluster of 1 to 16 blocks, which join their sums and candidates in
@@ -47,13 +49,14 @@ constexpr int kLpChosen = 1024;  // of these, as many are looked at again
 // Blocks of 256 threads, or of 64 for many short rows, whose end takes longer than their elements.  4000
 // rows in f32, us with 256 threads, with 64:
 //     elements a row     300         1000        4000        8000        8000 in bf16
-//     k = 0              19.5 11.7   21.3 12.6   24.4 22.1   31.3 34.6   27.4 23.4
-//     k = 5              39.1 22.1   41.4 23.0   46.1 32.9   54.0 46.8   51.0 35.6
-//     k = 20             44.4 28.0   48.2 28.9   51.6 40.5   59.7 55.2   56.5 44.6
+//     k = 0              19.5 10.6   21.3 11.8   24.4 20.6   31.3 32.3   27.4 22.9
+//     k = 5              39.1 21.2   41.4 22.6   46.1 32.2   54.0 45.0   51.0 35.8
+//     k = 20             44.4 26.8   48.2 28.4   51.6 40.3   59.7 54.2   56.5 45.5
 //     k = 64             81.8 80.2   63.9 85.4   65.7 126    74.1 159    73.3 152
+// (12 blocks of 64 a multiprocessor; with 16 a thread's 64 registers do not hold what it has: 16.8 us for 11.8.)
 // Where all rows run at once in 256 threads, these are as fast or faster (100 of 1000, k = 20: 6.3, 7.0).
 constexpr int kLpShort = 64, kLpLong = 256, kLpShortRow = 8192, kLpShortK = 32;
-constexpr int lp_blocks(int threads) { return threads == kLpLong ? 4 : 16; }  // a multiprocessor
+constexpr int lp_blocks(int threads) { return threads == kLpLong ? 4 : 12; }  // a multiprocessor
 constexpr float kLpLazy = 32.0f;     // 2^32 times 2^24 elements stay far below f32's top
 constexpr float kLpFar = 0x1p22f;    // scaled logits up to here are whole numbers' neighbours
 constexpr float kLpFloor = -0x1p100f;  // what -infinity counts as: its probability is 0, and 0 times it 0
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, lp_blocks(THREADS)) logprobs_kernel(c
         if (lane == 0) sm.warp_sums[warp] = a;
         // the thread's largest as if it were its group's last element: one of its elements reaches that
         uint64_t mine = 0;
-        int listed = 0;
+        int listed = 0, found = 0;
         if (p.k) {
             if (top_at >= 0) mine = lp_key(top, (uint32_t)(row.at(top_at) + kSpan));
             const int full = min(kWarps, (c1 - c0) / 32);  // warps whose threads all have elements
@@ -502,12 +505,14 @@ __global__ void __launch_bounds__(THREADS, lp_blocks(THREADS)) logprobs_kernel(c
             const uint64_t bound = sm.bound;
             const float least = bound ? lp_key_value(bound) : -INFINITY;
             // ---- the candidates: elements of the parts whose largest reaches the bound; of equal ones
-            // those that begin at its place or before it
+            // those that begin at its place or before it.  Where the bound is -infinity (most tokens are forbidden), or
+            // too many elements reach it, those above its value, and the first ones that equal it
+            bool above_only = least == -INFINITY;
             const int step = kAhead * kStride << p.shift, parts = (c1 - c0 - tid + step - 1) / step;
             const int last = (int)(0xFFFFFFFFu - (uint32_t)bound);
             for (int i = 0; i < parts; ++i) {
                 const float v = sm.slot[i][tid];
-                if (v > least || (v == least && (bound == 0 || row.at(c0 + tid + i * step) <= last))) {
+                if (v > least || (!above_only && v == least && row.at(c0 + tid + i * step) <= last)) {
                     const int to = atomicAdd(&sm.nchosen, 1);
                     if (to < kLpChosen) sm.chosen[to] = (uint16_t)(i * THREADS + tid);
                 }
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, lp_blocks(THREADS)) logprobs_kernel(c
             auto offer = [&](const float (&x)[V], int ch) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if (!(x[e] >= least)) continue;
+                    if (!(x[e] > least) && (above_only || x[e] != least)) continue;
                     const uint64_t key = row.key(ch, e, x[e]);
                     if (key < bound || key == 0) continue;
                     const int to = atomicAdd(&sm.count, 1);
@@ -541,13 +546,65 @@ __global__ void __launch_bounds__(THREADS, lp_blocks(THREADS)) logprobs_kernel(c
                 row.edge(edge, x);
                 offer(x, edge);
             }
+            __syncthreads();
+            found = sm.count;
+            if (found > kLpCand) {
+                above_only = true;
+                __syncthreads();
+                if (tid == 0) sm.count = 0;
+                __syncthreads();
+                for (int ch = edge >= 0 ? edge : c0 + tid; edge >= 0 || ch < c1;) {
+                    float x[V];
+                    row.load(ch, x);
+                    offer(x, ch);
+                    ch = ch == edge ? c0 + tid : ch + THREADS;
+                    if (ch >= c1) break;
+                }
+                __syncthreads();
+                found = sm.count;
+            }
+            // the first elements that equal the bound, in their order, THREADS chunks at a time
+            const int above = found, turns = max(0, (c1 - c0 + THREADS - 1) / THREADS);
+            for (int i = -1; above_only && i <= turns && found < p.k; ++i) {  // the edge before them, the others, the one after
+                int ch = -1, n = 0;
+                if (i < 0 || i == turns) {
+                    if (tid == (i < 0 ? 0 : 1)) ch = edge;
+                } else if (c0 + i * THREADS + tid < c1) {
+                    ch = c0 + i * THREADS + tid;
+                }
+                uint32_t equal = 0;
+                if (ch >= 0) {
+                    float x[V];
+                    row.load(ch, x);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (x[e] == least && row.key(ch, e, x[e]) != 0) equal |= 1u << e;
+                    n = __popc(equal);
+                }
+                int at = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                    if (lane >= o) at += y;
+                }
+                if (lane == 31) sm.warp_key[warp] = (uint64_t)at;
+                __syncthreads();
+                int all = 0;
+                at += found - n;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) at += (int)sm.warp_key[w];
+                    all += (int)sm.warp_key[w];
+                }
+                for (; equal && at < p.k; equal &= equal - 1) sm.cand[at++] = lp_key(least, (uint32_t)(row.at(ch) + __ffs(equal) - 1));
+                found += all;
+                __syncthreads();
+            }
+            if (above < p.k) found = min(found, p.k);
         }
-        __syncthreads();
         LpSmem<THREADS> *first = &sm;
         if (p.cluster > 1) first = cg::this_cluster().map_shared_rank(&sm, 0);
         if (tid == 0) first->sums[rank] = a;
         if (p.k) {
-            const int found = sm.count;
             uint64_t *out = first->joined + rank * p.k;
             for (int i = tid; i < p.k; i += THREADS)
                 if (i >= found) out[i] = 0;  // fewer elements than that

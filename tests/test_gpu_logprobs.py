@@ -190,6 +190,30 @@ def test_the_largest_in_few_threads(name, n, vocab):
             assert np.array_equal(g["top_tokens"][i], np.lexsort((np.arange(vocab), -row))[:k])
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(2, 41549), (50, 4289), (700, 4289), (3, 128256), (650, 70000)])
+@pytest.mark.parametrize("kind", ["masked", "levels", "late"])
+def test_many_equal_logits(name, n, vocab, kind):
+    """Rows of which almost all is forbidden, rows of a few different values, and equal ones that come late or between larger ones:
+    places by value, then in order, whichever block and pass they come from."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(vocab + n)
+    x = logits(13, n, vocab, name)
+    u = torch.rand((n, vocab), device="cuda", generator=g)
+    if kind == "masked":
+        x[u < 0.999] = -float("inf")
+    elif kind == "levels":
+        x = (u * 3).floor().to(_type(name))
+    else:
+        x = torch.where(u < 0.0003, 3.0, torch.where(torch.arange(vocab, device="cuda") > vocab * 0.7, 1.0, 0.0)).to(_type(name))
+    rows = [0, n // 2, n - 1]
+    for k in (1, 20, 32, 64):
+        got = call(x, None, k)
+        for i in rows:
+            row = x[i].double().cpu().numpy()
+            assert np.array_equal(got["top_tokens"][i], np.lexsort((np.arange(vocab), -row))[:k]), (k, i)
+
+
 def test_signed_zeros_are_equal():
     import torch
     x = torch.full((1, 100), -1.0, device="cuda")
